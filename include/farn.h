@@ -50,6 +50,9 @@ extern "C" {
 /* Largest number of rank partials one call accepts. */
 #define FARN_MAX_W 32
 
+/* Largest number of experts of the router and of the grouped product. */
+#define FARN_MAX_EXPERTS 1024
+
 typedef enum {
     FARN_OK = 0,
     FARN_ERR_INVALID_ARG = -1,  /* null pointer, W/T/H/eps out of range     */
@@ -311,6 +314,104 @@ int farn_plan_moe_combine(const farn_ctx *ctx, int K, int64_t T, int64_t H,
                           const void *weight, const void *reduced_out,
                           const void *residual_out, const void *norm_out,
                           int *variant, int *threads);
+
+/* farn_moe_route - the MoE router: which experts every token goes to, with
+ * which gates, and where its rows lie when the (token, expert) pairs are
+ * sorted by expert.  Its outputs are the inputs of farn_grouped_matmul
+ * (rows, offsets) and farn_moe_combine (index, gates).
+ *     experts[t,k]  the expert of the k-th largest of logits[t,:]; of equal
+ *                   logits (-0 and +0 are equal) the lowest expert first.
+ *                   A logit of -inf (a masked expert) or NaN is never
+ *                   chosen: where fewer than K are left, -1.
+ *     gates[t,k]    p(experts[t,k]) / sum of p, p(e) = exp(logits[t,e] - max)
+ *                   in fp32 (1 for an infinite maximum), the sum over the
+ *                   chosen experts (renormalize != 0) or over all E; 0 where
+ *                   the expert is -1.
+ *     offsets[e]    the first slot of expert e; offsets[E] the number of
+ *                   slots in use (pairs whose expert is not -1)
+ *     index[t,k]    the pair's slot, or -1: slots are sorted by expert, then
+ *                   by token
+ *     rows[s]       the token of slot s; -1 for slots from offsets[E] on
+ * The whole numbers are exact functions of the logits.
+ *   logits  bf16 or fp32 [T, E] (logits_dtype a farn_dtype)
+ *   E       1 .. FARN_MAX_EXPERTS;  K  1 .. min(E, FARN_MAX_W);  T * K < 2^31
+ *   experts, index  int32 [T, K];  gates  fp32 [T, K];  rows  int32 [T * K];
+ *   offsets int32 [E + 1], all 4-byte aligned
+ * T == 0 writes the offsets (all 0) only; the other pointers may be NULL.
+ * No memory beyond the outputs is used.  Returns FARN_ERR_INVALID_ARG,
+ * FARN_ERR_ALIAS (an output over another tensor) or FARN_ERR_CUDA. */
+int farn_moe_route(const farn_ctx *ctx, const void *logits, int logits_dtype,
+                   int64_t T, int E, int K, int renormalize,
+                   int32_t *experts, float *gates, int32_t *index,
+                   int32_t *rows, int32_t *offsets, cudaStream_t stream);
+
+/* farn_grouped_matmul - the experts' products:
+ *     out[s,n] = bf16( sum_h f(x[r,h]) * f(weights[e,n,h]) )
+ * for every slot s of expert e, offsets[e] <= s < offsets[e+1], with r =
+ * rows[s], or r = s where rows is NULL.  Products and sums in fp32 (the
+ * order of the sum is the kernel's own and the same in every call with the
+ * same arguments), one rounding to bf16.
+ *   x        bf16 [n_rows, H]; rows NULL needs n_rows == n_slots
+ *   rows     int32 [n_slots] or NULL (4-byte aligned).  A slot whose row is
+ *            outside [0, n_rows) gets zeros; nothing is read for it.
+ *   weights  bf16 [E, N, H], E 1 .. FARN_MAX_EXPERTS
+ *   offsets  int32 [E + 1] on the device, ascending, within 0 .. n_slots.
+ *            An expert may have no slots.  (Other values cannot lead outside
+ *            the tensors, but the outputs are then unspecified.)
+ *   out      bf16 [n_slots, N]; slots below offsets[0] and from offsets[E]
+ *            on are left as they were
+ *   n_slots, n_rows, N, H < 2^31; n_slots == 0 returns FARN_OK and launches
+ *            nothing
+ * The fast kernels need x and weights 16-byte aligned and H a multiple of 8;
+ * other shapes are served by a slower kernel.  Returns FARN_ERR_INVALID_ARG,
+ * FARN_ERR_ALIAS (out over an input) or FARN_ERR_CUDA. */
+int farn_grouped_matmul(const farn_ctx *ctx, const void *x, int64_t n_rows,
+                        const int32_t *rows, int64_t n_slots,
+                        const void *weights, int E, const int32_t *offsets,
+                        int64_t N, int64_t H, void *out, cudaStream_t stream);
+
+/* farn_nvfp4_quantize - NVFP4 codes and block scales of a bf16 tensor
+ * x [T,H], for tensors that no norm produces (weights, expert activations):
+ * the format and arithmetic of farn_forward_nvfp4's copy of norm_out, with x
+ * in norm_out's place.
+ *   codes        uint8 [T, H/2];  block_scale  uint8 [T, H/16]
+ *   tensor_scale finite, > 0;  H a multiple of 16;  T == 0 launches nothing
+ * x 16-byte and codes 8-byte aligned take the fast kernel.  Returns
+ * FARN_ERR_INVALID_ARG, FARN_ERR_ALIAS, FARN_ERR_UNSUPPORTED (more than
+ * 2^41 elements) or FARN_ERR_CUDA. */
+int farn_nvfp4_quantize(const farn_ctx *ctx, const void *x, int64_t T, int64_t H,
+                        float tensor_scale, void *codes, void *block_scale,
+                        cudaStream_t stream);
+
+/* farn_nvfp4_dequantize - the values that NVFP4 codes stand for, in bf16:
+ *     out[t,h] = bf16( value(code) * (value(block_scale) / tensor_scale) )
+ * with the quotient and the product each rounded to fp32.  Arguments and
+ * errors as for farn_nvfp4_quantize; out bf16 [T,H], 16-byte aligned for the
+ * fast kernel. */
+int farn_nvfp4_dequantize(const farn_ctx *ctx, const void *codes,
+                          const void *block_scale, int64_t T, int64_t H,
+                          float tensor_scale, void *out, cudaStream_t stream);
+
+/* farn_nvfp4_matmul - the product of two NVFP4 tensors (farn_forward_nvfp4's
+ * or farn_nvfp4_quantize's outputs), for example activations by weights:
+ *     out[t,n] = bf16( alpha * sum_h va[t,h] * vb[n,h] )
+ *     v = value(code) * value(block_scale),  alpha = 1 / (a_tensor_scale *
+ *     b_tensor_scale), rounded once to fp32
+ * accumulated in fp32 (the order is the kernel's own and the same in every
+ * call with the same arguments), one rounding to bf16.  A block scale of NaN
+ * makes its products NaN; the sign bit of a block scale has to be 0.
+ *   a_codes uint8 [T, H/2], a_scale uint8 [T, H/16]; b_codes, b_scale the
+ *   same with N rows; out bf16 [T, N]
+ *   H a multiple of 16; T, N, H < 2^31; T == 0 launches nothing
+ * The fast kernels need the codes 16-byte aligned and H a multiple of 32;
+ * other shapes are served by a slower kernel.  Returns FARN_ERR_INVALID_ARG
+ * (also for an alpha that fp32 cannot hold), FARN_ERR_ALIAS or
+ * FARN_ERR_CUDA. */
+int farn_nvfp4_matmul(const farn_ctx *ctx, const void *a_codes,
+                      const void *a_scale, float a_tensor_scale,
+                      const void *b_codes, const void *b_scale,
+                      float b_tensor_scale, int64_t T, int64_t N, int64_t H,
+                      void *out, cudaStream_t stream);
 
 /* Flags of farn_plan_typed. */
 #define FARN_PLAN_FP8_OUT 1   /* the call also writes the FP8 norm output */

@@ -26,11 +26,16 @@ __all__ = [
     "farn_plan", "farn_status_string", "farn_device_status", "farn_forward_noalloc",
     "farn_forward_typed", "farn_plan_typed", "farn_forward_quant", "forward_quant",
     "farn_moe_combine", "moe_combine",
+    "FARN_MAX_EXPERTS", "farn_moe_route", "moe_route",
+    "farn_grouped_matmul", "grouped_matmul",
+    "farn_nvfp4_quantize", "nvfp4_quantize", "farn_nvfp4_dequantize", "nvfp4_dequantize",
+    "farn_nvfp4_matmul", "nvfp4_matmul",
     "FARN_BF16", "FARN_F32",
     "forward", "VARIANTS",
 ]
 
 FARN_MAX_W = 32
+FARN_MAX_EXPERTS = 1024
 FARN_OK = 0
 FARN_ERR_INVALID_ARG = -1
 FARN_ERR_UNSUPPORTED = -2
@@ -77,6 +82,17 @@ def _load():
         lib.farn_moe_combine.argtypes = [vp, cvp, i64, cvp, cvp, i32, cvp, cvp, f32, i64, i64,
                                          vp, vp, vp, vp]
         lib.farn_moe_combine.restype = i32
+        lib.farn_moe_route.argtypes = [vp, cvp, i32, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+        lib.farn_moe_route.restype = i32
+        lib.farn_grouped_matmul.argtypes = [vp, cvp, i64, cvp, i64, cvp, i32, cvp, i64, i64, vp,
+                                            vp]
+        lib.farn_grouped_matmul.restype = i32
+        lib.farn_nvfp4_quantize.argtypes = [vp, cvp, i64, i64, f32, vp, vp, vp]
+        lib.farn_nvfp4_quantize.restype = i32
+        lib.farn_nvfp4_dequantize.argtypes = [vp, cvp, cvp, i64, i64, f32, vp, vp]
+        lib.farn_nvfp4_dequantize.restype = i32
+        lib.farn_nvfp4_matmul.argtypes = [vp, cvp, cvp, f32, cvp, cvp, f32, i64, i64, i64, vp, vp]
+        lib.farn_nvfp4_matmul.restype = i32
         lib.farn_check_args.argtypes = [pvp, i32, cvp, cvp, f32, i64, i64,
                                         cvp, cvp, cvp]
         lib.farn_check_args.restype = i32
@@ -188,6 +204,50 @@ def farn_moe_combine(ctx, expert_out, n_slots, index, gates, K, residual, weight
         ctypes.c_void_p(ctx) if ctx else None, v(expert_out), int(n_slots), v(index), v(gates),
         int(K), v(residual), v(weight), float(eps), int(T), int(H), v(reduced_out),
         v(residual_out), v(norm_out), ctypes.c_void_p(int(stream)))
+
+
+def _addr(a):
+    return ctypes.c_void_p(int(a)) if a else None
+
+
+def farn_moe_route(ctx, logits, logits_dtype, T, E, K, renormalize, experts, gates, index, rows,
+                   offsets, stream=0) -> int:
+    """C ``farn_moe_route`` on raw device addresses (ints)."""
+    return _load().farn_moe_route(
+        _addr(ctx), _addr(logits), int(logits_dtype), int(T), int(E), int(K), int(renormalize),
+        _addr(experts), _addr(gates), _addr(index), _addr(rows), _addr(offsets), _addr(stream))
+
+
+def farn_grouped_matmul(ctx, x, n_rows, rows, n_slots, weights, E, offsets, N, H, out,
+                        stream=0) -> int:
+    """C ``farn_grouped_matmul`` on raw device addresses (ints); rows 0 for
+    slot s reading row s."""
+    return _load().farn_grouped_matmul(
+        _addr(ctx), _addr(x), int(n_rows), _addr(rows), int(n_slots), _addr(weights), int(E),
+        _addr(offsets), int(N), int(H), _addr(out), _addr(stream))
+
+
+def farn_nvfp4_quantize(ctx, x, T, H, tensor_scale, codes, block_scale, stream=0) -> int:
+    """C ``farn_nvfp4_quantize`` on raw device addresses (ints)."""
+    return _load().farn_nvfp4_quantize(
+        _addr(ctx), _addr(x), int(T), int(H), float(tensor_scale), _addr(codes),
+        _addr(block_scale), _addr(stream))
+
+
+def farn_nvfp4_dequantize(ctx, codes, block_scale, T, H, tensor_scale, out, stream=0) -> int:
+    """C ``farn_nvfp4_dequantize`` on raw device addresses (ints)."""
+    return _load().farn_nvfp4_dequantize(
+        _addr(ctx), _addr(codes), _addr(block_scale), int(T), int(H), float(tensor_scale),
+        _addr(out), _addr(stream))
+
+
+def farn_nvfp4_matmul(ctx, a_codes, a_scale, a_tensor_scale, b_codes, b_scale, b_tensor_scale,
+                      T, N, H, out, stream=0) -> int:
+    """C ``farn_nvfp4_matmul`` on raw device addresses (ints)."""
+    return _load().farn_nvfp4_matmul(
+        _addr(ctx), _addr(a_codes), _addr(a_scale), float(a_tensor_scale), _addr(b_codes),
+        _addr(b_scale), float(b_tensor_scale), int(T), int(N), int(H), _addr(out),
+        _addr(stream))
 
 
 def farn_forward_noalloc(device, partials, W, residual, weight, eps, T, H,
@@ -516,3 +576,170 @@ def moe_combine(expert_out, index, gates, residual, weight, eps: float, out=None
     bf16 [H].  Returns (reduced, residual_out, norm_out)."""
     return prepare_moe_combine(expert_out, index, gates, residual, weight, eps, out, ctx,
                                stream)()
+
+
+def prepare_moe_route(logits, top_k: int, renormalize: bool = True, out=None, ctx=None,
+                      stream=None):
+    """``moe_route`` checked and marshalled once."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    dev, K = logits.device, int(top_k)
+    _check_tensor(logits, "logits", (T, E), dev, (torch.bfloat16, torch.float32))
+    if not 1 <= E <= FARN_MAX_EXPERTS:
+        raise ValueError(f"the number of experts must be 1..{FARN_MAX_EXPERTS}, got {E}")
+    if not 1 <= K <= min(E, FARN_MAX_W):
+        raise ValueError(f"top_k must be 1..{min(E, FARN_MAX_W)}, got {K}")
+    i32, f32 = (torch.int32,), (torch.float32,)
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=dt[0], device=dev) for shape, dt in
+                    (((T, K), i32), ((T, K), f32), ((T, K), i32), ((T * K,), i32),
+                     ((E + 1,), i32)))
+    else:
+        for name, t, shape, dt in zip(("experts", "gates", "index", "rows", "offsets"), out,
+                                      ((T, K), (T, K), (T, K), (T * K,), (E + 1,)),
+                                      (i32, f32, i32, i32, i32)):
+            _check_tensor(t, name, shape, dev, dt)
+    c, s = _ctx_stream(ctx, stream, dev)
+    args = (ctypes.c_void_p(c.handle), _vp(logits),
+            FARN_F32 if logits.dtype == torch.float32 else FARN_BF16, T, E, K,
+            1 if renormalize else 0) + tuple(_vp(t) for t in out) + (s,)
+    return PreparedCall(_load().farn_moe_route, args, "farn_moe_route", tuple(out), (logits, c))
+
+
+def moe_route(logits, top_k: int, renormalize: bool = True, out=None, ctx=None, stream=None):
+    """The MoE router on a bf16 or fp32 tensor of logits [T,E].  Returns
+    (experts int32 [T,K], gates fp32 [T,K], index int32 [T,K], rows int32
+    [T*K], offsets int32 [E+1]): rows and offsets are ``grouped_matmul``'s,
+    index and gates ``moe_combine``'s.  An expert masked with -inf is never
+    chosen; a pair without an expert has expert -1, gate 0 and index -1."""
+    return prepare_moe_route(logits, top_k, renormalize, out, ctx, stream)()
+
+
+def prepare_grouped_matmul(x, weights, offsets, rows=None, out=None, ctx=None, stream=None):
+    """``grouped_matmul`` checked and marshalled once."""
+    import torch
+    if x.dim() != 2 or weights.dim() != 3:
+        raise ValueError("x must be [rows, H] and weights [E, N, H]")
+    n_rows, H = x.shape
+    E, N, _ = weights.shape
+    dev = x.device
+    _check_tensor(x, "x", (n_rows, H), dev)
+    _check_tensor(weights, "weights", (E, N, H), dev)
+    _check_tensor(offsets, "offsets", (E + 1,), dev, (torch.int32,))
+    S = n_rows
+    if rows is not None:
+        S = rows.shape[0] if rows.dim() == 1 else -1
+        _check_tensor(rows, "rows", (S,), dev, (torch.int32,))
+    if out is None:
+        out = torch.empty((S, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_tensor(out, "out", (S, N), dev)
+    c, s = _ctx_stream(ctx, stream, dev)
+    args = (ctypes.c_void_p(c.handle), _vp(x), n_rows, _vp(rows), S, _vp(weights), E,
+            _vp(offsets), N, H, _vp(out), s)
+    return PreparedCall(_load().farn_grouped_matmul, args, "farn_grouped_matmul", out,
+                        (x, weights, offsets, rows, c))
+
+
+def grouped_matmul(x, weights, offsets, rows=None, out=None, ctx=None, stream=None):
+    """The experts' products on torch CUDA tensors: x bf16 [n,H], weights bf16
+    [E,N,H], offsets int32 [E+1] (expert e has the slots offsets[e] ..
+    offsets[e+1]-1), rows int32 [S] (the row of x that a slot reads; None:
+    slot s reads row s).  Returns out bf16 [S,N], ``moe_combine``'s
+    expert_out; slots that no expert has are left as they were."""
+    return prepare_grouped_matmul(x, weights, offsets, rows, out, ctx, stream)()
+
+
+def _nvfp4_shape(codes, scales, name):
+    import torch
+    if codes.dim() != 2:
+        raise ValueError(f"{name} must be [rows, H/2]")
+    T, H = codes.shape[0], codes.shape[1] * 2
+    if H % 16:
+        raise ValueError(f"NVFP4 needs H % 16 == 0, got H = {H}")
+    _check_tensor(codes, name, (T, H // 2), codes.device, (torch.uint8,))
+    _check_tensor(scales, name + " scales", (T, H // 16), codes.device, (torch.uint8,))
+    return T, H
+
+
+def prepare_nvfp4_quantize(x, tensor_scale: float, out=None, ctx=None, stream=None):
+    """``nvfp4_quantize`` checked and marshalled once."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    dev = x.device
+    _check_tensor(x, "x", (T, H), dev)
+    if H % 16:
+        raise ValueError(f"NVFP4 needs H % 16 == 0, got H = {H}")
+    if out is None:
+        out = (torch.empty((T, H // 2), dtype=torch.uint8, device=dev),
+               torch.empty((T, H // 16), dtype=torch.uint8, device=dev))
+    else:
+        _check_tensor(out[0], "codes", (T, H // 2), dev, (torch.uint8,))
+        _check_tensor(out[1], "scales", (T, H // 16), dev, (torch.uint8,))
+    c, s = _ctx_stream(ctx, stream, dev)
+    args = (ctypes.c_void_p(c.handle), _vp(x), T, H, tensor_scale, _vp(out[0]), _vp(out[1]), s)
+    return PreparedCall(_load().farn_nvfp4_quantize, args, "farn_nvfp4_quantize", tuple(out),
+                        (x, c))
+
+
+def nvfp4_quantize(x, tensor_scale: float, out=None, ctx=None, stream=None):
+    """NVFP4 codes of a bf16 tensor [T,H], in ``forward_nvfp4``'s format.
+    Returns (codes uint8 [T,H/2], block_scale uint8 [T,H/16]); H must be a
+    multiple of 16."""
+    return prepare_nvfp4_quantize(x, tensor_scale, out, ctx, stream)()
+
+
+def prepare_nvfp4_dequantize(codes, block_scale, tensor_scale: float, out=None, ctx=None,
+                             stream=None):
+    """``nvfp4_dequantize`` checked and marshalled once."""
+    import torch
+    T, H = _nvfp4_shape(codes, block_scale, "codes")
+    dev = codes.device
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_tensor(out, "out", (T, H), dev)
+    c, s = _ctx_stream(ctx, stream, dev)
+    args = (ctypes.c_void_p(c.handle), _vp(codes), _vp(block_scale), T, H, tensor_scale,
+            _vp(out), s)
+    return PreparedCall(_load().farn_nvfp4_dequantize, args, "farn_nvfp4_dequantize", out,
+                        (codes, block_scale, c))
+
+
+def nvfp4_dequantize(codes, block_scale, tensor_scale: float, out=None, ctx=None, stream=None):
+    """The values of NVFP4 codes and block scales, as a bf16 tensor [T,H]."""
+    return prepare_nvfp4_dequantize(codes, block_scale, tensor_scale, out, ctx, stream)()
+
+
+def prepare_nvfp4_matmul(a_codes, a_scale, a_tensor_scale: float, b_codes, b_scale,
+                         b_tensor_scale: float, out=None, ctx=None, stream=None):
+    """``nvfp4_matmul`` checked and marshalled once."""
+    import torch
+    T, H = _nvfp4_shape(a_codes, a_scale, "a_codes")
+    N, HB = _nvfp4_shape(b_codes, b_scale, "b_codes")
+    dev = a_codes.device
+    if HB != H:
+        raise ValueError(f"a and b must have the same H, got {H} and {HB}")
+    if b_codes.device != dev:
+        raise ValueError(f"b_codes must be on {dev}, got {b_codes.device}")
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_tensor(out, "out", (T, N), dev)
+    c, s = _ctx_stream(ctx, stream, dev)
+    args = (ctypes.c_void_p(c.handle), _vp(a_codes), _vp(a_scale), a_tensor_scale, _vp(b_codes),
+            _vp(b_scale), b_tensor_scale, T, N, H, _vp(out), s)
+    return PreparedCall(_load().farn_nvfp4_matmul, args, "farn_nvfp4_matmul", out,
+                        (a_codes, a_scale, b_codes, b_scale, c))
+
+
+def nvfp4_matmul(a_codes, a_scale, a_tensor_scale: float, b_codes, b_scale,
+                 b_tensor_scale: float, out=None, ctx=None, stream=None):
+    """The product of two NVFP4 tensors, a [T,H] and b [N,H] (as
+    ``forward_nvfp4`` and ``nvfp4_quantize`` give them), in bf16 [T,N]."""
+    return prepare_nvfp4_matmul(a_codes, a_scale, a_tensor_scale, b_codes, b_scale,
+                                b_tensor_scale, out, ctx, stream)()

@@ -17,44 +17,14 @@
 #include <new>
 
 #include "farn.h"
+#include "farn_internal.h"
 #include "farn_kernels.cuh"
 
+using farn_host::DeviceGuard;
+using farn_host::aligned16;
+using farn_host::overlaps;
+
 static_assert(FARN_MAX_W == farn::kMaxW, "FARN_MAX_W and kernel limit differ");
-
-enum {
-  kVariantRow = 0,
-  kVariantCluster = 1,
-  kVariantGeneric = 2,
-  kVariantBulk = 3,
-  kVariantStage = 4,
-  kVariantCombine = 5,   // the MoE combine's one-CTA-per-row gather kernel
-  kVariantAuto = -1
-};
-
-struct farn_ctx {
-  int device;
-  int num_sms;
-  int max_cluster;     // largest power-of-two cluster size that can be scheduled
-  int force_variant;   // kVariantAuto unless FARN_VARIANT says otherwise
-  int force_cluster;   // 0 = choose; else CTAs per row for the cluster variant
-  int force_vpt;       // 0 = choose; else 16-byte vectors per thread
-  int pdl;             // launch with programmatic stream serialisation
-  int64_t small_t;     // below this many rows a call counts as latency bound
-  int bulk;            // 1: the TMA-staged kernel serves long inputs by default
-  int bulk_ctas;       // resident bulk CTAs per SM (1 or 2)
-  int stage;           // 1: the cp.async-staged kernel serves long inputs
-  int stage_r;         // 0 = choose; else chunks in flight per thread (8/12/16)
-  int stage_ctas;      // 0 = choose; else resident stage CTAs per SM (1..4)
-  int64_t stage_min_t; // the stage kernel serves calls with at least this many rows,
-  int64_t stage_min_bytes;  // or half as many that read at least this many bytes
-  int stage_regs[4][2];  // registers per thread of the staged kernels
-                         // [plain, FP8, MoE combine, NVFP4][4 vectors]
-  int max_smem;        // opt-in shared memory per CTA, bytes
-  int* d_status;       // device status word of the bulk kernel (256 B block)
-  int fault_launch;    // FARN_FAULT_INJECT=launch at create: every launch fails
-  int stall_test;      // FARN_FAULT_INJECT=stall at create: the TMA-staged kernel's
-                       // CTA 0 runs its bounded waits out (a test of the status word)
-};
 
 namespace {
 
@@ -270,14 +240,6 @@ VecKernel pick_vec(int vpt, int cs, int pb, bool one_row = false, bool quant = t
   }
   return pb == 4 ? pick_vec_pb<4>(vpt, cs) : pick_vec_pb<2>(vpt, cs);
 }
-
-bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
-  if (na <= 0 || nb <= 0) return false;
-  uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-  return a0 < b0 + (uintptr_t)nb && b0 < a0 + (uintptr_t)na;
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 int env_int(const char* name, int dflt) {
   const char* s = getenv(name);
@@ -588,19 +550,6 @@ int make_moe_plan(const farn_ctx* ctx, int K, int64_t T, int64_t H, bool vec_ok,
   return FARN_OK;
 }
 
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-    if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
-};
-
 }  // namespace
 
 extern "C" {
@@ -804,6 +753,11 @@ int farn_create(farn_ctx** out, int device) {
       int& regs = c->stage_regs[2][vpt >= 4];
       if (fa.numRegs > regs) regs = fa.numRegs;
     }
+  }
+  if (!farn_host::route_setup(c)) {
+    delete c;
+    cudaGetLastError();
+    return FARN_ERR_CUDA;
   }
   // The bulk kernel's status word: set on a bounded-wait timeout, read and
   // cleared by farn_device_status.
