@@ -754,7 +754,7 @@ int farn_create(farn_ctx** out, int device) {
       if (fa.numRegs > regs) regs = fa.numRegs;
     }
   }
-  if (!farn_host::route_setup(c)) {
+  if (!farn_host::route_setup(c) || !farn_host::product_setup(c)) {
     delete c;
     cudaGetLastError();
     return FARN_ERR_CUDA;

@@ -41,12 +41,15 @@ struct farn_ctx {
   int fault_launch;    // FARN_FAULT_INJECT=launch at create: every launch fails
   int stall_test;      // FARN_FAULT_INJECT=stall at create: the TMA-staged kernel's
                        // CTA 0 runs its bounded waits out (a test of the status word)
+  void* encode_tiled;  // the driver's tensor-map encoder (the products' kernels)
+  int max_clusters[4]; // clusters of 1, 2, 4 and 8 such CTAs that fit the device at a time
 };
 
 namespace farn_host {
 
 // One-time kernel set-up on the current device (farn_create).
 bool route_setup(const farn_ctx* ctx);
+bool product_setup(farn_ctx* ctx);
 
 inline bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
   if (na <= 0 || nb <= 0) return false;

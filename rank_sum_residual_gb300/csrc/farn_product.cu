@@ -9,6 +9,7 @@
 #include "farn.h"
 #include "farn_internal.h"
 #include "farn_product.cuh"
+#include "farn_product_tc.cuh"
 
 static_assert(FARN_MAX_EXPERTS == farn::kMaxExperts, "FARN_MAX_EXPERTS and kernel limit differ");
 
@@ -46,9 +47,179 @@ int launch_plain(const farn_ctx* ctx, const ProductParams& p, bool fp4, cudaStre
   return FARN_OK;
 }
 
+// ------------------------------------------------------ tensor-core kernels
+typedef void (*TcKernel)(const farn::TcParams, const CUtensorMap, const CUtensorMap);
+
+struct TcKind {
+  bool fp4, gather;
+  int cg, bn;
+  TcKernel kernel;
+  int warps, stage_bytes, box;
+};
+
+template <bool FP4, int CG, int BN, bool GATHER>
+TcKind kind() {
+  using Sh = farn::TcShape<FP4, CG, BN>;
+  return TcKind{FP4, GATHER, CG, BN, &farn::farn_product_tc_kernel<FP4, CG, BN, GATHER>,
+                Sh::kWarps, Sh::kStageBytes, Sh::kBox};
+}
+
+const TcKind kKinds[] = {
+    kind<false, 1, 16, false>(),  kind<false, 1, 16, true>(),  kind<false, 1, 32, false>(),
+    kind<false, 1, 32, true>(),   kind<false, 1, 64, false>(), kind<false, 1, 64, true>(),
+    kind<false, 1, 128, false>(), kind<false, 1, 128, true>(), kind<false, 2, 256, false>(),
+    kind<false, 2, 256, true>(),  kind<true, 1, 16, false>(),  kind<true, 1, 32, false>(),
+    kind<true, 1, 64, false>(),   kind<true, 1, 128, false>(), kind<true, 2, 224, false>(),
+};
+
+const TcKind* find_kind(bool fp4, int cg, int bn, bool gather) {
+  for (const TcKind& k : kKinds)
+    if (k.fp4 == fp4 && k.cg == cg && k.bn == bn && k.gather == gather) return &k;
+  return nullptr;
+}
+
+struct TcPlan {
+  const TcKind* kind;
+  int ks, stages;
+  unsigned grid;
+  uint32_t groups_at, part_at, smem;
+};
+
+// Shared memory of a call: the ring, the barriers, the groups, and the
+// parts that the CTAs of a split row exchange; then 1 KB to align the ring.
+bool fit(const farn_ctx* ctx, const TcKind* k, int E, int ks, TcPlan* pl) {
+  const uint32_t part = ks > 1 ? (uint32_t)k->bn * farn::kPartPitch * 4 : 0;
+  const uint32_t fixed =
+      1024 + ((uint32_t)sizeof(farn::TcBarriers) + 15u) / 16 * 16 +
+      (farn::groups_bytes(E) + 15u) / 16 * 16 + part;
+  int stages = ((int)ctx->max_smem - (int)fixed) / k->stage_bytes;
+  if (stages > farn::kTcMaxStages) stages = farn::kTcMaxStages;
+  if (stages < 2) return false;
+  pl->kind = k;
+  pl->ks = ks;
+  pl->stages = stages;
+  pl->groups_at = (uint32_t)stages * k->stage_bytes +
+                  ((uint32_t)sizeof(farn::TcBarriers) + 15u) / 16 * 16;
+  pl->part_at = pl->groups_at + (farn::groups_bytes(E) + 15u) / 16 * 16;
+  pl->smem = pl->part_at + part + 1024;
+  return true;
+}
+
+int log2_of(int v) { return v >= 8 ? 3 : v >= 4 ? 2 : v >= 2 ? 1 : 0; }
+
+// The kernel for a call of S slots in E groups.
+bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, TcPlan* pl) {
+  const bool gather = p.rows != nullptr;
+  const int64_t groups = p.E < p.S ? p.E : p.S;
+  const int64_t avg = (p.S + groups - 1) / groups;     // slots of a group that has some
+  int cg = 1, bn = 128;
+  if (avg <= 8) bn = 16;
+  else if (avg <= 24) bn = 32;
+  else if (avg <= 64) bn = 64;
+  else if (avg <= 128 || p.N <= 128) bn = 128;
+  else { cg = 2; bn = fp4 ? 224 : 256; }
+  const int64_t wts = (p.N + cg * farn::kTcWeights - 1) / (cg * farn::kTcWeights);
+  const int64_t tiles = (p.S / bn + groups) * wts;
+  const int64_t chunks = (p.H + (fp4 ? 255 : 63)) / (fp4 ? 256 : 64);
+  int ks = 1;
+  if (cg == 1)
+    while (ks < 8 && tiles * ks * 2 <= ctx->num_sms && chunks >= ks * 4) ks *= 2;
+  if (!fit(ctx, find_kind(fp4, cg, bn, gather), p.E, ks, pl)) return false;
+  const int csize = cg == 2 ? 2 : ks;
+  const int64_t most = ctx->max_clusters[log2_of(csize)];
+  if (most < 1) return false;
+  pl->grid = (unsigned)((tiles < most ? tiles : most) * csize);
+  return true;
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Rows of `inner` elements, `rows` of them, `outer` times (0: a map of two
+// dimensions); boxes of 128 bytes by `box` rows, written with the 128-byte
+// swizzle, zeros outside the tensor.
+bool encode(const farn_ctx* ctx, CUtensorMap* map, bool fp4, const void* base, int64_t inner,
+            int64_t rows, int64_t outer, int box) {
+  const int64_t bytes = fp4 ? inner / 2 : inner * 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)(fp4 ? inner / 2 : inner), (cuuint64_t)rows,
+                              (cuuint64_t)(outer ? outer : 1)};
+  const cuuint64_t strides[2] = {(cuuint64_t)bytes, (cuuint64_t)bytes * (cuuint64_t)rows};
+  const cuuint32_t boxes[3] = {fp4 ? 128u : 64u, (cuuint32_t)box, 1u};
+  const cuuint32_t steps[3] = {1u, 1u, 1u};
+  return ((EncodeTiled)ctx->encode_tiled)(
+             map, fp4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             outer ? 3 : 2, const_cast<void*>(base), dims, strides, boxes, steps,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// What the tensor-core kernels need of a call: rows that TMA can read (both
+// operands 16-byte aligned, rows a multiple of 16 bytes, strides below 2^40)
+// and slot numbers with room for a tile behind the last.
+bool tc_takes(const farn_ctx* ctx, const ProductParams& p, bool fp4) {
+  return ctx->encode_tiled && ctx->force_variant != kVariantGeneric && aligned16(p.a) &&
+         aligned16(p.b) && p.H % (fp4 ? 32 : 8) == 0 && p.n_a > 0 && p.S <= 0x7FFFFC00 &&
+         p.N <= 0x7FFFFC00 && product_fits(p.N, 2 * p.H) && p.N * 2 * p.H < ((int64_t)1 << 40);
+}
+
+int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPlan& pl,
+              cudaStream_t stream) {
+  farn::TcParams t;
+  memset(&t, 0, sizeof t);
+  t.p = p;
+  t.stages = pl.stages;
+  t.ks = pl.ks;
+  t.pair_stores = p.N % 2 == 0 && ((uintptr_t)p.out & 3u) == 0;
+  t.groups_at = pl.groups_at;
+  t.part_at = pl.part_at;
+  if (fp4) {
+    const int64_t pitch = p.H / 16;
+    const uintptr_t at = (uintptr_t)p.a_scale | (uintptr_t)p.b_scale | (uintptr_t)pitch;
+    t.scale_step = (at & 15u) == 0 ? 16 : (at & 3u) == 0 ? 4 : 1;
+  }
+  CUtensorMap map_w, map_x;
+  const TcKind* k = pl.kind;
+  if (!encode(ctx, &map_w, fp4, p.b, p.H, p.N, p.E, farn::kTcWeights) ||
+      !encode(ctx, &map_x, fp4, p.a, p.H, p.n_a, 0, k->gather ? 1 : k->box))
+    return FARN_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(pl.grid, 1, 1);
+  cfg.blockDim = dim3((unsigned)k->warps * 32, 1, 1);
+  cfg.dynamicSmemBytes = pl.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attrs[2];
+  unsigned n = 0;
+  const unsigned csize = k->cg == 2 ? 2u : (unsigned)pl.ks;
+  if (csize > 1) {
+    attrs[n].id = cudaLaunchAttributeClusterDimension;
+    attrs[n].val.clusterDim.x = csize;
+    attrs[n].val.clusterDim.y = 1;
+    attrs[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (ctx->pdl) {
+    attrs[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attrs;
+  cfg.numAttrs = n;
+  if (cudaLaunchKernelEx(&cfg, k->kernel, t, map_w, map_x) != cudaSuccess) {
+    cudaGetLastError();
+    return FARN_ERR_CUDA;
+  }
+  return FARN_OK;
+}
+
 int launch(const farn_ctx* ctx, const ProductParams& p, bool fp4, cudaStream_t stream) {
   DeviceGuard dg(ctx->device);
   if (!dg.ok) { cudaGetLastError(); return FARN_ERR_CUDA; }
+  TcPlan pl;
+  if (tc_takes(ctx, p, fp4) && plan_tc(ctx, p, fp4, &pl))
+    return launch_tc(ctx, p, fp4, pl, stream);
   return launch_plain(ctx, p, fp4, stream);
 }
 
@@ -59,6 +230,46 @@ bool sizes_ok(int64_t S, int64_t N, int64_t H) {
 }
 
 }  // namespace
+
+namespace farn_host {
+
+// On the current device: the tensor-map encoder, the kernels' shared-memory
+// opt-in, and how many clusters of one-per-SM CTAs fit at a time.
+bool product_setup(farn_ctx* ctx) {
+  ctx->encode_tiled = nullptr;
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                       &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess)
+    return false;
+  for (const TcKind& k : kKinds)
+    if (cudaFuncSetAttribute((const void*)k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ctx->max_smem) != cudaSuccess)
+      return false;
+  for (int i = 0; i < 4; ++i) {
+    // one CTA per SM, as any of the kernels takes it
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(1 << i), 1, 1);
+    cfg.blockDim = dim3(farn::kTcWarpsFp4 * 32, 1, 1);
+    cfg.dynamicSmemBytes = ctx->max_smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1u << i;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(
+            &ctx->max_clusters[i],
+            (const void*)farn::farn_product_tc_kernel<true, 1, 16, false>, &cfg) != cudaSuccess)
+      return false;
+  }
+  ctx->encode_tiled = fn;
+  return true;
+}
+
+}  // namespace farn_host
 
 extern "C" {
 

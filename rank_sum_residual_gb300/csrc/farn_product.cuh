@@ -30,18 +30,22 @@ struct ProductParams {
 };
 
 // The groups' slots and tiles, in shared memory: first[e] .. first[e] +
-// count(e) are the slots of group e, tile[e] the number of slot tiles before
-// it.  Offsets are clamped to 0..S and to be ascending, so that no value of
-// them leads outside the tensors.
+// count[e] - 1 are the slots of group e, tile[e] the number of slot tiles
+// before it.  Offsets are clamped to 0..S and to be ascending, so that no
+// value of them leads outside the tensors.
 struct Groups {
-  int32_t first[kMaxExperts];
-  int32_t count[kMaxExperts];
-  int32_t tile[kMaxExperts + 1];
-  int32_t ws[33];
+  int32_t* first;   // [E]
+  int32_t* count;   // [E]
+  int32_t* tile;    // [E + 1]
 };
+__host__ __device__ constexpr uint32_t groups_bytes(int E) { return (3u * E + 1u) * 4u; }
+__device__ __forceinline__ Groups groups_at(void* smem, int E) {
+  int32_t* v = static_cast<int32_t*>(smem);
+  return Groups{v, v + E, v + 2 * E};
+}
 
 // By all threads of the block (a multiple of 32, at least 64).
-__device__ __forceinline__ void load_groups(Groups* g, const ProductParams& p, int bn) {
+__device__ __forceinline__ void load_groups(const Groups& g, const ProductParams& p, int bn) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
   for (int e = tid; e < p.E; e += nt) {
     int64_t lo = 0, hi = p.S;
@@ -49,25 +53,25 @@ __device__ __forceinline__ void load_groups(Groups* g, const ProductParams& p, i
       lo = min(max((int64_t)p.offsets[e], (int64_t)0), p.S);
       hi = min(max((int64_t)p.offsets[e + 1], lo), p.S);
     }
-    g->first[e] = (int32_t)lo;
-    g->count[e] = (int32_t)(hi - lo);
+    g.first[e] = (int32_t)lo;
+    g.count[e] = (int32_t)(hi - lo);
   }
   __syncthreads();
   if (tid < 32) {   // a warp scans the tile counts, 32 groups at a time
     int32_t at = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      const int32_t n = e < p.E ? (int32_t)(((int64_t)g->count[e] + bn - 1) / bn) : 0;
+      const int32_t n = e < p.E ? (int32_t)(((int64_t)g.count[e] + bn - 1) / bn) : 0;
       int32_t inc = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
         if (lane >= o) inc += y;
       }
-      if (e < p.E) g->tile[e] = at + inc - n;
+      if (e < p.E) g.tile[e] = at + inc - n;
       at += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
-    if (lane == 0) g->tile[p.E] = at;
+    if (lane == 0) g.tile[p.E] = at;
   }
   __syncthreads();
 }
@@ -85,15 +89,15 @@ struct Tile {
 // operands' rows in L2.
 constexpr int kSuper = 8;
 
-__device__ __forceinline__ Tile find_tile(const Groups* g, int E, int64_t t, int wts, int bn) {
+__device__ __forceinline__ Tile find_tile(const Groups& g, int E, int64_t t, int wts, int bn) {
   const int32_t q = (int32_t)(t / wts);
   int lo = 0, hi = E - 1;            // the last e with tile[e] <= q
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (g->tile[mid] <= q) lo = mid; else hi = mid - 1;
+    if (g.tile[mid] <= q) lo = mid; else hi = mid - 1;
   }
-  const int32_t st = g->tile[lo + 1] - g->tile[lo];       // slot tiles of the group
-  const int64_t local = t - (int64_t)g->tile[lo] * wts;
+  const int32_t st = g.tile[lo + 1] - g.tile[lo];       // slot tiles of the group
+  const int64_t local = t - (int64_t)g.tile[lo] * wts;
   const int64_t per = (int64_t)kSuper * wts;
   const int32_t sup = (int32_t)(local / per);
   const int32_t in = (int32_t)(local - sup * per);
@@ -102,8 +106,8 @@ __device__ __forceinline__ Tile find_tile(const Groups* g, int E, int64_t t, int
   r.e = lo;
   r.wt = in / width;
   const int32_t s = sup * kSuper + (in - r.wt * width);
-  r.slot0 = g->first[lo] + s * bn;
-  r.n = min(bn, g->count[lo] - s * bn);
+  r.slot0 = g.first[lo] + s * bn;
+  r.n = min(bn, g.count[lo] - s * bn);
   return r;
 }
 
@@ -136,16 +140,17 @@ __device__ __forceinline__ float product_value(const void* t, const uint8_t* sca
 template <bool FP4>
 __global__ void __launch_bounds__(kPlainThreads)
 farn_product_plain_kernel(const ProductParams p) {
-  __shared__ Groups g;
+  __shared__ int32_t gmem[groups_bytes(kMaxExperts) / 4];
+  const Groups g = groups_at(gmem, p.E);
   __shared__ float as[kPlainK][kPlainTile + 1], bs[kPlainK][kPlainTile + 1];
   pdl_wait();
   pdl_trigger();
-  load_groups(&g, p, kPlainTile);
+  load_groups(g, p, kPlainTile);
   const int tid = threadIdx.x, ti = tid / 16, tj = tid % 16;
   const int wts = (int)((p.N + kPlainTile - 1) / kPlainTile);
   const int64_t tiles = (int64_t)g.tile[p.E] * wts;
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const Tile w = find_tile(&g, p.E, t, wts, kPlainTile);
+    const Tile w = find_tile(g, p.E, t, wts, kPlainTile);
     const int64_t n0 = (int64_t)w.wt * kPlainTile;
     float acc[4][4] = {};
     for (int64_t h0 = 0; h0 < p.H; h0 += kPlainK) {
