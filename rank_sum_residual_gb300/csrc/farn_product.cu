@@ -48,20 +48,21 @@ int launch_plain(const farn_ctx* ctx, const ProductParams& p, bool fp4, cudaStre
 }
 
 // ------------------------------------------------------ tensor-core kernels
-typedef void (*TcKernel)(const farn::TcParams, const CUtensorMap, const CUtensorMap);
+typedef void (*TcKernel)(const farn::TcParams, const CUtensorMap, const CUtensorMap,
+                         const CUtensorMap);
 
 struct TcKind {
   bool fp4, gather;
   int cg, bn;
   TcKernel kernel;
-  int warps, stage_bytes, box;
+  int warps, stage_bytes, rows, box;
 };
 
 template <bool FP4, int CG, int BN, bool GATHER>
 TcKind kind() {
-  using Sh = farn::TcShape<FP4, CG, BN>;
+  using Sh = farn::TcShape<FP4, CG, BN, GATHER>;
   return TcKind{FP4, GATHER, CG, BN, &farn::farn_product_tc_kernel<FP4, CG, BN, GATHER>,
-                Sh::kWarps, Sh::kStageBytes, Sh::kBox};
+                Sh::kWarps, Sh::kStageBytes, Sh::kRows, Sh::kBox};
 }
 
 const TcKind kKinds[] = {
@@ -94,7 +95,7 @@ bool fit(const farn_ctx* ctx, const TcKind* k, int E, int ks, TcPlan* pl) {
       (farn::groups_bytes(E) + 15u) / 16 * 16 + part;
   int stages = ((int)ctx->max_smem - (int)fixed) / k->stage_bytes;
   if (stages > farn::kTcMaxStages) stages = farn::kTcMaxStages;
-  if (stages < 2) return false;
+  if (stages < 2 || stages < k->warps - farn::kTcWarpsBf16) return false;
   pl->kind = k;
   pl->ks = ks;
   pl->stages = stages;
@@ -180,11 +181,18 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
     const uintptr_t at = (uintptr_t)p.a_scale | (uintptr_t)p.b_scale | (uintptr_t)pitch;
     t.scale_step = (at & 15u) == 0 ? 16 : (at & 3u) == 0 ? 4 : 1;
   }
-  CUtensorMap map_w, map_x;
+  CUtensorMap map_w, map_x, map_part;
   const TcKind* k = pl.kind;
-  if (!encode(ctx, &map_w, fp4, p.b, p.H, p.N, p.E, farn::kTcWeights) ||
-      !encode(ctx, &map_x, fp4, p.a, p.H, p.n_a, 0, k->gather ? 1 : k->box))
+  if (!encode(ctx, &map_w, fp4, p.b, p.H, p.N, p.E, farn::kTcWeights)) return FARN_ERR_CUDA;
+  if (k->gather) {
+    map_x = map_part = map_w;     // not read
+  } else if (!encode(ctx, &map_x, fp4, p.a, p.H, p.n_a, 0, k->rows)) {
     return FARN_ERR_CUDA;
+  } else if (k->box == k->rows) {
+    map_part = map_x;
+  } else if (!encode(ctx, &map_part, fp4, p.a, p.H, p.n_a, 0, k->box)) {
+    return FARN_ERR_CUDA;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.grid, 1, 1);
   cfg.blockDim = dim3((unsigned)k->warps * 32, 1, 1);
@@ -207,7 +215,7 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
   }
   cfg.attrs = attrs;
   cfg.numAttrs = n;
-  if (cudaLaunchKernelEx(&cfg, k->kernel, t, map_w, map_x) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, k->kernel, t, map_w, map_x, map_part) != cudaSuccess) {
     cudaGetLastError();
     return FARN_ERR_CUDA;
   }
@@ -251,7 +259,7 @@ bool product_setup(farn_ctx* ctx) {
     // one CTA per SM, as any of the kernels takes it
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(1 << i), 1, 1);
-    cfg.blockDim = dim3(farn::kTcWarpsFp4 * 32, 1, 1);
+    cfg.blockDim = dim3(farn::kTcWarpsMost * 32, 1, 1);
     cfg.dynamicSmemBytes = ctx->max_smem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;

@@ -102,12 +102,17 @@ __device__ __forceinline__ Tile find_tile(const Groups& g, int E, int64_t t, int
   const int32_t sup = (int32_t)(local / per);
   const int32_t in = (int32_t)(local - sup * per);
   const int32_t width = min(kSuper, st - sup * kSuper);
+  // The group's tiles are of one size (a multiple of 32, or of bn below
+  // that), rather than full ones and a rest: a tile of few slots streams its
+  // weights for little work.  None is empty: count > (st - 1) * bn.
+  const int32_t count = g.count[lo], step = min(bn, 32);
+  const int32_t size = ((count - 1) / st / step + 1) * step;
   Tile r;
   r.e = lo;
   r.wt = in / width;
   const int32_t s = sup * kSuper + (in - r.wt * width);
-  r.slot0 = g.first[lo] + s * bn;
-  r.n = min(bn, g.count[lo] - s * bn);
+  r.slot0 = g.first[lo] + s * size;
+  r.n = min(size, count - s * size);
   return r;
 }
 

@@ -6,10 +6,11 @@
 // rows still streams full tiles of weights.  The accumulator is transposed
 // on the way out.
 //
-// A CTA has a producer warp (TMA; a gathering call fetches the slots' rows
-// by index), a warp whose first lane issues the matrix instructions, four
-// epilogue warps, and for NVFP4 four warps that bring the block scales into
-// the layout the tensor cores read.  The ring of stages runs on across
+// A CTA has a producer warp (TMA), a warp that issues the matrix
+// instructions, four epilogue warps, and for NVFP4 four warps that bring the
+// block scales into the layout the tensor cores read, or for a gathering call
+// four warps that copy the slots' rows (cp.async: a TMA gather of four rows of
+// 128 bytes took 95 cycles, 3 times the matrix instructions' time).  The ring of stages runs on across
 // tiles, and two accumulators let the epilogue of one tile overlap the
 // products of the next.
 //
@@ -34,8 +35,13 @@ constexpr int kTcMaxStages = 12;
 constexpr int kTcRowBytes = 128;       // bytes of a row per stage: one swizzle span
 constexpr int kTcWeights = 128;        // weights per CTA and tile
 constexpr int kTcWarpsBf16 = 6;
-constexpr int kTcWarpsFp4 = 10;
-constexpr int kTcScaleWarps = 4;
+// Further warps for block scales, or for gathered rows.  Each takes every
+// kAux-th stage.  They may not be more than the ring has stages: a warp that
+// waits for a stage has to be within one round of the ring, or the parity of
+// the phase it waits for says nothing.
+constexpr int kTcAuxFp4 = 4;
+constexpr int kTcAuxGather = 6;
+constexpr int kTcWarpsMost = kTcWarpsBf16 + kTcAuxGather;
 constexpr int kErrTcFull = 16;         // status bits: matrix warp waiting for operands,
 constexpr int kErrTcEmpty = 32;        // producers waiting for a free stage,
 constexpr int kErrTcTile = 64;         // epilogue or matrix warp waiting for a tile,
@@ -54,7 +60,7 @@ struct TcParams {
 struct TcBarriers {
   uint64_t full[kTcMaxStages];
   uint64_t empty[kTcMaxStages];
-  uint64_t scales[kTcMaxStages];
+  uint64_t aux[kTcMaxStages];      // scales or gathered rows in place
   uint64_t tile_full[2];
   uint64_t tile_empty[2];
   uint64_t part_full;
@@ -66,9 +72,10 @@ struct TcBarriers {
 
 constexpr int kPartPitch = kTcWeights + 4;
 
-template <bool FP4, int CG, int BN>
+template <bool FP4, int CG, int BN, bool GATHER>
 struct TcShape {
-  static constexpr int kWarps = FP4 ? kTcWarpsFp4 : kTcWarpsBf16;
+  static constexpr int kAux = FP4 ? kTcAuxFp4 : GATHER ? kTcAuxGather : 0;
+  static constexpr int kWarps = kTcWarpsBf16 + kAux;
   static constexpr int kRows = BN / CG;                      // slots per CTA
   static constexpr int kBox = kRows % 32 == 0 ? 32 : 16;     // rows of a TMA box
   static constexpr int kABytes = kTcWeights * kTcRowBytes;
@@ -85,14 +92,17 @@ struct TcShape {
   static_assert(kColsUsed <= 512 && kBBytes % 1024 == 0 && kScaleBytes % 1024 == 0, "");
 };
 
-// Bounded phase wait with cluster scope.
+// Bounded phase wait.  JOIN: what other CTAs of the cluster wrote before they
+// arrived is read afterwards.
+constexpr uint32_t kTcSleepNs = 1000000;
+
+template <bool JOIN = false>
 __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                         int* err, int code) {
-  if (tc::mbar_try_wait_cluster(bar, parity)) return true;
+  if (tc::mbar_wait_some<JOIN>(bar, parity, kTcSleepNs)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-    for (int i = 0; i < 16; ++i)
-      if (tc::mbar_try_wait_cluster(bar, parity)) return true;
+    if (tc::mbar_wait_some<JOIN>(bar, parity, kTcSleepNs)) return true;
     if (*abort_flag) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       *abort_flag = 1;
@@ -102,10 +112,23 @@ __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile 
   }
 }
 
+// A place in the ring of stages.
+struct RingPos {
+  uint32_t stage = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t stages) {
+    if (++stage == stages) { stage = 0; phase ^= 1; }
+  }
+  // `by` stages on
+  __device__ __forceinline__ void skip(uint32_t by, uint32_t stages) {
+    for (stage += by; stage >= stages; stage -= stages) phase ^= 1;
+  }
+};
+
 // The same by a whole warp, whose lanes go on or give up together.
+template <bool JOIN = false>
 __device__ __forceinline__ bool tc_wait_warp(uint32_t bar, uint32_t parity,
                                              volatile int* abort_flag, int* err, int code) {
-  return __all_sync(0xFFFFFFFFu, tc_wait(bar, parity, abort_flag, err, code));
+  return __all_sync(0xFFFFFFFFu, tc_wait<JOIN>(bar, parity, abort_flag, err, code));
 }
 
 // 16 scale bytes of a row from `at`, of which `left` belong to the row; the
@@ -126,33 +149,35 @@ __device__ __forceinline__ uint4 load_scales16(const uint8_t* at, int64_t left, 
 }
 
 template <bool FP4, int CG, int BN, bool GATHER>
-__global__ void __launch_bounds__(TcShape<FP4, CG, BN>::kWarps * 32, 1)
+__global__ void __launch_bounds__(TcShape<FP4, CG, BN, GATHER>::kWarps * 32, 1)
 farn_product_tc_kernel(const __grid_constant__ TcParams t,
                        const __grid_constant__ CUtensorMap map_w,
-                       const __grid_constant__ CUtensorMap map_x) {
-  using Sh = TcShape<FP4, CG, BN>;
+                       const __grid_constant__ CUtensorMap map_x,
+                       const __grid_constant__ CUtensorMap map_part) {
+  using Sh = TcShape<FP4, CG, BN, GATHER>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const ProductParams& p = t.p;
   const uint32_t base = (tc::smem_addr(smem_raw) + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - tc::smem_addr(smem_raw));
-  const int NS = t.stages;
+  const uint32_t NS = t.stages;
   TcBarriers* bb = reinterpret_cast<TcBarriers*>(smem + (size_t)NS * Sh::kStageBytes);
   const Groups g = groups_at(smem + t.groups_at, p.E);
   const uint32_t full0 = tc::smem_addr(&bb->full[0]);
   const uint32_t empty0 = tc::smem_addr(&bb->empty[0]);
-  const uint32_t scales0 = tc::smem_addr(&bb->scales[0]);
+  const uint32_t aux0 = tc::smem_addr(&bb->aux[0]);
   const uint32_t tfull0 = tc::smem_addr(&bb->tile_full[0]);
   const uint32_t tempty0 = tc::smem_addr(&bb->tile_empty[0]);
   volatile int* abort_flag = &bb->abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // uniform
   const uint32_t rank = cluster_ctarank();
   const int csize = CG == 2 ? 2 : t.ks;
 
   if (tid == 0) {
-    for (int s = 0; s < NS; ++s) {
+    for (uint32_t s = 0; s < NS; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
-      mbar_init(scales0 + 8 * s, CG);
+      mbar_init(aux0 + 8 * s, CG);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull0 + 8 * i, 1);
@@ -167,7 +192,10 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
   if (warp == 5) tc::tmem_alloc<CG>(tc::smem_addr(&bb->tmem), Sh::kCols);
   if (tid == 4 * 32) {
     tc::prefetch_map(&map_w);
-    tc::prefetch_map(&map_x);
+    if constexpr (!GATHER) {
+      tc::prefetch_map(&map_x);
+      tc::prefetch_map(&map_part);
+    }
   }
   pdl_wait();
   pdl_trigger();
@@ -190,7 +218,8 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
   if (warp == 4) {
     // ---------------------------------------------------------- producer
     const uint32_t bar_rank = CG == 2 ? 0 : rank;
-    uint32_t it = 0;
+    RingPos at;
+    uint32_t armed = 0;        // stages given to TMA, all but the last NS done
     bool ok = true;
     if (t.p.stall_test && blockIdx.x == 0)
       ok = tc_wait_warp(tc::smem_addr(&bb->never), 0, abort_flag, p.err, kErrTcEmpty);
@@ -199,55 +228,48 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       const int n_eff = (w.n + Sh::kStep - 1) / Sh::kStep * Sh::kStep;
       const int rows = n_eff / CG;                       // of this CTA, a multiple of 16
       const int first = w.slot0 + w_rank * rows;
-      const int loads = GATHER ? rows / 4 : (rows + Sh::kBox - 1) / Sh::kBox;
-      const uint32_t bytes = GATHER ? (uint32_t)rows * kTcRowBytes
-                                    : (uint32_t)loads * Sh::kBox * kTcRowBytes;
-      int4 r4 = make_int4(0, 0, 0, 0);
-      if constexpr (GATHER) {
-        // a row that does not exist reads row 0; the epilogue writes zeros
-        int* r = &r4.x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t s = (int64_t)first + lane * 4 + i;
-          int v = 0;
-          if (lane < loads && s < p.S) v = p.rows[s];
-          r[i] = v >= 0 && v < p.n_a ? v : 0;
-        }
-      }
+      // whole tiles with one box, others with boxes of a few rows
+      const bool whole = rows > Sh::kRows - Sh::kBox;
+      const int loads = GATHER ? 0 : whole ? 1 : (rows + Sh::kBox - 1) / Sh::kBox;
+      const uint32_t bytes = (uint32_t)loads * (whole ? Sh::kRows : Sh::kBox) * kTcRowBytes;
       const int n0 = w.wt * kTileWeights + w_rank * kTcWeights;
-      for (int c = c0; c < c1; ++c, ++it) {
-        const uint32_t s = it % NS, ph = (it / NS) & 1;
-        ok = tc_wait_warp(empty0 + 8 * s, ph ^ 1, abort_flag, p.err, kErrTcEmpty);
+      for (int c = c0; c < c1; ++c, at.next(NS), ++armed) {
+        const uint32_t s = at.stage;
+        ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
         if (!ok) break;
         const uint32_t a = base + s * Sh::kStageBytes, b = a + Sh::kABytes;
         const uint32_t bar = tc::map_rank(full0 + 8 * s, bar_rank);
-        if (lane == 0 && w_rank == 0)
-          mbar_arrive_expect_tx(full0 + 8 * s, CG * (Sh::kABytes + bytes));
-        __syncwarp();
         const int x = c * (FP4 ? kTcRowBytes : Sh::kChunk);
-        if (lane == 0) tc::load_3d<CG>(a, &map_w, x, n0, w.e, bar);
-        if constexpr (GATHER) {
-          if (lane < loads) tc::gather4<CG>(b + lane * 4 * kTcRowBytes, &map_x, x, r4, bar);
-        } else {
-          if (lane < loads)
-            tc::load_2d<CG>(b + lane * Sh::kBox * kTcRowBytes, &map_x, x,
-                            first + lane * Sh::kBox, bar);
+        if (tc::elect_one()) {
+          if (w_rank == 0)
+            mbar_arrive_expect_tx(full0 + 8 * s, CG * (Sh::kABytes + bytes));
+          tc::load_3d<CG>(a, &map_w, x, n0, w.e, bar);
+          if (!GATHER && whole) {
+            tc::load_2d<CG>(b, &map_x, x, first, bar);
+          } else if constexpr (!GATHER) {
+            for (int i = 0; i < loads; ++i)
+              tc::load_2d<CG>(b + i * Sh::kBox * kTcRowBytes, &map_part, x, first + i * Sh::kBox,
+                              bar);
+          }
         }
+        __syncwarp();
       }
     }
     // After an abort: the stages in flight land before the CTA leaves.
     if (*abort_flag && w_rank == 0) {
-      for (uint32_t k = it > (uint32_t)NS ? it - NS : 0; k < it; ++k) {
+      for (uint32_t k = armed > NS ? armed - NS : 0; k < armed; ++k) {
         const uint64_t begin = globaltimer_ns();
-        while (!tc::mbar_try_wait_cluster(full0 + 8 * (k % NS), (k / NS) & 1) &&
+        while (!tc::mbar_wait_some<true>(full0 + 8 * (k % NS), (k / NS) & 1, kTcSleepNs) &&
                globaltimer_ns() - begin < kWaitLimitNs) {}
       }
     }
   } else if (warp == 5) {
     // ------------------------------------------------- matrix instructions
-    if (lane == 0 && w_rank == 0) {
-      uint32_t it = 0, nt = 0;
+    if (w_rank == 0) {
+      RingPos at;
+      uint32_t nt = 0;
       bool ok = true;
+      const uint64_t desc0 = tc::operand_desc(base);
       const uint32_t sf_a = tmem + 2 * BN, sf_b = sf_a + 16;
       for (int64_t tile = t0; ok && tile < tiles; tile += tstep, ++nt) {
         const Tile w = find_tile(g, p.E, tile, wts, BN);
@@ -255,19 +277,19 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         const uint32_t idesc = FP4 ? tc::idesc_nvfp4(kTileWeights, n_eff)
                                    : tc::idesc_bf16(kTileWeights, n_eff);
         const uint32_t acc = nt & 1, d = tmem + acc * BN;
-        ok = tc_wait(tempty0 + 8 * acc, ((nt >> 1) & 1) ^ 1, abort_flag, p.err, kErrTcTile);
+        ok = tc_wait_warp(tempty0 + 8 * acc, ((nt >> 1) & 1) ^ 1, abort_flag, p.err, kErrTcTile);
         if (!ok) break;
         tc::fence_after();
-        for (int c = 0; c < nc; ++c, ++it) {
-          const uint32_t s = it % NS, ph = (it / NS) & 1;
-          ok = tc_wait(full0 + 8 * s, ph, abort_flag, p.err, kErrTcFull);
-          if (FP4 && ok) ok = tc_wait(scales0 + 8 * s, ph, abort_flag, p.err, kErrTcFull);
+        for (int c = 0; c < nc; ++c, at.next(NS)) {
+          const uint32_t s = at.stage, ph = at.phase;
+          ok = tc_wait_warp(full0 + 8 * s, ph, abort_flag, p.err, kErrTcFull);
+          if (Sh::kAux && ok) ok = tc_wait_warp(aux0 + 8 * s, ph, abort_flag, p.err, kErrTcFull);
           if (!ok) break;
           tc::fence_after();
-          const uint32_t a = base + s * Sh::kStageBytes, b = a + Sh::kABytes;
-          const uint64_t da = tc::operand_desc(a), db = tc::operand_desc(b);
+          const uint64_t da = desc0 + (s * Sh::kStageBytes >> 4), db = da + (Sh::kABytes >> 4);
+          if (tc::elect_one()) {
           if constexpr (FP4) {
-            const uint32_t sc = b + Sh::kBBytes;
+            const uint32_t sc = base + s * Sh::kStageBytes + Sh::kABytes + Sh::kBBytes;
             const int blocks = (n_eff + 127) / 128;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -286,9 +308,10 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
               tc::mma_bf16<CG>(d, da + 2 * k, db + 2 * k, idesc, c > 0 || k > 0);
           }
           tc::commit<CG>(empty0 + 8 * s);
+          if (c == nc - 1) tc::commit<CG>(tfull0 + 8 * acc);
+          }
+          __syncwarp();
         }
-        if (!ok) break;
-        tc::commit<CG>(tfull0 + 8 * acc);
       }
     }
     __syncwarp();
@@ -310,7 +333,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       const bool split = CG == 1 && csize > 1;
       if (split) {
         // the other CTAs have read this one's last part
-        ok = tc_wait_warp(part_empty, (nt & 1) ^ 1, abort_flag, p.err, kErrTcJoin);
+        ok = tc_wait_warp<true>(part_empty, (nt & 1) ^ 1, abort_flag, p.err, kErrTcJoin);
         if (!ok) break;
         for (int c = 0; c < w.n; c += 16) {
           uint32_t v[16];
@@ -363,7 +386,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(tempty0 + 8 * acc, CG == 2 ? 0 : rank));
       if (split) {
         if (lane < csize) tc::mbar_arrive_cluster(tc::map_rank(part_full, lane));
-        ok = tc_wait_warp(part_full, nt & 1, abort_flag, p.err, kErrTcJoin);
+        ok = tc_wait_warp<true>(part_full, nt & 1, abort_flag, p.err, kErrTcJoin);
         if (!ok) break;
         const uint32_t mine = tc::smem_addr(part);
         for (int i = (int)rank * 128 + tid; i < w.n * 128; i += csize * 128) {
@@ -388,15 +411,17 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     // four scales of the k-th 64 elements.
     const int mine = warp - 6;
     const int64_t pitch = p.H / 16;
-    uint32_t it = 0;
+    RingPos at;
+    at.skip(mine, NS);
+    int ahead = mine;          // stages until this warp's next
     bool ok = true;
     for (int64_t tile = t0; ok && tile < tiles; tile += tstep) {
       const Tile w = find_tile(g, p.E, tile, wts, BN);
       const int64_t n0 = (int64_t)w.wt * kTileWeights + w_rank * kTcWeights;
       const int blocks = (w.n + 127) / 128;
-      for (int c = c0; c < c1; ++c, ++it) {
-        if ((int)(it % kTcScaleWarps) != mine) continue;
-        const uint32_t s = it % NS, ph = (it / NS) & 1;
+      int c = c0 + ahead;
+      for (; c < c1; c += Sh::kAux, at.skip(Sh::kAux, NS)) {
+        const uint32_t s = at.stage;
         const int64_t left = pitch - (int64_t)c * 16;
         uint4 v[1 + Sh::kSlotBlocks][4];
 #pragma unroll
@@ -412,7 +437,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
                            : make_uint4(0u, 0u, 0u, 0u);
           }
         }
-        ok = tc_wait_warp(empty0 + 8 * s, ph ^ 1, abort_flag, p.err, kErrTcEmpty);
+        ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
         if (!ok) break;
         unsigned char* dst = smem + s * Sh::kStageBytes + Sh::kABytes + Sh::kBBytes;
 #pragma unroll
@@ -426,7 +451,65 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         }
         tc::fence_async_shared();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(scales0 + 8 * s, CG == 2 ? 0 : rank));
+        if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(aux0 + 8 * s, CG == 2 ? 0 : rank));
+      }
+      ahead = c - c1;
+    }
+  }
+
+  if constexpr (GATHER) {
+    if (warp >= 6) {
+      // ------------------------------------------------------ gathered rows
+      // Warp i takes every sixth stage, so that a stage's copies have the whole
+      // ring's time to land.  Eight lanes copy a row's 128 bytes, in the
+      // swizzled layout that TMA would write: 16-byte column j of row r at
+      // j ^ (r & 7).  Lane l knows the rows l, l + 32, l + 64 and l + 96.
+      constexpr int kHeld = (Sh::kRows + 31) / 32;
+      const int mine = warp - 6, col = lane & 7, sub = lane >> 3;
+      const char* x = static_cast<const char*>(p.a) + col * 16;
+      const uint64_t pitch = (uint64_t)p.H * 2;
+      RingPos at;
+      at.skip(mine, NS);
+      int ahead = mine;
+      bool ok = true;
+      for (int64_t tile = t0; ok && tile < tiles; tile += tstep) {
+        const Tile w = find_tile(g, p.E, tile, wts, BN);
+        const int n_eff = (w.n + Sh::kStep - 1) / Sh::kStep * Sh::kStep;
+        const int rows = n_eff / CG;           // a multiple of 16
+        int32_t held[kHeld];                   // negative: zeros
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+          const int r = w_rank * rows + i * 32 + lane;
+          held[i] = -1;
+          if (i * 32 + lane < rows && r < w.n) held[i] = p.rows[(int64_t)w.slot0 + r];
+          if (held[i] >= p.n_a) held[i] = -1;
+        }
+        int c = c0 + ahead;
+        for (; c < c1; c += Sh::kAux, at.skip(Sh::kAux, NS)) {
+          const uint32_t s = at.stage;
+          ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
+          if (!ok) break;
+          const uint32_t b = base + s * Sh::kStageBytes + Sh::kABytes + sub * kTcRowBytes;
+          const bool in_row = (int64_t)c * Sh::kChunk + col * 8 < p.H;
+          const char* from = x + (int64_t)c * kTcRowBytes;
+#pragma unroll
+          for (int i = 0; i < kHeld; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {       // rows i * 32 + j * 4 + sub
+              if (i * 32 + j * 4 >= rows) break;
+              const int32_t row = __shfl_sync(0xFFFFFFFFu, held[i], j * 4 + sub);
+              const bool have = in_row && row >= 0;
+              tc::copy16(b + (i * 32 + j * 4) * kTcRowBytes + ((col ^ ((j * 4 + sub) & 7)) << 4),
+                         have ? from + (uint32_t)row * pitch : p.a, have ? 16u : 0u);
+            }
+          cp_async_commit();
+          cp_async_wait<0>();
+          tc::fence_async_shared();
+          __syncwarp();
+          if (lane == 0)
+            tc::mbar_arrive_cluster(tc::map_rank(aux0 + 8 * s, CG == 2 ? 0 : rank));
+        }
+        ahead = c - c1;
       }
     }
   }
@@ -435,11 +518,12 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
   // with the last tile; after an abort the tensor cores may still be at work
   // on what they were given, so the warp waits for that here.
   __syncthreads();
-  if (*abort_flag && warp == 5 && lane == 0 && w_rank == 0) {
+  if (*abort_flag && warp == 5 && w_rank == 0) {
     const uint32_t never = tc::smem_addr(&bb->never);
-    tc::commit<CG>(never);
+    if (tc::elect_one()) tc::commit<CG>(never);
+    __syncwarp();
     const uint64_t begin = globaltimer_ns();
-    while (!tc::mbar_try_wait_cluster(never, 0) && globaltimer_ns() - begin < kWaitLimitNs) {}
+    while (!tc::mbar_wait_some<true>(never, 0, kTcSleepNs) && globaltimer_ns() - begin < kWaitLimitNs) {}
   }
   tc::fence_before();
   if (csize > 1) tc::cluster_sync(); else __syncthreads();
