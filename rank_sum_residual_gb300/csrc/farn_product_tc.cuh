@@ -60,7 +60,6 @@ struct TcParams {
 struct TcBarriers {
   uint64_t full[kTcMaxStages];
   uint64_t empty[kTcMaxStages];
-  uint64_t aux[kTcMaxStages];      // scales or gathered rows in place
   uint64_t tile_full[2];
   uint64_t tile_empty[2];
   uint64_t part_full;
@@ -164,7 +163,6 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
   const Groups g = groups_at(smem + t.groups_at, p.E);
   const uint32_t full0 = tc::smem_addr(&bb->full[0]);
   const uint32_t empty0 = tc::smem_addr(&bb->empty[0]);
-  const uint32_t aux0 = tc::smem_addr(&bb->aux[0]);
   const uint32_t tfull0 = tc::smem_addr(&bb->tile_full[0]);
   const uint32_t tempty0 = tc::smem_addr(&bb->tile_empty[0]);
   volatile int* abort_flag = &bb->abort_flag;
@@ -175,9 +173,8 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
 
   if (tid == 0) {
     for (uint32_t s = 0; s < NS; ++s) {
-      mbar_init(full0 + 8 * s, 1);
+      mbar_init(full0 + 8 * s, Sh::kAux ? 1 + CG : 1);   // TMA; scales or gathered rows
       mbar_init(empty0 + 8 * s, 1);
-      mbar_init(aux0 + 8 * s, CG);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull0 + 8 * i, 1);
@@ -270,6 +267,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       uint32_t nt = 0;
       bool ok = true;
       const uint64_t desc0 = tc::operand_desc(base);
+      const uint64_t scale0 = tc::scale_desc(base + Sh::kABytes + Sh::kBBytes);
       const uint32_t sf_a = tmem + 2 * BN, sf_b = sf_a + 16;
       for (int64_t tile = t0; ok && tile < tiles; tile += tstep, ++nt) {
         const Tile w = find_tile(g, p.E, tile, wts, BN);
@@ -283,20 +281,20 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         for (int c = 0; c < nc; ++c, at.next(NS)) {
           const uint32_t s = at.stage, ph = at.phase;
           ok = tc_wait_warp(full0 + 8 * s, ph, abort_flag, p.err, kErrTcFull);
-          if (Sh::kAux && ok) ok = tc_wait_warp(aux0 + 8 * s, ph, abort_flag, p.err, kErrTcFull);
           if (!ok) break;
           tc::fence_after();
           const uint64_t da = desc0 + (s * Sh::kStageBytes >> 4), db = da + (Sh::kABytes >> 4);
           if (tc::elect_one()) {
           if constexpr (FP4) {
-            const uint32_t sc = base + s * Sh::kStageBytes + Sh::kABytes + Sh::kBBytes;
-            const int blocks = (n_eff + 127) / 128;
+            const uint64_t sc = scale0 + (s * Sh::kStageBytes >> 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              tc::copy_scales<CG>(sf_a + 4 * k, tc::scale_desc(sc + 512 * k));
-              for (int j = 0; j < blocks; ++j)
-                tc::copy_scales<CG>(sf_b + (k * Sh::kSlotBlocks + j) * 4,
-                                    tc::scale_desc(sc + 2048 * (1 + j) + 512 * k));
+              tc::copy_scales<CG>(sf_a + 4 * k, sc + (512 >> 4) * k);
+#pragma unroll
+              for (int j = 0; j < Sh::kSlotBlocks; ++j)
+                if (j == 0 || n_eff > 128)
+                  tc::copy_scales<CG>(sf_b + (k * Sh::kSlotBlocks + j) * 4,
+                                      sc + (2048 >> 4) * (1 + j) + (512 >> 4) * k);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -451,7 +449,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         }
         tc::fence_async_shared();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(aux0 + 8 * s, CG == 2 ? 0 : rank));
+        if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(full0 + 8 * s, CG == 2 ? 0 : rank));
       }
       ahead = c - c1;
     }
@@ -507,7 +505,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
           tc::fence_async_shared();
           __syncwarp();
           if (lane == 0)
-            tc::mbar_arrive_cluster(tc::map_rank(aux0 + 8 * s, CG == 2 ? 0 : rank));
+            tc::mbar_arrive_cluster(tc::map_rank(full0 + 8 * s, CG == 2 ? 0 : rank));
         }
         ahead = c - c1;
       }
