@@ -49,7 +49,7 @@ int launch_plain(const farn_ctx* ctx, const ProductParams& p, bool fp4, cudaStre
 
 // ------------------------------------------------------ tensor-core kernels
 typedef void (*TcKernel)(const farn::TcParams, const CUtensorMap, const CUtensorMap,
-                         const CUtensorMap);
+                         const CUtensorMap, const CUtensorMap, const CUtensorMap);
 
 struct TcKind {
   bool fp4, gather;
@@ -157,6 +157,20 @@ bool encode(const farn_ctx* ctx, CUtensorMap* map, bool fp4, const void* base, i
          CUDA_SUCCESS;
 }
 
+// Block scales: 16 bytes (256 elements) of 128 rows, as they lie.
+bool encode_scales(const farn_ctx* ctx, CUtensorMap* map, const void* base, int64_t pitch,
+                   int64_t rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)pitch};
+  const cuuint32_t boxes[2] = {16u, 128u};
+  const cuuint32_t steps[2] = {1u, 1u};
+  return ((EncodeTiled)ctx->encode_tiled)(
+             map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, boxes,
+             steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
 // What the tensor-core kernels need of a call: rows that TMA can read (both
 // operands 16-byte aligned, rows a multiple of 16 bytes, strides below 2^40)
 // and slot numbers with room for a tile behind the last.
@@ -180,8 +194,9 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
     const int64_t pitch = p.H / 16;
     const uintptr_t at = (uintptr_t)p.a_scale | (uintptr_t)p.b_scale | (uintptr_t)pitch;
     t.scale_step = (at & 15u) == 0 ? 16 : (at & 3u) == 0 ? 4 : 1;
+    t.tma_scales = t.scale_step == 16;
   }
-  CUtensorMap map_w, map_x, map_part;
+  CUtensorMap map_w, map_x, map_part, map_ws, map_xs;
   const TcKind* k = pl.kind;
   if (!encode(ctx, &map_w, fp4, p.b, p.H, p.N, p.E, farn::kTcWeights)) return FARN_ERR_CUDA;
   if (k->gather) {
@@ -193,6 +208,10 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
   } else if (!encode(ctx, &map_part, fp4, p.a, p.H, p.n_a, 0, k->box)) {
     return FARN_ERR_CUDA;
   }
+  map_ws = map_xs = map_w;        // not read, unless
+  if (t.tma_scales && (!encode_scales(ctx, &map_ws, p.b_scale, p.H / 16, p.N) ||
+                       !encode_scales(ctx, &map_xs, p.a_scale, p.H / 16, p.n_a)))
+    return FARN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.grid, 1, 1);
   cfg.blockDim = dim3((unsigned)k->warps * 32, 1, 1);
@@ -215,7 +234,7 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
   }
   cfg.attrs = attrs;
   cfg.numAttrs = n;
-  if (cudaLaunchKernelEx(&cfg, k->kernel, t, map_w, map_x, map_part) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, k->kernel, t, map_w, map_x, map_part, map_ws, map_xs) != cudaSuccess) {
     cudaGetLastError();
     return FARN_ERR_CUDA;
   }

@@ -52,13 +52,15 @@ struct TcParams {
   int stages;
   int ks;            // CTAs of a cluster that split the row (CG = 1)
   int pair_stores;   // N even and out 4-byte aligned
-  int scale_step;    // NVFP4: bytes per load of scales that alignment allows
+  int tma_scales;    // NVFP4: rows of scales that TMA can read, else
+  int scale_step;    // bytes per load of scales that alignment allows
   uint32_t groups_at;  // shared-memory offsets
   uint32_t part_at;    // fp32 [BN][kPartPitch], for ks > 1
 };
 
 struct TcBarriers {
   uint64_t full[kTcMaxStages];
+  uint64_t raw[kTcMaxStages];      // block scales as they lie in memory
   uint64_t empty[kTcMaxStages];
   uint64_t tile_full[2];
   uint64_t tile_empty[2];
@@ -152,7 +154,9 @@ __global__ void __launch_bounds__(TcShape<FP4, CG, BN, GATHER>::kWarps * 32, 1)
 farn_product_tc_kernel(const __grid_constant__ TcParams t,
                        const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ CUtensorMap map_x,
-                       const __grid_constant__ CUtensorMap map_part) {
+                       const __grid_constant__ CUtensorMap map_part,
+                       const __grid_constant__ CUtensorMap map_ws,
+                       const __grid_constant__ CUtensorMap map_xs) {
   using Sh = TcShape<FP4, CG, BN, GATHER>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const ProductParams& p = t.p;
@@ -163,6 +167,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
   const Groups g = groups_at(smem + t.groups_at, p.E);
   const uint32_t full0 = tc::smem_addr(&bb->full[0]);
   const uint32_t empty0 = tc::smem_addr(&bb->empty[0]);
+  const uint32_t raw0 = tc::smem_addr(&bb->raw[0]);
   const uint32_t tfull0 = tc::smem_addr(&bb->tile_full[0]);
   const uint32_t tempty0 = tc::smem_addr(&bb->tile_empty[0]);
   volatile int* abort_flag = &bb->abort_flag;
@@ -175,6 +180,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     for (uint32_t s = 0; s < NS; ++s) {
       mbar_init(full0 + 8 * s, Sh::kAux ? 1 + CG : 1);   // TMA; scales or gathered rows
       mbar_init(empty0 + 8 * s, 1);
+      mbar_init(raw0 + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull0 + 8 * i, 1);
@@ -192,6 +198,10 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     if constexpr (!GATHER) {
       tc::prefetch_map(&map_x);
       tc::prefetch_map(&map_part);
+    }
+    if (FP4 && t.tma_scales) {
+      tc::prefetch_map(&map_ws);
+      tc::prefetch_map(&map_xs);
     }
   }
   pdl_wait();
@@ -247,6 +257,14 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
             for (int i = 0; i < loads; ++i)
               tc::load_2d<CG>(b + i * Sh::kBox * kTcRowBytes, &map_part, x, first + i * Sh::kBox,
                               bar);
+          }
+          if (FP4 && t.tma_scales) {
+            const int blocks = w.n > 128 ? 2 : 1;
+            const uint32_t sc = b + Sh::kBBytes, rbar = raw0 + 8 * s;
+            mbar_arrive_expect_tx(rbar, 2048 * (1 + blocks));
+            tc::load_2d<1>(sc, &map_ws, c * 16, n0, rbar);
+            tc::load_2d<1>(sc + 2048, &map_xs, c * 16, w.slot0, rbar);
+            if (blocks > 1) tc::load_2d<1>(sc + 4096, &map_xs, c * 16, w.slot0 + 128, rbar);
           }
         }
         __syncwarp();
@@ -422,6 +440,19 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         const uint32_t s = at.stage;
         const int64_t left = pitch - (int64_t)c * 16;
         uint4 v[1 + Sh::kSlotBlocks][4];
+        unsigned char* dst = smem + s * Sh::kStageBytes + Sh::kABytes + Sh::kBBytes;
+        if (t.tma_scales) {
+          ok = tc_wait_warp(raw0 + 8 * s, at.phase, abort_flag, p.err, kErrTcFull);
+          if (!ok) break;
+#pragma unroll
+          for (int u = 0; u <= Sh::kSlotBlocks; ++u) {
+            if (u > blocks) break;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              v[u][r] = reinterpret_cast<const uint4*>(dst + u * 2048)[r * 32 + lane];
+          }
+          __syncwarp();       // in place: all of it is read before any is written
+        } else {
 #pragma unroll
         for (int u = 0; u <= Sh::kSlotBlocks; ++u) {
           if (u > blocks) break;
@@ -437,7 +468,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         }
         ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
         if (!ok) break;
-        unsigned char* dst = smem + s * Sh::kStageBytes + Sh::kABytes + Sh::kBBytes;
+        }
 #pragma unroll
         for (int u = 0; u <= Sh::kSlotBlocks; ++u) {
           if (u > blocks) break;
