@@ -83,7 +83,7 @@ struct TcPlan {
   const TcKind* kind;
   int ks, stages;
   unsigned grid;
-  uint32_t groups_at, part_at, smem;
+  uint32_t groups_at, turn_at, part_at, smem;
 };
 
 // Shared memory of a call: the ring, the barriers, the groups, and the
@@ -92,7 +92,7 @@ bool fit(const farn_ctx* ctx, const TcKind* k, int E, int ks, TcPlan* pl) {
   const uint32_t part = ks > 1 ? (uint32_t)k->bn * farn::kPartPitch * 4 : 0;
   const uint32_t fixed =
       1024 + ((uint32_t)sizeof(farn::TcBarriers) + 15u) / 16 * 16 +
-      (farn::groups_bytes(E) + 15u) / 16 * 16 + part;
+      (farn::groups_bytes(E) + 15u) / 16 * 16 + 4 * farn::kTurnBytes + part;
   int stages = ((int)ctx->max_smem - (int)fixed) / k->stage_bytes;
   if (stages > farn::kTcMaxStages) stages = farn::kTcMaxStages;
   if (stages < 2 || stages < k->warps - farn::kTcWarpsBf16) return false;
@@ -101,7 +101,8 @@ bool fit(const farn_ctx* ctx, const TcKind* k, int E, int ks, TcPlan* pl) {
   pl->stages = stages;
   pl->groups_at = (uint32_t)stages * k->stage_bytes +
                   ((uint32_t)sizeof(farn::TcBarriers) + 15u) / 16 * 16;
-  pl->part_at = pl->groups_at + (farn::groups_bytes(E) + 15u) / 16 * 16;
+  pl->turn_at = pl->groups_at + (farn::groups_bytes(E) + 15u) / 16 * 16;
+  pl->part_at = pl->turn_at + 4 * farn::kTurnBytes;
   pl->smem = pl->part_at + part + 1024;
   return true;
 }
@@ -125,7 +126,11 @@ bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, TcPlan* pl) 
   int ks = 1;
   if (cg == 1)
     while (ks < 8 && tiles * ks * 2 <= ctx->num_sms && chunks >= ks * 4) ks *= 2;
-  if (!fit(ctx, find_kind(fp4, cg, bn, gather), p.E, ks, pl)) return false;
+  // the parts of a split row take room from the ring: fewer, if it is short
+  while (!fit(ctx, find_kind(fp4, cg, bn, gather), p.E, ks, pl)) {
+    if (ks == 1) return false;
+    ks = 1;
+  }
   const int csize = cg == 2 ? 2 : ks;
   const int64_t most = ctx->max_clusters[log2_of(csize)];
   if (most < 1) return false;
@@ -187,14 +192,16 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
   t.p = p;
   t.stages = pl.stages;
   t.ks = pl.ks;
-  t.pair_stores = p.N % 2 == 0 && ((uintptr_t)p.out & 3u) == 0;
+  t.store_bytes = p.N % 8 == 0 && aligned16(p.out)                      ? 16
+                  : p.N % 2 == 0 && ((uintptr_t)p.out & 3u) == 0 ? 4
+                                                                 : 2;
   t.groups_at = pl.groups_at;
+  t.turn_at = pl.turn_at;
   t.part_at = pl.part_at;
   if (fp4) {
     const int64_t pitch = p.H / 16;
     const uintptr_t at = (uintptr_t)p.a_scale | (uintptr_t)p.b_scale | (uintptr_t)pitch;
-    t.scale_step = (at & 15u) == 0 ? 16 : (at & 3u) == 0 ? 4 : 1;
-    t.tma_scales = t.scale_step == 16;
+    t.scale_step = (at & 15u) == 0 ? 16 : (at & 3u) == 0 ? 4 : (at & 1u) == 0 ? 2 : 1;
   }
   CUtensorMap map_w, map_x, map_part, map_ws, map_xs;
   const TcKind* k = pl.kind;
@@ -209,7 +216,7 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
     return FARN_ERR_CUDA;
   }
   map_ws = map_xs = map_w;        // not read, unless
-  if (t.tma_scales && (!encode_scales(ctx, &map_ws, p.b_scale, p.H / 16, p.N) ||
+  if (fp4 && k->cg == 2 && t.scale_step == 16 && (!encode_scales(ctx, &map_ws, p.b_scale, p.H / 16, p.N) ||
                        !encode_scales(ctx, &map_xs, p.a_scale, p.H / 16, p.n_a)))
     return FARN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};

@@ -39,7 +39,7 @@ constexpr int kTcWarpsBf16 = 6;
 // kAux-th stage.  They may not be more than the ring has stages: a warp that
 // waits for a stage has to be within one round of the ring, or the parity of
 // the phase it waits for says nothing.
-constexpr int kTcAuxFp4 = 4;
+constexpr int kTcAuxFp4 = 4;        // 6 for pairs of CTAs
 constexpr int kTcAuxGather = 6;
 constexpr int kTcWarpsMost = kTcWarpsBf16 + kTcAuxGather;
 constexpr int kErrTcFull = 16;         // status bits: matrix warp waiting for operands,
@@ -51,10 +51,10 @@ struct TcParams {
   ProductParams p;
   int stages;
   int ks;            // CTAs of a cluster that split the row (CG = 1)
-  int pair_stores;   // N even and out 4-byte aligned
-  int tma_scales;    // NVFP4: rows of scales that TMA can read, else
-  int scale_step;    // bytes per load of scales that alignment allows
+  int store_bytes;   // 16, 4 or 2: what N and out allow a store of a row to be
+  int scale_step;    // NVFP4: 16, 4, 2 or 1: bytes of scales that alignment allows at a time
   uint32_t groups_at;  // shared-memory offsets
+  uint32_t turn_at;    // kTurnBytes for each epilogue warp
   uint32_t part_at;    // fp32 [BN][kPartPitch], for ks > 1
 };
 
@@ -72,10 +72,19 @@ struct TcBarriers {
 };
 
 constexpr int kPartPitch = kTcWeights + 4;
+// An epilogue warp's 16 pairs of slots by 32 weights, a word per pair; rows
+// of 36 words keep the 16-byte reads free of bank conflicts.
+constexpr int kTurnPitch = 36;
+constexpr int kTurnBytes = 16 * kTurnPitch * 4;
 
 template <bool FP4, int CG, int BN, bool GATHER>
 struct TcShape {
-  static constexpr int kAux = FP4 ? kTcAuxFp4 : GATHER ? kTcAuxGather : 0;
+  static constexpr int kAux = FP4 ? (CG == 2 ? 6 : kTcAuxFp4) : GATHER ? kTcAuxGather : 0;
+  // Block scales by TMA: 128 rows of 16 bytes cost it as much as an operand's
+  // 128 rows, but a warp that loads them waits longer (8192^3: 206 us against
+  // 236); one CTA per tile has the warps' time to spare (one token, 8192 x
+  // 8192: 15.5 us against 12.5).
+  static constexpr bool kTmaScales = FP4 && CG == 2;
   static constexpr int kWarps = kTcWarpsBf16 + kAux;
   static constexpr int kRows = BN / CG;                      // slots per CTA
   static constexpr int kBox = kRows % 32 == 0 ? 32 : 16;     // rows of a TMA box
@@ -85,7 +94,8 @@ struct TcShape {
   static constexpr int kScaleBytes = FP4 ? 2048 * (1 + kSlotBlocks) : 0;
   static constexpr int kStageBytes = kABytes + kBBytes + kScaleBytes;
   static constexpr int kScaleCols = FP4 ? 16 * (1 + kSlotBlocks) : 0;
-  static constexpr int kColsUsed = 2 * BN + kScaleCols;
+  // the epilogue reads 32 columns at a time
+  static constexpr int kColsUsed = (2 * BN + kScaleCols) < BN + 32 ? BN + 32 : 2 * BN + kScaleCols;
   static constexpr int kCols = kColsUsed <= 32 ? 32 : kColsUsed <= 64 ? 64
                                : kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
   static constexpr int kChunk = FP4 ? 256 : 64;              // elements of a row per stage
@@ -132,21 +142,108 @@ __device__ __forceinline__ bool tc_wait_warp(uint32_t bar, uint32_t parity,
   return __all_sync(0xFFFFFFFFu, tc_wait<JOIN>(bar, parity, abort_flag, err, code));
 }
 
-// 16 scale bytes of a row from `at`, of which `left` belong to the row; the
-// rest are 0.
-__device__ __forceinline__ uint4 load_scales16(const uint8_t* at, int64_t left, int step) {
-  if (step == 16 && left >= 16) return __ldg(reinterpret_cast<const uint4*>(at));
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-  if (step >= 4) {
+// Block scales in shared memory, as the tensor cores read them: 128 rows by
+// 16 bytes (256 elements) are four atoms of 512 bytes, one for each 64
+// elements; row r's four bytes of an atom are word r / 32 of its 16-byte
+// entry r % 32.
+__device__ __forceinline__ void put_scales(unsigned char* dst, const uint4* v, int lane) {
+  // v[r]: the 16 bytes of row lane + 32 r
+  uint4* at = reinterpret_cast<uint4*>(dst) + lane;
+  at[0] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+  at[32] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+  at[64] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+  at[96] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+}
+
+// The same from memory whose alignment allows loads of B bytes: 16 / B lanes
+// to a row, so that a load touches few lines.  `rows` and `left` (bytes of
+// the row from here on) bound what is read; the rest is 0.
+template <int B>
+__device__ __forceinline__ void copy_scale_block(unsigned char* dst, const uint8_t* src,
+                                                 int64_t pitch, int64_t rows, int64_t left,
+                                                 int lane) {
+  constexpr int kLanes = 16 / B, kRows = 32 / kLanes;
+  constexpr int kBatch = B == 1 ? 32 : 128 / kRows;
+  const int in = (lane % kLanes) * B, r0 = lane / kLanes;
+  for (int i0 = 0; i0 < 128 / kRows; i0 += kBatch) {
+    uint32_t v[kBatch];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (4 * i < left) w[i] = __ldg(reinterpret_cast<const uint32_t*>(at) + i);
-  } else {
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = (i0 + i) * kRows + r0;
+      v[i] = 0u;
+      if (r < rows && in < left) {
+        const uint8_t* at = src + r * pitch + in;
+        if constexpr (B == 4) v[i] = __ldg(reinterpret_cast<const uint32_t*>(at));
+        else if constexpr (B == 2) v[i] = __ldg(reinterpret_cast<const uint16_t*>(at));
+        else v[i] = __ldg(at);
+      }
+    }
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < left) w[i >> 2] |= (uint32_t)__ldg(at + i) << (8 * (i & 3));
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = (i0 + i) * kRows + r0;
+      unsigned char* to = dst + (in >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (in & 3);
+      if constexpr (B == 4) *reinterpret_cast<uint32_t*>(to) = v[i];
+      else if constexpr (B == 2) *reinterpret_cast<uint16_t*>(to) = (uint16_t)v[i];
+      else *to = (uint8_t)v[i];
+    }
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Up to 32 slots by the warp's 32 weights, from the accumulator's columns at
+// `tmem` to rows of the output.  The accumulator has a weight per lane; the
+// warp turns it over in shared memory, two slots to a word, and writes runs
+// of eight weights (about 110 instructions for 1024 values; one warp per
+// scheduler issues one in 4 to 5 cycles, so their number is the time).
+// n: slots; live: those whose row exists; first: the warp's first weight.
+template <bool GATHER>
+__device__ __forceinline__ void store_turned(const TcParams& t, uint32_t tmem, uint32_t* turn,
+                                             int64_t slot, int n, uint32_t live, int64_t first,
+                                             int lane) {
+  const ProductParams& p = t.p;
+  uint32_t v[32];
+  tc::tmem_ld32(tmem, v);
+  tc::tmem_ld_wait();
+  const float alpha = p.alpha;
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    turn[j * kTurnPitch + lane] = pack_bf16x2(__uint_as_float(v[2 * j]) * alpha,
+                                              __uint_as_float(v[2 * j + 1]) * alpha);
+  __syncwarp();
+  const int oct = lane & 3;
+  const int64_t col = first + oct * 8;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int pair = h * 8 + (lane >> 2);
+    const uint4 a = *reinterpret_cast<const uint4*>(turn + pair * kTurnPitch + oct * 8);
+    const uint4 b = *reinterpret_cast<const uint4*>(turn + pair * kTurnPitch + oct * 8 + 4);
+    uint4 w[2];
+    w[0] = make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                      __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
+    w[1] = make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                      __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int s = pair * 2 + i;
+      if (s >= n || col >= p.N) continue;
+      if (GATHER && !((live >> s) & 1u)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+      uint16_t* o = static_cast<uint16_t*>(p.out) + (slot + s) * p.N + col;
+      if (t.store_bytes == 16) {
+        *reinterpret_cast<uint4*>(o) = w[i];
+      } else {
+        const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (t.store_bytes == 4) {
+            if (col + 2 * k < p.N) reinterpret_cast<uint32_t*>(o)[k] = e[k];
+          } else {
+            if (col + 2 * k < p.N) o[2 * k] = (uint16_t)(e[k] & 0xFFFFu);
+            if (col + 2 * k + 1 < p.N) o[2 * k + 1] = (uint16_t)(e[k] >> 16);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
 }
 
 template <bool FP4, int CG, int BN, bool GATHER>
@@ -199,7 +296,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       tc::prefetch_map(&map_x);
       tc::prefetch_map(&map_part);
     }
-    if (FP4 && t.tma_scales) {
+    if (Sh::kTmaScales && t.scale_step == 16) {
       tc::prefetch_map(&map_ws);
       tc::prefetch_map(&map_xs);
     }
@@ -258,13 +355,19 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
               tc::load_2d<CG>(b + i * Sh::kBox * kTcRowBytes, &map_part, x, first + i * Sh::kBox,
                               bar);
           }
-          if (FP4 && t.tma_scales) {
+          if (Sh::kTmaScales && t.scale_step == 16) {
             const int blocks = w.n > 128 ? 2 : 1;
             const uint32_t sc = b + Sh::kBBytes, rbar = raw0 + 8 * s;
             mbar_arrive_expect_tx(rbar, 2048 * (1 + blocks));
             tc::load_2d<1>(sc, &map_ws, c * 16, n0, rbar);
-            tc::load_2d<1>(sc + 2048, &map_xs, c * 16, w.slot0, rbar);
-            if (blocks > 1) tc::load_2d<1>(sc + 4096, &map_xs, c * 16, w.slot0 + 128, rbar);
+            if constexpr (CG == 2) {
+              // both CTAs need all slots' scales: each loads one block for both
+              if (w_rank < blocks)
+                tc::load_2d_to(sc + 2048 * (1 + w_rank), &map_xs, c * 16,
+                               w.slot0 + 128 * w_rank, rbar, 3);
+            } else {
+              tc::load_2d<1>(sc + 2048, &map_xs, c * 16, w.slot0, rbar);
+            }
           }
         }
         __syncwarp();
@@ -339,6 +442,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     const uint32_t part_full = tc::smem_addr(&bb->part_full);
     const uint32_t part_empty = tc::smem_addr(&bb->part_empty);
     float* part = reinterpret_cast<float*>(smem + t.part_at);
+    uint32_t* turn = reinterpret_cast<uint32_t*>(smem + t.turn_at + warp * kTurnBytes);
     for (int64_t tile = t0; ok && tile < tiles; tile += tstep, ++nt) {
       const Tile w = find_tile(g, p.E, tile, wts, BN);
       const uint32_t acc = nt & 1, d = tmem + acc * BN + ((uint32_t)warp << 21);
@@ -360,41 +464,14 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
             part[(c + j) * kPartPitch + warp * 32 + lane] = __uint_as_float(v[j]);
         }
       } else {
-        const int64_t n = n0 + warp * 32 + lane;
-        for (int c = 0; c < w.n; c += 16) {
-          uint32_t v[16];
-          tc::tmem_ld16(d + c, v);
-          uint32_t live = 0xFFFFu;
+        for (int c = 0; c < w.n; c += 32) {
+          uint32_t live = 0xFFFFFFFFu;
           if constexpr (GATHER) {
-            const int64_t s = (int64_t)w.slot0 + c + lane;
-            const int r = lane < 16 && c + lane < w.n ? p.rows[s] : -1;
+            const int r = c + lane < w.n ? p.rows[(int64_t)w.slot0 + c + lane] : -1;
             live = __ballot_sync(0xFFFFFFFFu, r >= 0 && r < p.n_a);
           }
-          tc::tmem_ld_wait();
-          if (t.pair_stores) {
-            // lanes 2i and 2i + 1 exchange halves: the even one stores slots
-            // 0..7 of both weights, the odd one slots 8..15
-            const bool odd = lane & 1;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float keep = __uint_as_float(odd ? v[j + 8] : v[j]);
-              const float send = __uint_as_float(odd ? v[j] : v[j + 8]);
-              const float got = __shfl_xor_sync(0xFFFFFFFFu, send, 1);
-              const int jj = j + (odd ? 8 : 0);
-              uint32_t word = pack_bf16x2((odd ? got : keep) * p.alpha,
-                                          (odd ? keep : got) * p.alpha);
-              if (!((live >> jj) & 1u)) word = 0u;
-              if (c + jj < w.n && n < p.N)
-                *reinterpret_cast<uint32_t*>(
-                    out + ((int64_t)w.slot0 + c + jj) * p.N + (n & ~(int64_t)1)) = word;
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c + j < w.n && n < p.N)
-                out[((int64_t)w.slot0 + c + j) * p.N + n] =
-                    (live >> j) & 1u ? to_bf16(__uint_as_float(v[j]) * p.alpha) : (uint16_t)0;
-          }
+          store_turned<GATHER>(t, d + c, turn, (int64_t)w.slot0 + c, w.n - c, live,
+                               n0 + warp * 32, lane);
         }
       }
       tc::fence_before();
@@ -421,10 +498,10 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     }
   } else if constexpr (FP4) {
     // ------------------------------------------------------- block scales
-    // Warp i takes every fourth stage.  A lane reads 16 bytes (256 elements)
-    // of rows lane, +32, +64 and +96 of a block of 128 and writes them
-    // transposed: word r of the lane's 16 bytes of atom k is row lane + 32 r's
-    // four scales of the k-th 64 elements.
+    // A warp takes every kAux-th stage and brings its scales into the layout
+    // above: where their rows are whole 16-byte pieces, from shared memory
+    // (TMA put them there, in place) or 16 bytes per lane, else in smaller
+    // pieces.
     const int mine = warp - 6;
     const int64_t pitch = p.H / 16;
     RingPos at;
@@ -439,44 +516,50 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       for (; c < c1; c += Sh::kAux, at.skip(Sh::kAux, NS)) {
         const uint32_t s = at.stage;
         const int64_t left = pitch - (int64_t)c * 16;
-        uint4 v[1 + Sh::kSlotBlocks][4];
         unsigned char* dst = smem + s * Sh::kStageBytes + Sh::kABytes + Sh::kBBytes;
-        if (t.tma_scales) {
-          ok = tc_wait_warp(raw0 + 8 * s, at.phase, abort_flag, p.err, kErrTcFull);
-          if (!ok) break;
+        const uint8_t* src[2] = {p.b_scale + n0 * pitch + (int64_t)c * 16,
+                                 p.a_scale + (int64_t)w.slot0 * pitch + (int64_t)c * 16};
+        if (t.scale_step == 16) {
+          uint4 v[1 + Sh::kSlotBlocks][4];
+          if constexpr (Sh::kTmaScales) {
+            ok = tc_wait_warp(raw0 + 8 * s, at.phase, abort_flag, p.err, kErrTcFull);
+            if (!ok) break;
 #pragma unroll
-          for (int u = 0; u <= Sh::kSlotBlocks; ++u) {
-            if (u > blocks) break;
+            for (int u = 0; u <= Sh::kSlotBlocks; ++u)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              v[u][r] = reinterpret_cast<const uint4*>(dst + u * 2048)[r * 32 + lane];
+              for (int r = 0; r < 4; ++r)
+                if (u <= blocks)
+                  v[u][r] = reinterpret_cast<const uint4*>(dst + u * 2048)[r * 32 + lane];
+            __syncwarp();       // in place: all of it is read before any is written
+          } else {
+#pragma unroll
+            for (int u = 0; u <= Sh::kSlotBlocks; ++u)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int in = (u ? (u - 1) * 128 : 0) + r * 32 + lane;
+                v[u][r] = make_uint4(0u, 0u, 0u, 0u);
+                if (u ? in < w.n : n0 + in < p.N)
+                  v[u][r] = __ldg(reinterpret_cast<const uint4*>(src[u > 0] + in * pitch));
+              }
+            ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
+            if (!ok) break;
           }
-          __syncwarp();       // in place: all of it is read before any is written
+#pragma unroll
+          for (int u = 0; u <= Sh::kSlotBlocks; ++u)
+            if (u <= blocks) put_scales(dst + u * 2048, v[u], lane);
         } else {
-#pragma unroll
-        for (int u = 0; u <= Sh::kSlotBlocks; ++u) {
-          if (u > blocks) break;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int in = (u ? (u - 1) * 128 : 0) + r * 32 + lane;
-            const bool have = u ? in < w.n : n0 + in < p.N;
-            const int64_t row = u ? (int64_t)w.slot0 + in : (int64_t)w.e * p.N + n0 + in;
-            v[u][r] = have ? load_scales16((u ? p.a_scale : p.b_scale) + row * pitch + c * 16,
-                                           left, t.scale_step)
-                           : make_uint4(0u, 0u, 0u, 0u);
+          ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
+          if (!ok) break;
+          for (int u = 0; u <= blocks; ++u) {
+            const int64_t rows = u ? w.n - (u - 1) * 128 : p.N - n0;
+            const uint8_t* from = src[u > 0] + (u ? (u - 1) * 128 * pitch : 0);
+            if (t.scale_step == 4)
+              copy_scale_block<4>(dst + u * 2048, from, pitch, rows, left, lane);
+            else if (t.scale_step == 2)
+              copy_scale_block<2>(dst + u * 2048, from, pitch, rows, left, lane);
+            else
+              copy_scale_block<1>(dst + u * 2048, from, pitch, rows, left, lane);
           }
-        }
-        ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
-        if (!ok) break;
-        }
-#pragma unroll
-        for (int u = 0; u <= Sh::kSlotBlocks; ++u) {
-          if (u > blocks) break;
-          uint4* at = reinterpret_cast<uint4*>(dst + u * 2048) + lane;
-          at[0] = make_uint4(v[u][0].x, v[u][1].x, v[u][2].x, v[u][3].x);
-          at[32] = make_uint4(v[u][0].y, v[u][1].y, v[u][2].y, v[u][3].y);
-          at[64] = make_uint4(v[u][0].z, v[u][1].z, v[u][2].z, v[u][3].z);
-          at[96] = make_uint4(v[u][0].w, v[u][1].w, v[u][2].w, v[u][3].w);
         }
         tc::fence_async_shared();
         __syncwarp();
