@@ -578,34 +578,65 @@ def moe_combine(expert_out, index, gates, residual, weight, eps: float, out=None
                                stream)()
 
 
-def prepare_moe_route(logits, top_k: int, renormalize: bool = True, out=None, ctx=None,
-                      stream=None):
-    """``moe_route`` checked and marshalled once."""
+# The calls below check their tensors on a short path (a serving step makes
+# several of them per layer, and their kernels take a few microseconds); a
+# tensor that it turns down goes through _check_tensor for the message.
+def _raw_stream(stream, index):
+    if stream is not None:
+        return stream.cuda_stream
     import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _fits(t, dtype, index, shape):
+    return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()
+
+
+def _call(fn, args, name):
+    st = fn(*args)
+    if st != FARN_OK:
+        raise FarnError(st, name)
+
+
+def _moe_route_args(logits, top_k, renormalize, out, ctx, stream):
+    import torch
+    i32, f32 = torch.int32, torch.float32
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     T, E = logits.shape
-    dev, K = logits.device, int(top_k)
-    _check_tensor(logits, "logits", (T, E), dev, (torch.bfloat16, torch.float32))
+    K, index = int(top_k), logits.get_device()
+    if index < 0 or not logits.is_contiguous() or logits.dtype not in (torch.bfloat16, f32):
+        _check_tensor(logits, "logits", (T, E), logits.device, (torch.bfloat16, f32))
     if not 1 <= E <= FARN_MAX_EXPERTS:
         raise ValueError(f"the number of experts must be 1..{FARN_MAX_EXPERTS}, got {E}")
     if not 1 <= K <= min(E, FARN_MAX_W):
         raise ValueError(f"top_k must be 1..{min(E, FARN_MAX_W)}, got {K}")
-    i32, f32 = (torch.int32,), (torch.float32,)
     if out is None:
-        out = tuple(torch.empty(shape, dtype=dt[0], device=dev) for shape, dt in
-                    (((T, K), i32), ((T, K), f32), ((T, K), i32), ((T * K,), i32),
-                     ((E + 1,), i32)))
+        dev = logits.device
+        out = (torch.empty((T, K), dtype=i32, device=dev),
+               torch.empty((T, K), dtype=f32, device=dev),
+               torch.empty((T, K), dtype=i32, device=dev),
+               torch.empty((T * K,), dtype=i32, device=dev),
+               torch.empty((E + 1,), dtype=i32, device=dev))
     else:
+        out = tuple(out)
+        if len(out) != 5:
+            raise ValueError("out must be (experts, gates, index, rows, offsets)")
         for name, t, shape, dt in zip(("experts", "gates", "index", "rows", "offsets"), out,
                                       ((T, K), (T, K), (T, K), (T * K,), (E + 1,)),
                                       (i32, f32, i32, i32, i32)):
-            _check_tensor(t, name, shape, dev, dt)
-    c, s = _ctx_stream(ctx, stream, dev)
-    args = (ctypes.c_void_p(c.handle), _vp(logits),
-            FARN_F32 if logits.dtype == torch.float32 else FARN_BF16, T, E, K,
-            1 if renormalize else 0) + tuple(_vp(t) for t in out) + (s,)
-    return PreparedCall(_load().farn_moe_route, args, "farn_moe_route", tuple(out), (logits, c))
+            _check_tensor(t, name, shape, logits.device, (dt,))
+    c = ctx if ctx is not None else _context_for(index)
+    return (c.handle, logits.data_ptr(), FARN_F32 if logits.dtype is f32 else FARN_BF16, T, E, K,
+            1 if renormalize else 0, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
+            out[3].data_ptr(), out[4].data_ptr(), _raw_stream(stream, index)), out, c
+
+
+def prepare_moe_route(logits, top_k: int, renormalize: bool = True, out=None, ctx=None,
+                      stream=None):
+    """``moe_route`` checked and marshalled once."""
+    args, out, c = _moe_route_args(logits, top_k, renormalize, out, ctx, stream)
+    return PreparedCall(_load().farn_moe_route, args, "farn_moe_route", out, (logits, c))
 
 
 def moe_route(logits, top_k: int, renormalize: bool = True, out=None, ctx=None, stream=None):
@@ -614,31 +645,44 @@ def moe_route(logits, top_k: int, renormalize: bool = True, out=None, ctx=None, 
     [T*K], offsets int32 [E+1]): rows and offsets are ``grouped_matmul``'s,
     index and gates ``moe_combine``'s.  An expert masked with -inf is never
     chosen; a pair without an expert has expert -1, gate 0 and index -1."""
-    return prepare_moe_route(logits, top_k, renormalize, out, ctx, stream)()
+    args, out, _ = _moe_route_args(logits, top_k, renormalize, out, ctx, stream)
+    _call(_load().farn_moe_route, args, "farn_moe_route")
+    return out
+
+
+def _grouped_args(x, weights, offsets, rows, out, ctx, stream):
+    import torch
+    bf, i32 = torch.bfloat16, torch.int32
+    if x.dim() != 2 or weights.dim() != 3:
+        raise ValueError("x must be [rows, H] and weights [E, N, H]")
+    n_rows, H = x.shape
+    E, N, HW = weights.shape
+    index = x.get_device()
+    if (index < 0 or HW != H or x.dtype is not bf or not x.is_contiguous() or
+            not _fits(weights, bf, index, (E, N, H)) or
+            not _fits(offsets, i32, index, (E + 1,))):
+        dev = x.device
+        _check_tensor(x, "x", (n_rows, H), dev)
+        _check_tensor(weights, "weights", (E, N, H), dev)
+        _check_tensor(offsets, "offsets", (E + 1,), dev, (i32,))
+    S = n_rows
+    if rows is not None:
+        S = rows.shape[0] if rows.dim() == 1 else -1
+        if not _fits(rows, i32, index, (S,)):
+            _check_tensor(rows, "rows", (S,), x.device, (i32,))
+    if out is None:
+        out = torch.empty((S, N), dtype=bf, device=x.device)
+    elif not _fits(out, bf, index, (S, N)):
+        _check_tensor(out, "out", (S, N), x.device)
+    c = ctx if ctx is not None else _context_for(index)
+    return (c.handle, x.data_ptr(), n_rows, None if rows is None else rows.data_ptr(), S,
+            weights.data_ptr(), E, offsets.data_ptr(), N, H, out.data_ptr(),
+            _raw_stream(stream, index)), out, c
 
 
 def prepare_grouped_matmul(x, weights, offsets, rows=None, out=None, ctx=None, stream=None):
     """``grouped_matmul`` checked and marshalled once."""
-    import torch
-    if x.dim() != 2 or weights.dim() != 3:
-        raise ValueError("x must be [rows, H] and weights [E, N, H]")
-    n_rows, H = x.shape
-    E, N, _ = weights.shape
-    dev = x.device
-    _check_tensor(x, "x", (n_rows, H), dev)
-    _check_tensor(weights, "weights", (E, N, H), dev)
-    _check_tensor(offsets, "offsets", (E + 1,), dev, (torch.int32,))
-    S = n_rows
-    if rows is not None:
-        S = rows.shape[0] if rows.dim() == 1 else -1
-        _check_tensor(rows, "rows", (S,), dev, (torch.int32,))
-    if out is None:
-        out = torch.empty((S, N), dtype=torch.bfloat16, device=dev)
-    else:
-        _check_tensor(out, "out", (S, N), dev)
-    c, s = _ctx_stream(ctx, stream, dev)
-    args = (ctypes.c_void_p(c.handle), _vp(x), n_rows, _vp(rows), S, _vp(weights), E,
-            _vp(offsets), N, H, _vp(out), s)
+    args, out, c = _grouped_args(x, weights, offsets, rows, out, ctx, stream)
     return PreparedCall(_load().farn_grouped_matmul, args, "farn_grouped_matmul", out,
                         (x, weights, offsets, rows, c))
 
@@ -649,90 +693,119 @@ def grouped_matmul(x, weights, offsets, rows=None, out=None, ctx=None, stream=No
     offsets[e+1]-1), rows int32 [S] (the row of x that a slot reads; None:
     slot s reads row s).  Returns out bf16 [S,N], ``moe_combine``'s
     expert_out; slots that no expert has are left as they were."""
-    return prepare_grouped_matmul(x, weights, offsets, rows, out, ctx, stream)()
+    args, out, _ = _grouped_args(x, weights, offsets, rows, out, ctx, stream)
+    _call(_load().farn_grouped_matmul, args, "farn_grouped_matmul")
+    return out
 
 
 def _nvfp4_shape(codes, scales, name):
     import torch
     if codes.dim() != 2:
         raise ValueError(f"{name} must be [rows, H/2]")
-    T, H = codes.shape[0], codes.shape[1] * 2
+    T, half = codes.shape
+    H = half * 2
     if H % 16:
         raise ValueError(f"NVFP4 needs H % 16 == 0, got H = {H}")
-    _check_tensor(codes, name, (T, H // 2), codes.device, (torch.uint8,))
-    _check_tensor(scales, name + " scales", (T, H // 16), codes.device, (torch.uint8,))
-    return T, H
+    u8, index = torch.uint8, codes.get_device()
+    if (index < 0 or codes.dtype is not u8 or not codes.is_contiguous() or
+            not _fits(scales, u8, index, (T, H // 16))):
+        _check_tensor(codes, name, (T, half), codes.device, (u8,))
+        _check_tensor(scales, name + " scales", (T, H // 16), codes.device, (u8,))
+    return T, H, index
+
+
+def _quantize_args(x, tensor_scale, out, ctx, stream):
+    import torch
+    u8 = torch.uint8
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    index = x.get_device()
+    if index < 0 or x.dtype is not torch.bfloat16 or not x.is_contiguous():
+        _check_tensor(x, "x", (T, H), x.device)
+    if H % 16:
+        raise ValueError(f"NVFP4 needs H % 16 == 0, got H = {H}")
+    if out is None:
+        dev = x.device
+        out = (torch.empty((T, H // 2), dtype=u8, device=dev),
+               torch.empty((T, H // 16), dtype=u8, device=dev))
+    else:
+        out = tuple(out)
+        if len(out) != 2:
+            raise ValueError("out must be (codes, scales)")
+        _check_tensor(out[0], "codes", (T, H // 2), x.device, (u8,))
+        _check_tensor(out[1], "scales", (T, H // 16), x.device, (u8,))
+    c = ctx if ctx is not None else _context_for(index)
+    return (c.handle, x.data_ptr(), T, H, tensor_scale, out[0].data_ptr(), out[1].data_ptr(),
+            _raw_stream(stream, index)), out, c
 
 
 def prepare_nvfp4_quantize(x, tensor_scale: float, out=None, ctx=None, stream=None):
     """``nvfp4_quantize`` checked and marshalled once."""
-    import torch
-    if x.dim() != 2:
-        raise ValueError("x must be [T, H]")
-    T, H = x.shape
-    dev = x.device
-    _check_tensor(x, "x", (T, H), dev)
-    if H % 16:
-        raise ValueError(f"NVFP4 needs H % 16 == 0, got H = {H}")
-    if out is None:
-        out = (torch.empty((T, H // 2), dtype=torch.uint8, device=dev),
-               torch.empty((T, H // 16), dtype=torch.uint8, device=dev))
-    else:
-        _check_tensor(out[0], "codes", (T, H // 2), dev, (torch.uint8,))
-        _check_tensor(out[1], "scales", (T, H // 16), dev, (torch.uint8,))
-    c, s = _ctx_stream(ctx, stream, dev)
-    args = (ctypes.c_void_p(c.handle), _vp(x), T, H, tensor_scale, _vp(out[0]), _vp(out[1]), s)
-    return PreparedCall(_load().farn_nvfp4_quantize, args, "farn_nvfp4_quantize", tuple(out),
-                        (x, c))
+    args, out, c = _quantize_args(x, tensor_scale, out, ctx, stream)
+    return PreparedCall(_load().farn_nvfp4_quantize, args, "farn_nvfp4_quantize", out, (x, c))
 
 
 def nvfp4_quantize(x, tensor_scale: float, out=None, ctx=None, stream=None):
     """NVFP4 codes of a bf16 tensor [T,H], in ``forward_nvfp4``'s format.
     Returns (codes uint8 [T,H/2], block_scale uint8 [T,H/16]); H must be a
     multiple of 16."""
-    return prepare_nvfp4_quantize(x, tensor_scale, out, ctx, stream)()
+    args, out, _ = _quantize_args(x, tensor_scale, out, ctx, stream)
+    _call(_load().farn_nvfp4_quantize, args, "farn_nvfp4_quantize")
+    return out
+
+
+def _dequantize_args(codes, block_scale, tensor_scale, out, ctx, stream):
+    import torch
+    T, H, index = _nvfp4_shape(codes, block_scale, "codes")
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=codes.device)
+    elif not _fits(out, torch.bfloat16, index, (T, H)):
+        _check_tensor(out, "out", (T, H), codes.device)
+    c = ctx if ctx is not None else _context_for(index)
+    return (c.handle, codes.data_ptr(), block_scale.data_ptr(), T, H, tensor_scale,
+            out.data_ptr(), _raw_stream(stream, index)), out, c
 
 
 def prepare_nvfp4_dequantize(codes, block_scale, tensor_scale: float, out=None, ctx=None,
                              stream=None):
     """``nvfp4_dequantize`` checked and marshalled once."""
-    import torch
-    T, H = _nvfp4_shape(codes, block_scale, "codes")
-    dev = codes.device
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    else:
-        _check_tensor(out, "out", (T, H), dev)
-    c, s = _ctx_stream(ctx, stream, dev)
-    args = (ctypes.c_void_p(c.handle), _vp(codes), _vp(block_scale), T, H, tensor_scale,
-            _vp(out), s)
+    args, out, c = _dequantize_args(codes, block_scale, tensor_scale, out, ctx, stream)
     return PreparedCall(_load().farn_nvfp4_dequantize, args, "farn_nvfp4_dequantize", out,
                         (codes, block_scale, c))
 
 
 def nvfp4_dequantize(codes, block_scale, tensor_scale: float, out=None, ctx=None, stream=None):
     """The values of NVFP4 codes and block scales, as a bf16 tensor [T,H]."""
-    return prepare_nvfp4_dequantize(codes, block_scale, tensor_scale, out, ctx, stream)()
+    args, out, _ = _dequantize_args(codes, block_scale, tensor_scale, out, ctx, stream)
+    _call(_load().farn_nvfp4_dequantize, args, "farn_nvfp4_dequantize")
+    return out
+
+
+def _nvfp4_matmul_args(a_codes, a_scale, a_tensor_scale, b_codes, b_scale, b_tensor_scale, out,
+                       ctx, stream):
+    import torch
+    T, H, index = _nvfp4_shape(a_codes, a_scale, "a_codes")
+    N, HB, index_b = _nvfp4_shape(b_codes, b_scale, "b_codes")
+    if HB != H:
+        raise ValueError(f"a and b must have the same H, got {H} and {HB}")
+    if index_b != index:
+        raise ValueError(f"b_codes must be on {a_codes.device}, got {b_codes.device}")
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=a_codes.device)
+    elif not _fits(out, torch.bfloat16, index, (T, N)):
+        _check_tensor(out, "out", (T, N), a_codes.device)
+    c = ctx if ctx is not None else _context_for(index)
+    return (c.handle, a_codes.data_ptr(), a_scale.data_ptr(), a_tensor_scale,
+            b_codes.data_ptr(), b_scale.data_ptr(), b_tensor_scale, T, N, H, out.data_ptr(),
+            _raw_stream(stream, index)), out, c
 
 
 def prepare_nvfp4_matmul(a_codes, a_scale, a_tensor_scale: float, b_codes, b_scale,
                          b_tensor_scale: float, out=None, ctx=None, stream=None):
     """``nvfp4_matmul`` checked and marshalled once."""
-    import torch
-    T, H = _nvfp4_shape(a_codes, a_scale, "a_codes")
-    N, HB = _nvfp4_shape(b_codes, b_scale, "b_codes")
-    dev = a_codes.device
-    if HB != H:
-        raise ValueError(f"a and b must have the same H, got {H} and {HB}")
-    if b_codes.device != dev:
-        raise ValueError(f"b_codes must be on {dev}, got {b_codes.device}")
-    if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
-    else:
-        _check_tensor(out, "out", (T, N), dev)
-    c, s = _ctx_stream(ctx, stream, dev)
-    args = (ctypes.c_void_p(c.handle), _vp(a_codes), _vp(a_scale), a_tensor_scale, _vp(b_codes),
-            _vp(b_scale), b_tensor_scale, T, N, H, _vp(out), s)
+    args, out, c = _nvfp4_matmul_args(a_codes, a_scale, a_tensor_scale, b_codes, b_scale,
+                                      b_tensor_scale, out, ctx, stream)
     return PreparedCall(_load().farn_nvfp4_matmul, args, "farn_nvfp4_matmul", out,
                         (a_codes, a_scale, b_codes, b_scale, c))
 
@@ -741,5 +814,7 @@ def nvfp4_matmul(a_codes, a_scale, a_tensor_scale: float, b_codes, b_scale,
                  b_tensor_scale: float, out=None, ctx=None, stream=None):
     """The product of two NVFP4 tensors, a [T,H] and b [N,H] (as
     ``forward_nvfp4`` and ``nvfp4_quantize`` give them), in bf16 [T,N]."""
-    return prepare_nvfp4_matmul(a_codes, a_scale, a_tensor_scale, b_codes, b_scale,
-                                b_tensor_scale, out, ctx, stream)()
+    args, out, _ = _nvfp4_matmul_args(a_codes, a_scale, a_tensor_scale, b_codes, b_scale,
+                                      b_tensor_scale, out, ctx, stream)
+    _call(_load().farn_nvfp4_matmul, args, "farn_nvfp4_matmul")
+    return out
