@@ -504,10 +504,10 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     // pieces.
     const int mine = warp - 6;
     const int64_t pitch = p.H / 16;
+    bool ok = true;
     RingPos at;
     at.skip(mine, NS);
     int ahead = mine;          // stages until this warp's next
-    bool ok = true;
     for (int64_t tile = t0; ok && tile < tiles; tile += tstep) {
       const Tile w = find_tile(g, p.E, tile, wts, BN);
       const int64_t n0 = (int64_t)w.wt * kTileWeights + w_rank * kTcWeights;
@@ -517,8 +517,6 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         const uint32_t s = at.stage;
         const int64_t left = pitch - (int64_t)c * 16;
         unsigned char* dst = smem + s * Sh::kStageBytes + Sh::kABytes + Sh::kBBytes;
-        const uint8_t* src[2] = {p.b_scale + n0 * pitch + (int64_t)c * 16,
-                                 p.a_scale + (int64_t)w.slot0 * pitch + (int64_t)c * 16};
         if (t.scale_step == 16) {
           uint4 v[1 + Sh::kSlotBlocks][4];
           if constexpr (Sh::kTmaScales) {
@@ -536,10 +534,12 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
             for (int u = 0; u <= Sh::kSlotBlocks; ++u)
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                const int in = (u ? (u - 1) * 128 : 0) + r * 32 + lane;
+                const int64_t in = r * 32 + lane;
                 v[u][r] = make_uint4(0u, 0u, 0u, 0u);
                 if (u ? in < w.n : n0 + in < p.N)
-                  v[u][r] = __ldg(reinterpret_cast<const uint4*>(src[u > 0] + in * pitch));
+                  v[u][r] = __ldg(reinterpret_cast<const uint4*>(
+                      (u ? p.a_scale + (w.slot0 + in) * pitch : p.b_scale + (n0 + in) * pitch) +
+                      (int64_t)c * 16));
               }
             ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
             if (!ok) break;
@@ -552,7 +552,9 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
           if (!ok) break;
           for (int u = 0; u <= blocks; ++u) {
             const int64_t rows = u ? w.n - (u - 1) * 128 : p.N - n0;
-            const uint8_t* from = src[u > 0] + (u ? (u - 1) * 128 * pitch : 0);
+            const uint8_t* from =
+                (u ? p.a_scale + ((int64_t)w.slot0 + (u - 1) * 128) * pitch
+                   : p.b_scale + n0 * pitch) + (int64_t)c * 16;
             if (t.scale_step == 4)
               copy_scale_block<4>(dst + u * 2048, from, pitch, rows, left, lane);
             else if (t.scale_step == 2)
