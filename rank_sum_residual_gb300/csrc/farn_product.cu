@@ -55,14 +55,14 @@ struct TcKind {
   bool fp4, gather;
   int cg, bn;
   TcKernel kernel;
-  int warps, stage_bytes, rows, box;
+  int warps, stage_bytes, scale_bytes, rows, box;
 };
 
 template <bool FP4, int CG, int BN, bool GATHER>
 TcKind kind() {
   using Sh = farn::TcShape<FP4, CG, BN, GATHER>;
   return TcKind{FP4, GATHER, CG, BN, &farn::farn_product_tc_kernel<FP4, CG, BN, GATHER>,
-                Sh::kWarps, Sh::kStageBytes, Sh::kRows, Sh::kBox};
+                Sh::kWarps, Sh::kStageBytes, 2 * Sh::kScaleSlot, Sh::kRows, Sh::kBox};
 }
 
 const TcKind kKinds[] = {
@@ -83,26 +83,28 @@ struct TcPlan {
   const TcKind* kind;
   int ks, stages;
   unsigned grid;
-  uint32_t groups_at, turn_at, part_at, smem;
+  uint32_t scales_at, barriers_at, groups_at, part_at, smem;
 };
 
 // Shared memory of a call: the ring, the barriers, the groups, and the
 // parts that the CTAs of a split row exchange; then 1 KB to align the ring.
 bool fit(const farn_ctx* ctx, const TcKind* k, int E, int ks, TcPlan* pl) {
-  const uint32_t part = ks > 1 ? (uint32_t)k->bn * farn::kPartPitch * 4 : 0;
-  const uint32_t fixed =
-      1024 + ((uint32_t)sizeof(farn::TcBarriers) + 15u) / 16 * 16 +
-      (farn::groups_bytes(E) + 15u) / 16 * 16 + 4 * farn::kTurnBytes + part;
+  // the epilogue turns accumulators over, or exchanges parts of a split row
+  const uint32_t part =
+      ks > 1 ? (uint32_t)k->bn * farn::kPartPitch * 4 : 4 * (uint32_t)farn::kTurnBytes;
+  const uint32_t barriers = ((uint32_t)sizeof(farn::TcBarriers) + 15u) / 16 * 16;
+  const uint32_t groups = (farn::groups_bytes(E) + 15u) / 16 * 16;
+  const uint32_t fixed = 1024 + k->scale_bytes + barriers + groups + part;
   int stages = ((int)ctx->max_smem - (int)fixed) / k->stage_bytes;
   if (stages > farn::kTcMaxStages) stages = farn::kTcMaxStages;
-  if (stages < 2 || stages < k->warps - farn::kTcWarpsBf16) return false;
+  if (stages < 2 || (k->gather && stages < farn::kTcAuxGather)) return false;
   pl->kind = k;
   pl->ks = ks;
   pl->stages = stages;
-  pl->groups_at = (uint32_t)stages * k->stage_bytes +
-                  ((uint32_t)sizeof(farn::TcBarriers) + 15u) / 16 * 16;
-  pl->turn_at = pl->groups_at + (farn::groups_bytes(E) + 15u) / 16 * 16;
-  pl->part_at = pl->turn_at + 4 * farn::kTurnBytes;
+  pl->scales_at = (uint32_t)stages * k->stage_bytes;
+  pl->barriers_at = pl->scales_at + k->scale_bytes;
+  pl->groups_at = pl->barriers_at + barriers;
+  pl->part_at = pl->groups_at + groups;
   pl->smem = pl->part_at + part + 1024;
   return true;
 }
@@ -162,16 +164,17 @@ bool encode(const farn_ctx* ctx, CUtensorMap* map, bool fp4, const void* base, i
          CUDA_SUCCESS;
 }
 
-// Block scales: 16 bytes (256 elements) of 128 rows, as they lie.
+// Block scales: 64 bytes (1024 elements) of 128 rows, written with the
+// 64-byte swizzle.
 bool encode_scales(const farn_ctx* ctx, CUtensorMap* map, const void* base, int64_t pitch,
                    int64_t rows) {
   const cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)pitch};
-  const cuuint32_t boxes[2] = {16u, 128u};
+  const cuuint32_t boxes[2] = {64u, 128u};
   const cuuint32_t steps[2] = {1u, 1u};
   return ((EncodeTiled)ctx->encode_tiled)(
              map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, boxes,
-             steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
@@ -196,7 +199,8 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
                   : p.N % 2 == 0 && ((uintptr_t)p.out & 3u) == 0 ? 4
                                                                  : 2;
   t.groups_at = pl.groups_at;
-  t.turn_at = pl.turn_at;
+  t.scales_at = pl.scales_at;
+  t.barriers_at = pl.barriers_at;
   t.part_at = pl.part_at;
   if (fp4) {
     const int64_t pitch = p.H / 16;
@@ -216,7 +220,7 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
     return FARN_ERR_CUDA;
   }
   map_ws = map_xs = map_w;        // not read, unless
-  if (fp4 && k->cg == 2 && t.scale_step == 16 && (!encode_scales(ctx, &map_ws, p.b_scale, p.H / 16, p.N) ||
+  if (fp4 && t.scale_step == 16 && (!encode_scales(ctx, &map_ws, p.b_scale, p.H / 16, p.N) ||
                        !encode_scales(ctx, &map_xs, p.a_scale, p.H / 16, p.n_a)))
     return FARN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};

@@ -35,12 +35,16 @@ constexpr int kTcMaxStages = 12;
 constexpr int kTcRowBytes = 128;       // bytes of a row per stage: one swizzle span
 constexpr int kTcWeights = 128;        // weights per CTA and tile
 constexpr int kTcWarpsBf16 = 6;
-// Further warps for block scales, or for gathered rows.  Each takes every
-// kAux-th stage.  They may not be more than the ring has stages: a warp that
-// waits for a stage has to be within one round of the ring, or the parity of
-// the phase it waits for says nothing.
-constexpr int kTcAuxFp4 = 4;        // 6 for pairs of CTAs
+// Further warps for gathered rows.  Each takes every sixth stage.  They may
+// not be more than the ring has stages: a warp that waits for a stage has to
+// be within one round of the ring, or the parity of the phase it waits for
+// says nothing.
 constexpr int kTcAuxGather = 6;
+// NVFP4: block scales come for four stages at a time (64 bytes of a row), in
+// blocks of 128 rows (one of weights, the others of slots) that lie in a ring
+// of two slots of their own; two further warps to a block.
+constexpr int kTcScaleStages = 4;
+constexpr int kTcScaleBlock = 128 * 64;
 constexpr int kTcWarpsMost = kTcWarpsBf16 + kTcAuxGather;
 constexpr int kErrTcFull = 16;         // status bits: matrix warp waiting for operands,
 constexpr int kErrTcEmpty = 32;        // producers waiting for a free stage,
@@ -52,15 +56,20 @@ struct TcParams {
   int stages;
   int ks;            // CTAs of a cluster that split the row (CG = 1)
   int store_bytes;   // 16, 4 or 2: what N and out allow a store of a row to be
-  int scale_step;    // NVFP4: 16, 4, 2 or 1: bytes of scales that alignment allows at a time
+  int scale_step;    // NVFP4: bytes of scales that alignment allows at a time: 16 (by TMA),
+                     // 4, 2 or 1
   uint32_t groups_at;  // shared-memory offsets
-  uint32_t turn_at;    // kTurnBytes for each epilogue warp
-  uint32_t part_at;    // fp32 [BN][kPartPitch], for ks > 1
+  uint32_t scales_at;  // NVFP4: two slots of block scales
+  uint32_t barriers_at;
+  uint32_t part_at;    // fp32 [BN][kPartPitch] for ks > 1, else kTurnBytes for each
+                       // epilogue warp
 };
 
 struct TcBarriers {
   uint64_t full[kTcMaxStages];
-  uint64_t raw[kTcMaxStages];      // block scales as they lie in memory
+  uint64_t scale_raw[2][3];        // a block of scales has landed, as it lies in memory
+  uint64_t scale_full[2];          // the slot's scales are as the tensor cores read them
+  uint64_t scale_empty[2];
   uint64_t empty[kTcMaxStages];
   uint64_t tile_full[2];
   uint64_t tile_empty[2];
@@ -79,20 +88,15 @@ constexpr int kTurnBytes = 16 * kTurnPitch * 4;
 
 template <bool FP4, int CG, int BN, bool GATHER>
 struct TcShape {
-  static constexpr int kAux = FP4 ? (CG == 2 ? 6 : kTcAuxFp4) : GATHER ? kTcAuxGather : 0;
-  // Block scales by TMA: 128 rows of 16 bytes cost it as much as an operand's
-  // 128 rows, but a warp that loads them waits longer (8192^3: 206 us against
-  // 236); one CTA per tile has the warps' time to spare (one token, 8192 x
-  // 8192: 15.5 us against 12.5).
-  static constexpr bool kTmaScales = FP4 && CG == 2;
+  static constexpr int kSlotBlocks = (BN + 127) / 128;       // blocks of 128 slots' scales
+  static constexpr int kAux = FP4 ? 2 * (1 + kSlotBlocks) : GATHER ? kTcAuxGather : 0;
   static constexpr int kWarps = kTcWarpsBf16 + kAux;
   static constexpr int kRows = BN / CG;                      // slots per CTA
   static constexpr int kBox = kRows % 32 == 0 ? 32 : 16;     // rows of a TMA box
   static constexpr int kABytes = kTcWeights * kTcRowBytes;
   static constexpr int kBBytes = kRows * kTcRowBytes;
-  static constexpr int kSlotBlocks = (BN + 127) / 128;       // blocks of 128 slots' scales
-  static constexpr int kScaleBytes = FP4 ? 2048 * (1 + kSlotBlocks) : 0;
-  static constexpr int kStageBytes = kABytes + kBBytes + kScaleBytes;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kScaleSlot = FP4 ? kTcScaleBlock * (1 + kSlotBlocks) : 0;
   static constexpr int kScaleCols = FP4 ? 16 * (1 + kSlotBlocks) : 0;
   // the epilogue reads 32 columns at a time
   static constexpr int kColsUsed = (2 * BN + kScaleCols) < BN + 32 ? BN + 32 : 2 * BN + kScaleCols;
@@ -100,7 +104,7 @@ struct TcShape {
                                : kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
   static constexpr int kChunk = FP4 ? 256 : 64;              // elements of a row per stage
   static constexpr int kStep = 16 * CG;                      // granularity of a tile's slots
-  static_assert(kColsUsed <= 512 && kBBytes % 1024 == 0 && kScaleBytes % 1024 == 0, "");
+  static_assert(kColsUsed <= 512 && kBBytes % 1024 == 0, "");
 };
 
 // Bounded phase wait.  JOIN: what other CTAs of the cluster wrote before they
@@ -143,48 +147,65 @@ __device__ __forceinline__ bool tc_wait_warp(uint32_t bar, uint32_t parity,
 }
 
 // Block scales in shared memory, as the tensor cores read them: 128 rows by
-// 16 bytes (256 elements) are four atoms of 512 bytes, one for each 64
-// elements; row r's four bytes of an atom are word r / 32 of its 16-byte
-// entry r % 32.
-__device__ __forceinline__ void put_scales(unsigned char* dst, const uint4* v, int lane) {
-  // v[r]: the 16 bytes of row lane + 32 r
-  uint4* at = reinterpret_cast<uint4*>(dst) + lane;
-  at[0] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
-  at[32] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
-  at[64] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
-  at[96] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+// 4 bytes (64 elements) are an atom of 512 bytes, in which row r's four bytes
+// are word r / 32 of the 16-byte entry r % 32.  A block of 128 rows by 64
+// bytes is 16 atoms, in the order of the row.
+//
+// A block that TMA wrote as it lies in memory (64-byte rows under the 64-byte
+// swizzle, which moves 16-byte piece q of row r to q ^ (r / 2 % 4)), turned
+// into atoms in place by one warp: lane l holds the rows l, l + 32, ...
+__device__ __forceinline__ void turn_scales(unsigned char* block, int lane) {
+  uint4 v[4][4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int row = r * 32 + lane;
+      v[r][q] = *reinterpret_cast<const uint4*>(block + row * 64 + ((q ^ ((row >> 1) & 3)) << 4));
+    }
+  __syncwarp();       // all of it is read before any is written
+  uint4* to = reinterpret_cast<uint4*>(block) + lane;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    to[(q * 4 + 0) * 32] = make_uint4(v[0][q].x, v[1][q].x, v[2][q].x, v[3][q].x);
+    to[(q * 4 + 1) * 32] = make_uint4(v[0][q].y, v[1][q].y, v[2][q].y, v[3][q].y);
+    to[(q * 4 + 2) * 32] = make_uint4(v[0][q].z, v[1][q].z, v[2][q].z, v[3][q].z);
+    to[(q * 4 + 3) * 32] = make_uint4(v[0][q].w, v[1][q].w, v[2][q].w, v[3][q].w);
+  }
 }
 
-// The same from memory whose alignment allows loads of B bytes: 16 / B lanes
-// to a row, so that a load touches few lines.  `rows` and `left` (bytes of
-// the row from here on) bound what is read; the rest is 0.
+// Rows r0 .. r0 + 63 of a block from memory whose alignment allows loads of B
+// bytes, along the rows, so that a load touches few lines.  `rows` and `left`
+// (bytes of the row from here on) bound what is read; the rest is 0.
 template <int B>
-__device__ __forceinline__ void copy_scale_block(unsigned char* dst, const uint8_t* src,
-                                                 int64_t pitch, int64_t rows, int64_t left,
-                                                 int lane) {
-  constexpr int kLanes = 16 / B, kRows = 32 / kLanes;
-  constexpr int kBatch = B == 1 ? 32 : 128 / kRows;
-  const int in = (lane % kLanes) * B, r0 = lane / kLanes;
-  for (int i0 = 0; i0 < 128 / kRows; i0 += kBatch) {
-    uint32_t v[kBatch];
+__device__ __forceinline__ void copy_scales_of(unsigned char* block, const uint8_t* src,
+                                               int64_t pitch, int r0, int64_t rows, int64_t left,
+                                               int lane) {
+  constexpr int kLanes = 64 / B < 32 ? 64 / B : 32, kRows = 32 / kLanes;
+  constexpr int kBatch = 32 / kRows < 32 ? 32 / kRows * 2 : 32;
+  for (int piece = 0; piece < 64; piece += kLanes * B) {
+    const int in = piece + lane % kLanes * B;
+    for (int i0 = r0; i0 < r0 + 64; i0 += kBatch * kRows) {
+      uint32_t v[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = (i0 + i) * kRows + r0;
-      v[i] = 0u;
-      if (r < rows && in < left) {
-        const uint8_t* at = src + r * pitch + in;
-        if constexpr (B == 4) v[i] = __ldg(reinterpret_cast<const uint32_t*>(at));
-        else if constexpr (B == 2) v[i] = __ldg(reinterpret_cast<const uint16_t*>(at));
-        else v[i] = __ldg(at);
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = i0 + i * kRows + lane / kLanes;
+        v[i] = 0u;
+        if (r < rows && in < left) {
+          const uint8_t* at = src + r * pitch + in;
+          if constexpr (B == 4) v[i] = __ldg(reinterpret_cast<const uint32_t*>(at));
+          else if constexpr (B == 2) v[i] = __ldg(reinterpret_cast<const uint16_t*>(at));
+          else v[i] = __ldg(at);
+        }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = (i0 + i) * kRows + r0;
-      unsigned char* to = dst + (in >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (in & 3);
-      if constexpr (B == 4) *reinterpret_cast<uint32_t*>(to) = v[i];
-      else if constexpr (B == 2) *reinterpret_cast<uint16_t*>(to) = (uint16_t)v[i];
-      else *to = (uint8_t)v[i];
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = i0 + i * kRows + lane / kLanes;
+        unsigned char* to = block + (in >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (in & 3);
+        if constexpr (B == 4) *reinterpret_cast<uint32_t*>(to) = v[i];
+        else if constexpr (B == 2) *reinterpret_cast<uint16_t*>(to) = (uint16_t)v[i];
+        else *to = (uint8_t)v[i];
+      }
     }
   }
 }
@@ -260,11 +281,13 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
   const uint32_t base = (tc::smem_addr(smem_raw) + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - tc::smem_addr(smem_raw));
   const uint32_t NS = t.stages;
-  TcBarriers* bb = reinterpret_cast<TcBarriers*>(smem + (size_t)NS * Sh::kStageBytes);
+  TcBarriers* bb = reinterpret_cast<TcBarriers*>(smem + t.barriers_at);
   const Groups g = groups_at(smem + t.groups_at, p.E);
   const uint32_t full0 = tc::smem_addr(&bb->full[0]);
   const uint32_t empty0 = tc::smem_addr(&bb->empty[0]);
-  const uint32_t raw0 = tc::smem_addr(&bb->raw[0]);
+  const uint32_t sraw0 = tc::smem_addr(&bb->scale_raw[0][0]);
+  const uint32_t sfull0 = tc::smem_addr(&bb->scale_full[0]);
+  const uint32_t sempty0 = tc::smem_addr(&bb->scale_empty[0]);
   const uint32_t tfull0 = tc::smem_addr(&bb->tile_full[0]);
   const uint32_t tempty0 = tc::smem_addr(&bb->tile_empty[0]);
   volatile int* abort_flag = &bb->abort_flag;
@@ -275,13 +298,16 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
 
   if (tid == 0) {
     for (uint32_t s = 0; s < NS; ++s) {
-      mbar_init(full0 + 8 * s, Sh::kAux ? 1 + CG : 1);   // TMA; scales or gathered rows
+      mbar_init(full0 + 8 * s, GATHER ? 1 + CG : 1);   // TMA; gathered rows
       mbar_init(empty0 + 8 * s, 1);
-      mbar_init(raw0 + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull0 + 8 * i, 1);
       mbar_init(tempty0 + 8 * i, 4 * CG);
+      // one warp of each block's two by TMA, else both
+      mbar_init(sfull0 + 8 * i, (t.scale_step == 16 ? 1 : 2) * (1 + Sh::kSlotBlocks) * CG);
+      mbar_init(sempty0 + 8 * i, 1);
+      for (int u = 0; u < 3; ++u) mbar_init(sraw0 + 8 * (i * 3 + u), 1);
     }
     mbar_init(tc::smem_addr(&bb->part_full), 4 * csize);
     mbar_init(tc::smem_addr(&bb->part_empty), 4 * csize);
@@ -296,7 +322,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       tc::prefetch_map(&map_x);
       tc::prefetch_map(&map_part);
     }
-    if (Sh::kTmaScales && t.scale_step == 16) {
+    if (FP4 && t.scale_step == 16) {
       tc::prefetch_map(&map_ws);
       tc::prefetch_map(&map_xs);
     }
@@ -355,20 +381,6 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
               tc::load_2d<CG>(b + i * Sh::kBox * kTcRowBytes, &map_part, x, first + i * Sh::kBox,
                               bar);
           }
-          if (Sh::kTmaScales && t.scale_step == 16) {
-            const int blocks = w.n > 128 ? 2 : 1;
-            const uint32_t sc = b + Sh::kBBytes, rbar = raw0 + 8 * s;
-            mbar_arrive_expect_tx(rbar, 2048 * (1 + blocks));
-            tc::load_2d<1>(sc, &map_ws, c * 16, n0, rbar);
-            if constexpr (CG == 2) {
-              // both CTAs need all slots' scales: each loads one block for both
-              if (w_rank < blocks)
-                tc::load_2d_to(sc + 2048 * (1 + w_rank), &map_xs, c * 16,
-                               w.slot0 + 128 * w_rank, rbar, 3);
-            } else {
-              tc::load_2d<1>(sc + 2048, &map_xs, c * 16, w.slot0, rbar);
-            }
-          }
         }
         __syncwarp();
       }
@@ -388,7 +400,8 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       uint32_t nt = 0;
       bool ok = true;
       const uint64_t desc0 = tc::operand_desc(base);
-      const uint64_t scale0 = tc::scale_desc(base + Sh::kABytes + Sh::kBBytes);
+      const uint64_t scale0 = tc::scale_desc(base + t.scales_at);
+      uint32_t ng = 0;           // groups of scales so far
       const uint32_t sf_a = tmem + 2 * BN, sf_b = sf_a + 16;
       for (int64_t tile = t0; ok && tile < tiles; tile += tstep, ++nt) {
         const Tile w = find_tile(g, p.E, tile, wts, BN);
@@ -402,12 +415,16 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         for (int c = 0; c < nc; ++c, at.next(NS)) {
           const uint32_t s = at.stage, ph = at.phase;
           ok = tc_wait_warp(full0 + 8 * s, ph, abort_flag, p.err, kErrTcFull);
+          if (FP4 && ok && c % kTcScaleStages == 0)
+            ok = tc_wait_warp(sfull0 + 8 * (ng & 1), (ng >> 1) & 1, abort_flag, p.err,
+                              kErrTcFull);
           if (!ok) break;
           tc::fence_after();
           const uint64_t da = desc0 + (s * Sh::kStageBytes >> 4), db = da + (Sh::kABytes >> 4);
           if (tc::elect_one()) {
           if constexpr (FP4) {
-            const uint64_t sc = scale0 + (s * Sh::kStageBytes >> 4);
+            const uint64_t sc = scale0 + ((ng & 1) * Sh::kScaleSlot >> 4) +
+                                (c % kTcScaleStages) * (2048 >> 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               tc::copy_scales<CG>(sf_a + 4 * k, sc + (512 >> 4) * k);
@@ -415,7 +432,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
               for (int j = 0; j < Sh::kSlotBlocks; ++j)
                 if (j == 0 || n_eff > 128)
                   tc::copy_scales<CG>(sf_b + (k * Sh::kSlotBlocks + j) * 4,
-                                      sc + (2048 >> 4) * (1 + j) + (512 >> 4) * k);
+                                      sc + (kTcScaleBlock >> 4) * (1 + j) + (512 >> 4) * k);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -427,8 +444,11 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
               tc::mma_bf16<CG>(d, da + 2 * k, db + 2 * k, idesc, c > 0 || k > 0);
           }
           tc::commit<CG>(empty0 + 8 * s);
+          if (FP4 && (c % kTcScaleStages == kTcScaleStages - 1 || c == nc - 1))
+            tc::commit<CG>(sempty0 + 8 * (ng & 1));
           if (c == nc - 1) tc::commit<CG>(tfull0 + 8 * acc);
           }
+          if (FP4 && (c % kTcScaleStages == kTcScaleStages - 1 || c == nc - 1)) ++ng;
           __syncwarp();
         }
       }
@@ -442,7 +462,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     const uint32_t part_full = tc::smem_addr(&bb->part_full);
     const uint32_t part_empty = tc::smem_addr(&bb->part_empty);
     float* part = reinterpret_cast<float*>(smem + t.part_at);
-    uint32_t* turn = reinterpret_cast<uint32_t*>(smem + t.turn_at + warp * kTurnBytes);
+    uint32_t* turn = reinterpret_cast<uint32_t*>(smem + t.part_at + warp * kTurnBytes);
     for (int64_t tile = t0; ok && tile < tiles; tile += tstep, ++nt) {
       const Tile w = find_tile(g, p.E, tile, wts, BN);
       const uint32_t acc = nt & 1, d = tmem + acc * BN + ((uint32_t)warp << 21);
@@ -498,76 +518,112 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     }
   } else if constexpr (FP4) {
     // ------------------------------------------------------- block scales
-    // A warp takes every kAux-th stage and brings its scales into the layout
-    // above: where their rows are whole 16-byte pieces, from shared memory
-    // (TMA put them there, in place) or 16 bytes per lane, else in smaller
-    // pieces.
-    const int mine = warp - 6;
+    const int u = (warp - 6) >> 1, half = (warp - 6) & 1;    // block; its warp
     const int64_t pitch = p.H / 16;
+    const int groups = (nc + kTcScaleStages - 1) / kTcScaleStages;
+    unsigned char* block0 = smem + t.scales_at + u * kTcScaleBlock;
     bool ok = true;
-    RingPos at;
-    at.skip(mine, NS);
-    int ahead = mine;          // stages until this warp's next
-    for (int64_t tile = t0; ok && tile < tiles; tile += tstep) {
-      const Tile w = find_tile(g, p.E, tile, wts, BN);
-      const int64_t n0 = (int64_t)w.wt * kTileWeights + w_rank * kTcWeights;
-      const int blocks = (w.n + 127) / 128;
-      int c = c0 + ahead;
-      for (; c < c1; c += Sh::kAux, at.skip(Sh::kAux, NS)) {
-        const uint32_t s = at.stage;
-        const int64_t left = pitch - (int64_t)c * 16;
-        unsigned char* dst = smem + s * Sh::kStageBytes + Sh::kABytes + Sh::kBBytes;
-        if (t.scale_step == 16) {
-          uint4 v[1 + Sh::kSlotBlocks][4];
-          if constexpr (Sh::kTmaScales) {
-            ok = tc_wait_warp(raw0 + 8 * s, at.phase, abort_flag, p.err, kErrTcFull);
-            if (!ok) break;
-#pragma unroll
-            for (int u = 0; u <= Sh::kSlotBlocks; ++u)
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (u <= blocks)
-                  v[u][r] = reinterpret_cast<const uint4*>(dst + u * 2048)[r * 32 + lane];
-            __syncwarp();       // in place: all of it is read before any is written
-          } else {
-#pragma unroll
-            for (int u = 0; u <= Sh::kSlotBlocks; ++u)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const int64_t in = r * 32 + lane;
-                v[u][r] = make_uint4(0u, 0u, 0u, 0u);
-                if (u ? in < w.n : n0 + in < p.N)
-                  v[u][r] = __ldg(reinterpret_cast<const uint4*>(
-                      (u ? p.a_scale + (w.slot0 + in) * pitch : p.b_scale + (n0 + in) * pitch) +
-                      (int64_t)c * 16));
-              }
-            ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
-            if (!ok) break;
+    if (t.scale_step == 16) {
+      // TMA brings a block as it lies and one warp turns it; the next group's
+      // copy is on its way while this one's products run.  Both CTAs of a
+      // pair need all slots' scales, so each loads one block for both.
+      const bool mine = CG == 1 || u == 0 || u - 1 == w_rank;
+      int64_t tile = t0;
+      int gi = 0;                             // group of the tile
+      uint32_t asked = 0, done = 0;           // groups so far
+      auto ask = [&]() {                      // false: no more, or gave up
+        if (tile >= tiles) return false;
+        const Tile w = find_tile(g, p.E, tile, wts, BN);
+        const uint32_t slot = asked & 1;
+        if (!tc_wait_warp(sempty0 + 8 * slot, ((asked >> 1) & 1) ^ 1, abort_flag, p.err,
+                          kErrTcEmpty)) {
+          ok = false;
+          return false;
+        }
+        // slots above 128 that the tile does not have are not loaded
+        if (u < 2 || w.n > 128) {
+          if (tc::elect_one()) {
+            const uint32_t bar = sraw0 + 8 * (slot * 3 + u);
+            const uint32_t dst = base + t.scales_at + slot * Sh::kScaleSlot + u * kTcScaleBlock;
+            const int x = (c0 + gi * kTcScaleStages) * 16;
+            mbar_arrive_expect_tx(bar, kTcScaleBlock);
+            if (u == 0)
+              tc::load_2d<1>(dst, &map_ws, x, w.wt * kTileWeights + w_rank * kTcWeights, bar);
+            else if (CG == 1)
+              tc::load_2d<1>(dst, &map_xs, x, w.slot0, bar);
+            else if (mine)
+              tc::load_2d_to(dst, &map_xs, x, w.slot0 + (u - 1) * 128, bar, 3);
           }
-#pragma unroll
-          for (int u = 0; u <= Sh::kSlotBlocks; ++u)
-            if (u <= blocks) put_scales(dst + u * 2048, v[u], lane);
-        } else {
-          ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
-          if (!ok) break;
-          for (int u = 0; u <= blocks; ++u) {
-            const int64_t rows = u ? w.n - (u - 1) * 128 : p.N - n0;
-            const uint8_t* from =
-                (u ? p.a_scale + ((int64_t)w.slot0 + (u - 1) * 128) * pitch
-                   : p.b_scale + n0 * pitch) + (int64_t)c * 16;
-            if (t.scale_step == 4)
-              copy_scale_block<4>(dst + u * 2048, from, pitch, rows, left, lane);
-            else if (t.scale_step == 2)
-              copy_scale_block<2>(dst + u * 2048, from, pitch, rows, left, lane);
-            else
-              copy_scale_block<1>(dst + u * 2048, from, pitch, rows, left, lane);
+          __syncwarp();
+        }
+        ++asked;
+        if (++gi == groups) { gi = 0; tile += tstep; }
+        return true;
+      };
+      if (half == 0) {
+        uint32_t phase[2] = {0, 0};
+        bool more = ask() && ask();
+        for (int64_t at = t0; ok && at < tiles; at += tstep) {
+          const Tile w = find_tile(g, p.E, at, wts, BN);
+          for (int i = 0; ok && i < groups; ++i, ++done) {
+            const uint32_t slot = done & 1;
+            if (u < 2 || w.n > 128) {
+              ok = tc_wait_warp(sraw0 + 8 * (slot * 3 + u), slot ? phase[1] : phase[0],
+                                abort_flag, p.err, kErrTcFull);
+              if (!ok) break;
+              phase[0] ^= slot == 0;
+              phase[1] ^= slot == 1;
+              turn_scales(block0 + slot * Sh::kScaleSlot, lane);
+              tc::fence_async_shared();
+            }
+            __syncwarp();
+            if (lane == 0)
+              tc::mbar_arrive_cluster(tc::map_rank(sfull0 + 8 * slot, CG == 2 ? 0 : rank));
+            // the next group but one goes into the slot of the one before
+            // this, when its products are done; this one is turned by then
+            if (more && done > 0) more = ask();
           }
         }
-        tc::fence_async_shared();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(full0 + 8 * s, CG == 2 ? 0 : rank));
+        // after an abort: what was asked for lands before the CTA leaves
+        for (; done < asked; ++done) {
+          const uint32_t slot = done & 1;
+          const uint64_t begin = globaltimer_ns();
+          while (!tc::mbar_wait_some<true>(sraw0 + 8 * (slot * 3 + u),
+                                           slot ? phase[1] : phase[0], kTcSleepNs) &&
+                 globaltimer_ns() - begin < kWaitLimitNs) {}
+          phase[0] ^= slot == 0;
+          phase[1] ^= slot == 1;
+        }
       }
-      ahead = c - c1;
+    } else {
+      uint32_t ng = 0;
+      for (int64_t tile = t0; ok && tile < tiles; tile += tstep) {
+        const Tile w = find_tile(g, p.E, tile, wts, BN);
+        const int64_t n0 = (int64_t)w.wt * kTileWeights + w_rank * kTcWeights;
+        const int64_t rows = u ? w.n - (u - 1) * 128 : p.N - n0;
+        const uint8_t* src = u ? p.a_scale + ((int64_t)w.slot0 + (u - 1) * 128) * pitch
+                               : p.b_scale + n0 * pitch;
+        for (int i = 0; i < groups; ++i, ++ng) {
+          const uint32_t slot = ng & 1;
+          const int64_t x = (int64_t)(c0 + i * kTcScaleStages) * 16;
+          ok = tc_wait_warp(sempty0 + 8 * slot, ((ng >> 1) & 1) ^ 1, abort_flag, p.err,
+                            kErrTcEmpty);
+          if (!ok) break;
+          unsigned char* block = block0 + slot * Sh::kScaleSlot;
+          if (rows > 0) {
+            if (t.scale_step == 4)
+              copy_scales_of<4>(block, src + x, pitch, half * 64, rows, pitch - x, lane);
+            else if (t.scale_step == 2)
+              copy_scales_of<2>(block, src + x, pitch, half * 64, rows, pitch - x, lane);
+            else
+              copy_scales_of<1>(block, src + x, pitch, half * 64, rows, pitch - x, lane);
+          }
+          tc::fence_async_shared();
+          __syncwarp();
+          if (lane == 0)
+            tc::mbar_arrive_cluster(tc::map_rank(sfull0 + 8 * slot, CG == 2 ? 0 : rank));
+        }
+      }
     }
   }
 
