@@ -205,7 +205,7 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
   if (fp4) {
     const int64_t pitch = p.H / 16;
     const uintptr_t at = (uintptr_t)p.a_scale | (uintptr_t)p.b_scale | (uintptr_t)pitch;
-    t.scale_step = (at & 15u) == 0 ? 16 : (at & 3u) == 0 ? 4 : (at & 1u) == 0 ? 2 : 1;
+    t.tma_scales = (at & 15u) == 0;
   }
   CUtensorMap map_w, map_x, map_part, map_ws, map_xs;
   const TcKind* k = pl.kind;
@@ -220,7 +220,7 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
     return FARN_ERR_CUDA;
   }
   map_ws = map_xs = map_w;        // not read, unless
-  if (fp4 && t.scale_step == 16 && (!encode_scales(ctx, &map_ws, p.b_scale, p.H / 16, p.N) ||
+  if (t.tma_scales && (!encode_scales(ctx, &map_ws, p.b_scale, p.H / 16, p.N) ||
                        !encode_scales(ctx, &map_xs, p.a_scale, p.H / 16, p.n_a)))
     return FARN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -287,9 +287,10 @@ bool product_setup(farn_ctx* ctx) {
       return false;
   for (int i = 0; i < 4; ++i) {
     // one CTA per SM, as any of the kernels takes it
+    const TcKind* k = find_kind(false, 1, 16, false);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(1 << i), 1, 1);
-    cfg.blockDim = dim3(farn::kTcWarpsMost * 32, 1, 1);
+    cfg.blockDim = dim3((unsigned)k->warps * 32, 1, 1);
     cfg.dynamicSmemBytes = ctx->max_smem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -298,9 +299,9 @@ bool product_setup(farn_ctx* ctx) {
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(
-            &ctx->max_clusters[i],
-            (const void*)farn::farn_product_tc_kernel<true, 1, 16, false>, &cfg) != cudaSuccess)
+    if (cudaOccupancyMaxActiveClusters(&ctx->max_clusters[i], (const void*)k->kernel, &cfg) !=
+            cudaSuccess ||
+        (i < 2 && ctx->max_clusters[i] < 1))
       return false;
   }
   ctx->encode_tiled = fn;

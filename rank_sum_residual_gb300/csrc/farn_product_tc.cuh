@@ -42,10 +42,12 @@ constexpr int kTcWarpsBf16 = 6;
 constexpr int kTcAuxGather = 6;
 // NVFP4: block scales come for four stages at a time (64 bytes of a row), in
 // blocks of 128 rows (one of weights, the others of slots) that lie in a ring
-// of two slots of their own; two further warps to a block.
+// of two slots of their own.  Further warps to a block: one if TMA brings it,
+// else four, of 32 rows each (with two of 64 rows the shifting took longer
+// than the products: 4096 x 4096 x 4128 63 us).
 constexpr int kTcScaleStages = 4;
 constexpr int kTcScaleBlock = 128 * 64;
-constexpr int kTcWarpsMost = kTcWarpsBf16 + kTcAuxGather;
+constexpr int kTcScaleWarps = 4;
 constexpr int kErrTcFull = 16;         // status bits: matrix warp waiting for operands,
 constexpr int kErrTcEmpty = 32;        // producers waiting for a free stage,
 constexpr int kErrTcTile = 64;         // epilogue or matrix warp waiting for a tile,
@@ -56,8 +58,7 @@ struct TcParams {
   int stages;
   int ks;            // CTAs of a cluster that split the row (CG = 1)
   int store_bytes;   // 16, 4 or 2: what N and out allow a store of a row to be
-  int scale_step;    // NVFP4: bytes of scales that alignment allows at a time: 16 (by TMA),
-                     // 4, 2 or 1
+  int tma_scales;    // NVFP4: the scales' rows are such that TMA can read them
   uint32_t groups_at;  // shared-memory offsets
   uint32_t scales_at;  // NVFP4: two slots of block scales
   uint32_t barriers_at;
@@ -89,7 +90,7 @@ constexpr int kTurnBytes = 16 * kTurnPitch * 4;
 template <bool FP4, int CG, int BN, bool GATHER>
 struct TcShape {
   static constexpr int kSlotBlocks = (BN + 127) / 128;       // blocks of 128 slots' scales
-  static constexpr int kAux = FP4 ? 2 * (1 + kSlotBlocks) : GATHER ? kTcAuxGather : 0;
+  static constexpr int kAux = FP4 ? kTcScaleWarps * (1 + kSlotBlocks) : GATHER ? kTcAuxGather : 0;
   static constexpr int kWarps = kTcWarpsBf16 + kAux;
   static constexpr int kRows = BN / CG;                      // slots per CTA
   static constexpr int kBox = kRows % 32 == 0 ? 32 : 16;     // rows of a TMA box
@@ -174,38 +175,80 @@ __device__ __forceinline__ void turn_scales(unsigned char* block, int lane) {
   }
 }
 
-// Rows r0 .. r0 + 63 of a block from memory whose alignment allows loads of B
-// bytes, along the rows, so that a load touches few lines.  `rows` and `left`
-// (bytes of the row from here on) bound what is read; the rest is 0.
-template <int B>
-__device__ __forceinline__ void copy_scales_of(unsigned char* block, const uint8_t* src,
-                                               int64_t pitch, int r0, int64_t rows, int64_t left,
-                                               int lane) {
-  constexpr int kLanes = 64 / B < 32 ? 64 / B : 32, kRows = 32 / kLanes;
-  constexpr int kBatch = 32 / kRows < 32 ? 32 / kRows * 2 : 32;
-  for (int piece = 0; piece < 64; piece += kLanes * B) {
-    const int in = piece + lane % kLanes * B;
-    for (int i0 = r0; i0 < r0 + 64; i0 += kBatch * kRows) {
-      uint32_t v[kBatch];
+// 16 bytes at `at`, a multiple of 16, of which those outside [lo, hi) are not
+// read.
+__device__ __noinline__ uint4 load_within(uintptr_t at, uintptr_t lo, uintptr_t hi) {
+  if (at >= lo && at + 16 <= hi) return __ldg(reinterpret_cast<const uint4*>(at));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = i0 + i * kRows + lane / kLanes;
-        v[i] = 0u;
-        if (r < rows && in < left) {
-          const uint8_t* at = src + r * pitch + in;
-          if constexpr (B == 4) v[i] = __ldg(reinterpret_cast<const uint32_t*>(at));
-          else if constexpr (B == 2) v[i] = __ldg(reinterpret_cast<const uint16_t*>(at));
-          else v[i] = __ldg(at);
-        }
-      }
+  for (int i = 0; i < 16; ++i)
+    if (at + i >= lo && at + i < hi)
+      w[i >> 2] |= (uint32_t)__ldg(reinterpret_cast<const uint8_t*>(at + i)) << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 32 rows of a block whose rows in memory start at any byte (H not a multiple
+// of 256), by one warp: five lanes read the five aligned 16-byte pieces that
+// 64 bytes can touch, six rows to a load and all six loads in flight; the words
+// are then shifted into place with the next lane's first.
+struct ScaleRows {
+  const uint8_t* src;    // the first of the rows
+  int rows;              // rows that exist (32 at most); the others are 0
+  int left;              // bytes of a row from src on; what follows is 0
+};
+constexpr int kScaleLoads = 6;
+
+// [lo, hi): the whole tensor, outside of which nothing is read.
+__device__ __forceinline__ void load_scale_rows(uint4* v, const ScaleRows& b, int64_t pitch,
+                                                uintptr_t lo, uintptr_t hi, int lane) {
+  const int piece = lane % 5, sub = lane / 5;
+  const int lim = b.left < 64 ? b.left : 64;
+  const uintptr_t first = (uintptr_t)b.src;
+  // only the tensor's first and last rows have pieces that reach out of it
+  const bool inside = (first & ~(uintptr_t)15) >= lo &&
+                      first + (b.rows - 1) * pitch + lim + 15 <= hi;
+  if (inside) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = i0 + i * kRows + lane / kLanes;
-        unsigned char* to = block + (in >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (in & 3);
-        if constexpr (B == 4) *reinterpret_cast<uint32_t*>(to) = v[i];
-        else if constexpr (B == 2) *reinterpret_cast<uint16_t*>(to) = (uint16_t)v[i];
-        else *to = (uint8_t)v[i];
-      }
+    for (int i = 0; i < kScaleLoads; ++i) {
+      const int k = i * 6 + sub;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      const uintptr_t a = first + k * pitch, at = (a & ~(uintptr_t)15) + piece * 16;
+      if (sub < 6 && k < b.rows && at < a + lim) v[i] = __ldg(reinterpret_cast<const uint4*>(at));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; ++i) {
+      const int k = i * 6 + sub;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      const uintptr_t a = first + k * pitch, at = (a & ~(uintptr_t)15) + piece * 16;
+      if (sub < 6 && k < b.rows && at < a + lim) v[i] = load_within(at, lo, hi);
+    }
+  }
+}
+
+// quarter: the rows' place in the block, which is one word of every entry
+__device__ __forceinline__ void put_scale_rows(unsigned char* block, const uint4* v,
+                                               const ScaleRows& b, int64_t pitch,
+                                               int quarter, int lane) {
+  const int piece = lane % 5, sub = lane / 5;
+  const int lim = b.left < 64 ? b.left : 64;
+  const uint32_t low = (uint32_t)(uintptr_t)b.src, step = (uint32_t)pitch;
+#pragma unroll
+  for (int i = 0; i < kScaleLoads; ++i) {
+    const int k = i * 6 + sub;
+    const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, v[i].x, 1);
+    const uint32_t off = (low + k * step) & 15u, by = 8 * (off & 3u);
+    const uint32_t w[5] = {v[i].x, v[i].y, v[i].z, v[i].w, next};
+    const int b0 = piece * 16 - (int)(off & 12u);
+    const int to = k * 16 + quarter * 4 + b0 * 128;
+    const bool mine = sub < 6 && k < 32;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = b0 + 4 * j;
+      uint32_t word = __funnelshift_r(w[j], w[j + 1], by);
+      if (lim < 64 && at + 4 > lim)
+        word = at >= lim ? 0u : word & ((1u << (8 * (lim - at))) - 1u);
+      if (mine && (uint32_t)at < 64u) *reinterpret_cast<uint32_t*>(block + to + 512 * j) = word;
     }
   }
 }
@@ -304,8 +347,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull0 + 8 * i, 1);
       mbar_init(tempty0 + 8 * i, 4 * CG);
-      // one warp of each block's two by TMA, else both
-      mbar_init(sfull0 + 8 * i, (t.scale_step == 16 ? 1 : 2) * (1 + Sh::kSlotBlocks) * CG);
+      mbar_init(sfull0 + 8 * i, (t.tma_scales ? 1 : kTcScaleWarps) * (1 + Sh::kSlotBlocks) * CG);
       mbar_init(sempty0 + 8 * i, 1);
       for (int u = 0; u < 3; ++u) mbar_init(sraw0 + 8 * (i * 3 + u), 1);
     }
@@ -322,7 +364,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       tc::prefetch_map(&map_x);
       tc::prefetch_map(&map_part);
     }
-    if (FP4 && t.scale_step == 16) {
+    if (FP4 && t.tma_scales) {
       tc::prefetch_map(&map_ws);
       tc::prefetch_map(&map_xs);
     }
@@ -518,12 +560,12 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     }
   } else if constexpr (FP4) {
     // ------------------------------------------------------- block scales
-    const int u = (warp - 6) >> 1, half = (warp - 6) & 1;    // block; its warp
+    const int u = (warp - 6) / kTcScaleWarps, quarter = (warp - 6) % kTcScaleWarps;
     const int64_t pitch = p.H / 16;
     const int groups = (nc + kTcScaleStages - 1) / kTcScaleStages;
     unsigned char* block0 = smem + t.scales_at + u * kTcScaleBlock;
     bool ok = true;
-    if (t.scale_step == 16) {
+    if (t.tma_scales) {
       // TMA brings a block as it lies and one warp turns it; the next group's
       // copy is on its way while this one's products run.  Both CTAs of a
       // pair need all slots' scales, so each loads one block for both.
@@ -560,7 +602,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         if (++gi == groups) { gi = 0; tile += tstep; }
         return true;
       };
-      if (half == 0) {
+      if (quarter == 0) {
         uint32_t phase[2] = {0, 0};
         bool more = ask() && ask();
         for (int64_t at = t0; ok && at < tiles; at += tstep) {
@@ -596,32 +638,46 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         }
       }
     } else {
-      uint32_t ng = 0;
-      for (int64_t tile = t0; ok && tile < tiles; tile += tstep) {
+      const uintptr_t lo = (uintptr_t)(u ? p.a_scale : p.b_scale);
+      const uintptr_t hi = lo + (u ? p.n_a : p.N) * pitch;
+      // The next group's rows are on their way while the warp waits for a
+      // slot.
+      int64_t tile = t0;
+      int gi = 0;
+      auto next = [&]() {
         const Tile w = find_tile(g, p.E, tile, wts, BN);
         const int64_t n0 = (int64_t)w.wt * kTileWeights + w_rank * kTcWeights;
-        const int64_t rows = u ? w.n - (u - 1) * 128 : p.N - n0;
-        const uint8_t* src = u ? p.a_scale + ((int64_t)w.slot0 + (u - 1) * 128) * pitch
-                               : p.b_scale + n0 * pitch;
-        for (int i = 0; i < groups; ++i, ++ng) {
-          const uint32_t slot = ng & 1;
-          const int64_t x = (int64_t)(c0 + i * kTcScaleStages) * 16;
-          ok = tc_wait_warp(sempty0 + 8 * slot, ((ng >> 1) & 1) ^ 1, abort_flag, p.err,
-                            kErrTcEmpty);
-          if (!ok) break;
-          unsigned char* block = block0 + slot * Sh::kScaleSlot;
-          if (rows > 0) {
-            if (t.scale_step == 4)
-              copy_scales_of<4>(block, src + x, pitch, half * 64, rows, pitch - x, lane);
-            else if (t.scale_step == 2)
-              copy_scales_of<2>(block, src + x, pitch, half * 64, rows, pitch - x, lane);
-            else
-              copy_scales_of<1>(block, src + x, pitch, half * 64, rows, pitch - x, lane);
-          }
-          tc::fence_async_shared();
-          __syncwarp();
-          if (lane == 0)
-            tc::mbar_arrive_cluster(tc::map_rank(sfull0 + 8 * slot, CG == 2 ? 0 : rank));
+        const int first = (u ? (u - 1) * 128 : 0) + quarter * 32;
+        const int64_t x = (int64_t)(c0 + gi * kTcScaleStages) * 16;
+        ScaleRows b;
+        b.src = (u ? p.a_scale + ((int64_t)w.slot0 + first) * pitch
+                   : p.b_scale + (n0 + first) * pitch) + x;
+        b.rows = (int)min((u ? (int64_t)w.n : p.N - n0) - first, (int64_t)32);
+        b.left = (int)min(pitch - x, (int64_t)64);
+        if (++gi == groups) { gi = 0; tile += tstep; }
+        return b;
+      };
+      uint4 v[kScaleLoads];
+      ScaleRows b = {};
+      bool more = tile < tiles;
+      if (more) {
+        b = next();
+        load_scale_rows(v, b, pitch, lo, hi, lane);
+      }
+      for (uint32_t ng = 0; more; ++ng) {
+        const uint32_t slot = ng & 1;
+        ok = tc_wait_warp(sempty0 + 8 * slot, ((ng >> 1) & 1) ^ 1, abort_flag, p.err,
+                          kErrTcEmpty);
+        if (!ok) break;
+        put_scale_rows(block0 + slot * Sh::kScaleSlot, v, b, pitch, quarter, lane);
+        tc::fence_async_shared();
+        __syncwarp();
+        if (lane == 0)
+          tc::mbar_arrive_cluster(tc::map_rank(sfull0 + 8 * slot, CG == 2 ? 0 : rank));
+        more = tile < tiles;
+        if (more) {           // after the fence, which waits for loads too
+          b = next();
+          load_scale_rows(v, b, pitch, lo, hi, lane);
         }
       }
     }
