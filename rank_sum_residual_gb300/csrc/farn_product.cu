@@ -29,6 +29,7 @@ int launch_plain(const farn_ctx* ctx, const ProductParams& p, bool fp4, cudaStre
   const int64_t tiles =
       slot_tiles * ((p.N + farn::kPlainTile - 1) / farn::kPlainTile);
   const int64_t most = (int64_t)ctx->num_sms * 4;
+  if (tiles > 0x7FFFFFFF / 2) return FARN_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles < most ? tiles : most), 1, 1);
   cfg.blockDim = dim3(farn::kPlainThreads, 1, 1);
@@ -52,30 +53,38 @@ typedef void (*TcKernel)(const farn::TcParams, const CUtensorMap, const CUtensor
                          const CUtensorMap, const CUtensorMap, const CUtensorMap);
 
 struct TcKind {
-  bool fp4, gather;
+  bool fp4, gather, copy;
   int cg, bn;
   TcKernel kernel;
   int warps, stage_bytes, scale_bytes, rows, box;
 };
 
-template <bool FP4, int CG, int BN, bool GATHER>
+template <bool FP4, int CG, int BN, bool GATHER, bool COPY>
 TcKind kind() {
-  using Sh = farn::TcShape<FP4, CG, BN, GATHER>;
-  return TcKind{FP4, GATHER, CG, BN, &farn::farn_product_tc_kernel<FP4, CG, BN, GATHER>,
-                Sh::kWarps, Sh::kStageBytes, 2 * Sh::kScaleSlot, Sh::kRows, Sh::kBox};
+  using Sh = farn::TcShape<FP4, CG, BN, GATHER, COPY>;
+  return TcKind{FP4, GATHER, COPY, CG, BN,
+                &farn::farn_product_tc_kernel<FP4, CG, BN, GATHER, COPY>,
+                Sh::kWarps, Sh::kStageBytes, farn::kTcScaleSlots * Sh::kScaleSlot, Sh::kRows, Sh::kBox};
 }
 
 const TcKind kKinds[] = {
-    kind<false, 1, 16, false>(),  kind<false, 1, 16, true>(),  kind<false, 1, 32, false>(),
-    kind<false, 1, 32, true>(),   kind<false, 1, 64, false>(), kind<false, 1, 64, true>(),
-    kind<false, 1, 128, false>(), kind<false, 1, 128, true>(), kind<false, 2, 256, false>(),
-    kind<false, 2, 256, true>(),  kind<true, 1, 16, false>(),  kind<true, 1, 32, false>(),
-    kind<true, 1, 64, false>(),   kind<true, 1, 128, false>(), kind<true, 2, 224, false>(),
+    kind<false, 1, 16, false, false>(),  kind<false, 1, 16, true, false>(),
+    kind<false, 1, 32, false, false>(),  kind<false, 1, 32, true, false>(),
+    kind<false, 1, 64, false, false>(),  kind<false, 1, 64, true, false>(),
+    kind<false, 1, 128, false, false>(), kind<false, 1, 128, true, false>(),
+    kind<false, 2, 256, false, false>(), kind<false, 2, 256, true, false>(),
+    kind<true, 1, 16, false, false>(),   kind<true, 1, 16, false, true>(),
+    kind<true, 1, 32, false, false>(),   kind<true, 1, 32, false, true>(),
+    kind<true, 1, 64, false, false>(),   kind<true, 1, 64, false, true>(),
+    kind<true, 1, 128, false, false>(),  kind<true, 1, 128, false, true>(),
+    kind<true, 2, 224, false, false>(),  kind<true, 2, 224, false, true>(),
 };
 
-const TcKind* find_kind(bool fp4, int cg, int bn, bool gather) {
+// copy: an NVFP4 call whose block scales TMA cannot read
+const TcKind* find_kind(bool fp4, int cg, int bn, bool gather, bool copy) {
   for (const TcKind& k : kKinds)
-    if (k.fp4 == fp4 && k.cg == cg && k.bn == bn && k.gather == gather) return &k;
+    if (k.fp4 == fp4 && k.cg == cg && k.bn == bn && k.gather == gather && k.copy == copy)
+      return &k;
   return nullptr;
 }
 
@@ -114,6 +123,9 @@ int log2_of(int v) { return v >= 8 ? 3 : v >= 4 ? 2 : v >= 2 ? 1 : 0; }
 // The kernel for a call of S slots in E groups.
 bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, TcPlan* pl) {
   const bool gather = p.rows != nullptr;
+  // TMA reads rows of whole 16-byte pieces
+  const bool copy = fp4 && (((uintptr_t)p.a_scale | (uintptr_t)p.b_scale |
+                             (uintptr_t)(p.H / 16)) & 15u) != 0;
   const int64_t groups = p.E < p.S ? p.E : p.S;
   const int64_t avg = (p.S + groups - 1) / groups;     // slots of a group that has some
   int cg = 1, bn = 128;
@@ -124,12 +136,13 @@ bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, TcPlan* pl) 
   else { cg = 2; bn = fp4 ? 224 : 256; }
   const int64_t wts = (p.N + cg * farn::kTcWeights - 1) / (cg * farn::kTcWeights);
   const int64_t tiles = (p.S / bn + groups) * wts;
+  if (tiles > 0x7FFFFFFF / 2) return false;
   const int64_t chunks = (p.H + (fp4 ? 255 : 63)) / (fp4 ? 256 : 64);
   int ks = 1;
   if (cg == 1)
     while (ks < 8 && tiles * ks * 2 <= ctx->num_sms && chunks >= ks * 4) ks *= 2;
   // the parts of a split row take room from the ring: fewer, if it is short
-  while (!fit(ctx, find_kind(fp4, cg, bn, gather), p.E, ks, pl)) {
+  while (!fit(ctx, find_kind(fp4, cg, bn, gather, copy), p.E, ks, pl)) {
     if (ks == 1) return false;
     ks = 1;
   }
@@ -164,13 +177,13 @@ bool encode(const farn_ctx* ctx, CUtensorMap* map, bool fp4, const void* base, i
          CUDA_SUCCESS;
 }
 
-// Block scales: 64 bytes (1024 elements) of 128 rows, written with the
-// 64-byte swizzle.
+// Block scales: 32 bytes (512 elements) of 128 rows, written with the 32-byte
+// swizzle.
 bool encode_scales(const farn_ctx* ctx, CUtensorMap* map, const void* base, int64_t pitch,
                    int64_t rows) {
   const cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)pitch};
-  const cuuint32_t boxes[2] = {64u, 128u};
+  const cuuint32_t boxes[2] = {(cuuint32_t)farn::kTcScaleRow, 128u};
   const cuuint32_t steps[2] = {1u, 1u};
   return ((EncodeTiled)ctx->encode_tiled)(
              map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, boxes,
@@ -202,11 +215,6 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
   t.scales_at = pl.scales_at;
   t.barriers_at = pl.barriers_at;
   t.part_at = pl.part_at;
-  if (fp4) {
-    const int64_t pitch = p.H / 16;
-    const uintptr_t at = (uintptr_t)p.a_scale | (uintptr_t)p.b_scale | (uintptr_t)pitch;
-    t.tma_scales = (at & 15u) == 0;
-  }
   CUtensorMap map_w, map_x, map_part, map_ws, map_xs;
   const TcKind* k = pl.kind;
   if (!encode(ctx, &map_w, fp4, p.b, p.H, p.N, p.E, farn::kTcWeights)) return FARN_ERR_CUDA;
@@ -220,7 +228,7 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
     return FARN_ERR_CUDA;
   }
   map_ws = map_xs = map_w;        // not read, unless
-  if (t.tma_scales && (!encode_scales(ctx, &map_ws, p.b_scale, p.H / 16, p.N) ||
+  if (k->fp4 && !k->copy && (!encode_scales(ctx, &map_ws, p.b_scale, p.H / 16, p.N) ||
                        !encode_scales(ctx, &map_xs, p.a_scale, p.H / 16, p.n_a)))
     return FARN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -287,7 +295,7 @@ bool product_setup(farn_ctx* ctx) {
       return false;
   for (int i = 0; i < 4; ++i) {
     // one CTA per SM, as any of the kernels takes it
-    const TcKind* k = find_kind(false, 1, 16, false);
+    const TcKind* k = find_kind(false, 1, 16, false, false);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(1 << i), 1, 1);
     cfg.blockDim = dim3((unsigned)k->warps * 32, 1, 1);

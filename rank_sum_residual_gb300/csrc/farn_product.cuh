@@ -83,24 +83,26 @@ struct Tile {
   int wt;          // weight tile
 };
 
-// Tile t of the walk over all groups; wts: weight tiles per group.  Within a
+// Tile t (the host keeps their number below 2^31) of the walk over all groups,
+// by a whole warp; wts: weight tiles per
+// group.  Within a
 // group the walk covers kSuper slot tiles by all weight tiles before it goes
 // on, slot tiles fastest, so that the tiles in flight at a time share both
 // operands' rows in L2.
 constexpr int kSuper = 8;
 
-__device__ __forceinline__ Tile find_tile(const Groups& g, int E, int64_t t, int wts, int bn) {
-  const int32_t q = (int32_t)(t / wts);
+__device__ __forceinline__ Tile find_tile(const Groups& g, int E, int32_t t, int wts, int bn) {
+  const int32_t q = t / wts;
   int lo = 0, hi = E - 1;            // the last e with tile[e] <= q
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (g.tile[mid] <= q) lo = mid; else hi = mid - 1;
   }
   const int32_t st = g.tile[lo + 1] - g.tile[lo];       // slot tiles of the group
-  const int64_t local = t - (int64_t)g.tile[lo] * wts;
-  const int64_t per = (int64_t)kSuper * wts;
-  const int32_t sup = (int32_t)(local / per);
-  const int32_t in = (int32_t)(local - sup * per);
+  const int32_t local = t - g.tile[lo] * wts;
+  const int32_t per = kSuper * wts;
+  const int32_t sup = local / per;
+  const int32_t in = local - sup * per;
   const int32_t width = min(kSuper, st - sup * kSuper);
   // The group's tiles are of one size (a multiple of 32, or of bn below
   // that), rather than full ones and a rest: a tile of few slots streams its
@@ -113,6 +115,12 @@ __device__ __forceinline__ Tile find_tile(const Groups& g, int E, int64_t t, int
   const int32_t s = sup * kSuper + (in - r.wt * width);
   r.slot0 = g.first[lo] + s * size;
   r.n = min(size, count - s * size);
+  // all lanes hold the same; a broadcast lets the compiler know it, and the
+  // TMA and matrix instructions' operands then need no move of their own
+  r.e = __shfl_sync(0xFFFFFFFFu, r.e, 0);
+  r.wt = __shfl_sync(0xFFFFFFFFu, r.wt, 0);
+  r.slot0 = __shfl_sync(0xFFFFFFFFu, r.slot0, 0);
+  r.n = __shfl_sync(0xFFFFFFFFu, r.n, 0);
   return r;
 }
 
@@ -153,8 +161,8 @@ farn_product_plain_kernel(const ProductParams p) {
   load_groups(g, p, kPlainTile);
   const int tid = threadIdx.x, ti = tid / 16, tj = tid % 16;
   const int wts = (int)((p.N + kPlainTile - 1) / kPlainTile);
-  const int64_t tiles = (int64_t)g.tile[p.E] * wts;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+  const int32_t tiles = g.tile[p.E] * wts;
+  for (int32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const Tile w = find_tile(g, p.E, t, wts, kPlainTile);
     const int64_t n0 = (int64_t)w.wt * kPlainTile;
     float acc[4][4] = {};

@@ -34,20 +34,23 @@ namespace farn {
 constexpr int kTcMaxStages = 12;
 constexpr int kTcRowBytes = 128;       // bytes of a row per stage: one swizzle span
 constexpr int kTcWeights = 128;        // weights per CTA and tile
-constexpr int kTcWarpsBf16 = 6;
 // Further warps for gathered rows.  Each takes every sixth stage.  They may
 // not be more than the ring has stages: a warp that waits for a stage has to
 // be within one round of the ring, or the parity of the phase it waits for
 // says nothing.
 constexpr int kTcAuxGather = 6;
-// NVFP4: block scales come for four stages at a time (64 bytes of a row), in
+// NVFP4: block scales come for two stages at a time (32 bytes of a row), in
 // blocks of 128 rows (one of weights, the others of slots) that lie in a ring
-// of two slots of their own.  Further warps to a block: one if TMA brings it,
-// else four, of 32 rows each (with two of 64 rows the shifting took longer
-// than the products: 4096 x 4096 x 4128 63 us).
+// of four slots of their own.  With two slots of four stages a group's copy
+// could only be asked for one group ahead, and its latency with the turning
+// (about 2500 cycles) was four stages' time: 8192^3 178 us.
+// Further warps to a block: one if TMA brings it, else (COPY) four, of 32 rows
+// each (two of 64 rows took longer for the shifting than the products).
 constexpr int kTcScaleStages = 4;
-constexpr int kTcScaleBlock = 128 * 64;
-constexpr int kTcScaleWarps = 4;
+constexpr int kTcScaleSlots = 2;
+constexpr int kTcScaleRow = 16 * kTcScaleStages;      // bytes
+constexpr int kTcScaleBlock = 128 * kTcScaleRow;
+constexpr int kTcCopyWarps = 4;
 constexpr int kErrTcFull = 16;         // status bits: matrix warp waiting for operands,
 constexpr int kErrTcEmpty = 32;        // producers waiting for a free stage,
 constexpr int kErrTcTile = 64;         // epilogue or matrix warp waiting for a tile,
@@ -58,9 +61,8 @@ struct TcParams {
   int stages;
   int ks;            // CTAs of a cluster that split the row (CG = 1)
   int store_bytes;   // 16, 4 or 2: what N and out allow a store of a row to be
-  int tma_scales;    // NVFP4: the scales' rows are such that TMA can read them
   uint32_t groups_at;  // shared-memory offsets
-  uint32_t scales_at;  // NVFP4: two slots of block scales
+  uint32_t scales_at;  // NVFP4: the slots of block scales
   uint32_t barriers_at;
   uint32_t part_at;    // fp32 [BN][kPartPitch] for ks > 1, else kTurnBytes for each
                        // epilogue warp
@@ -68,9 +70,9 @@ struct TcParams {
 
 struct TcBarriers {
   uint64_t full[kTcMaxStages];
-  uint64_t scale_raw[2][3];        // a block of scales has landed, as it lies in memory
-  uint64_t scale_full[2];          // the slot's scales are as the tensor cores read them
-  uint64_t scale_empty[2];
+  uint64_t scale_raw[kTcScaleSlots][3];   // a block of scales has landed, as it lies in memory
+  uint64_t scale_full[kTcScaleSlots];     // the slot's scales are as the tensor cores read them
+  uint64_t scale_empty[kTcScaleSlots];
   uint64_t empty[kTcMaxStages];
   uint64_t tile_full[2];
   uint64_t tile_empty[2];
@@ -87,11 +89,15 @@ constexpr int kPartPitch = kTcWeights + 4;
 constexpr int kTurnPitch = 36;
 constexpr int kTurnBytes = 16 * kTurnPitch * 4;
 
-template <bool FP4, int CG, int BN, bool GATHER>
+template <bool FP4, int CG, int BN, bool GATHER, bool COPY>
 struct TcShape {
   static constexpr int kSlotBlocks = (BN + 127) / 128;       // blocks of 128 slots' scales
-  static constexpr int kAux = FP4 ? kTcScaleWarps * (1 + kSlotBlocks) : GATHER ? kTcAuxGather : 0;
-  static constexpr int kWarps = kTcWarpsBf16 + kAux;
+  static constexpr int kScaleWarps = COPY ? kTcCopyWarps : 1;
+  static constexpr int kAux = FP4 ? kScaleWarps * (1 + kSlotBlocks) : GATHER ? kTcAuxGather : 0;
+  // four epilogue warps, the weights' producer, the matrix warp, and unless
+  // the rows are gathered the slots' producer; then the further ones
+  static constexpr int kFirstAux = GATHER ? 6 : 7;
+  static constexpr int kWarps = kFirstAux + kAux;
   static constexpr int kRows = BN / CG;                      // slots per CTA
   static constexpr int kBox = kRows % 32 == 0 ? 32 : 16;     // rows of a TMA box
   static constexpr int kABytes = kTcWeights * kTcRowBytes;
@@ -104,9 +110,28 @@ struct TcShape {
   static constexpr int kCols = kColsUsed <= 32 ? 32 : kColsUsed <= 64 ? 64
                                : kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
   static constexpr int kChunk = FP4 ? 256 : 64;              // elements of a row per stage
+  static constexpr int kMapStep = FP4 ? kTcRowBytes : kChunk;  // the same in map elements
   static constexpr int kStep = 16 * CG;                      // granularity of a tile's slots
   static_assert(kColsUsed <= 512 && kBBytes % 1024 == 0, "");
 };
+
+// A tile's slots as one CTA's part of the matrix instruction's N side.
+struct SlotRows {
+  int first;        // slot
+  bool whole;       // one box of all rows, else `loads` boxes of a few
+  int loads;
+  uint32_t bytes;
+};
+template <typename Sh, int CG>
+__device__ __forceinline__ SlotRows slot_rows(const Tile& w, int w_rank) {
+  const int rows = (w.n + Sh::kStep - 1) / Sh::kStep * Sh::kStep / CG;
+  SlotRows r;
+  r.first = w.slot0 + w_rank * rows;
+  r.whole = rows > Sh::kRows - Sh::kBox;
+  r.loads = (rows + Sh::kBox - 1) / Sh::kBox;
+  r.bytes = (uint32_t)(r.whole ? Sh::kRows : r.loads * Sh::kBox) * kTcRowBytes;
+  return r;
+}
 
 // Bounded phase wait.  JOIN: what other CTAs of the cluster wrote before they
 // arrived is read afterwards.
@@ -140,6 +165,10 @@ struct RingPos {
   }
 };
 
+// A value that all lanes hold, in a form that the compiler takes for uniform:
+// the matrix instructions' operands then need no move of their own.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 // The same by a whole warp, whose lanes go on or give up together.
 template <bool JOIN = false>
 __device__ __forceinline__ bool tc_wait_warp(uint32_t bar, uint32_t parity,
@@ -149,11 +178,11 @@ __device__ __forceinline__ bool tc_wait_warp(uint32_t bar, uint32_t parity,
 
 // Block scales in shared memory, as the tensor cores read them: 128 rows by
 // 4 bytes (64 elements) are an atom of 512 bytes, in which row r's four bytes
-// are word r / 32 of the 16-byte entry r % 32.  A block of 128 rows by 64
-// bytes is 16 atoms, in the order of the row.
+// are word r / 32 of the 16-byte entry r % 32.  A block of 128 rows by 32
+// bytes is 8 atoms, in the order of the row.
 //
-// A block that TMA wrote as it lies in memory (64-byte rows under the 64-byte
-// swizzle, which moves 16-byte piece q of row r to q ^ (r / 2 % 4)), turned
+// A block that TMA wrote as it lies in memory (32-byte rows under the 32-byte
+// swizzle, which moves 16-byte piece q of row r to q ^ (r / 4 % 2)), turned
 // into atoms in place by one warp: lane l holds the rows l, l + 32, ...
 __device__ __forceinline__ void turn_scales(unsigned char* block, int lane) {
   uint4 v[4][4];
@@ -188,21 +217,23 @@ __device__ __noinline__ uint4 load_within(uintptr_t at, uintptr_t lo, uintptr_t 
 }
 
 // 32 rows of a block whose rows in memory start at any byte (H not a multiple
-// of 256), by one warp: five lanes read the five aligned 16-byte pieces that
-// 64 bytes can touch, six rows to a load and all six loads in flight; the words
-// are then shifted into place with the next lane's first.
+// of 256), by one warp: three lanes read the three aligned 16-byte pieces that
+// 32 bytes can touch, ten rows to a load and all four loads in flight; the
+// words are then shifted into place with the next lane's first.
 struct ScaleRows {
   const uint8_t* src;    // the first of the rows
   int rows;              // rows that exist (32 at most); the others are 0
   int left;              // bytes of a row from src on; what follows is 0
 };
+constexpr int kScalePieces = 5;
+constexpr int kScaleRows = 6;        // per load
 constexpr int kScaleLoads = 6;
 
 // [lo, hi): the whole tensor, outside of which nothing is read.
 __device__ __forceinline__ void load_scale_rows(uint4* v, const ScaleRows& b, int64_t pitch,
                                                 uintptr_t lo, uintptr_t hi, int lane) {
-  const int piece = lane % 5, sub = lane / 5;
-  const int lim = b.left < 64 ? b.left : 64;
+  const int piece = lane % kScalePieces, sub = lane / kScalePieces;
+  const int lim = b.left < kTcScaleRow ? b.left : kTcScaleRow;
   const uintptr_t first = (uintptr_t)b.src;
   // only the tensor's first and last rows have pieces that reach out of it
   const bool inside = (first & ~(uintptr_t)15) >= lo &&
@@ -210,18 +241,18 @@ __device__ __forceinline__ void load_scale_rows(uint4* v, const ScaleRows& b, in
   if (inside) {
 #pragma unroll
     for (int i = 0; i < kScaleLoads; ++i) {
-      const int k = i * 6 + sub;
+      const int k = i * kScaleRows + sub;
       v[i] = make_uint4(0u, 0u, 0u, 0u);
       const uintptr_t a = first + k * pitch, at = (a & ~(uintptr_t)15) + piece * 16;
-      if (sub < 6 && k < b.rows && at < a + lim) v[i] = __ldg(reinterpret_cast<const uint4*>(at));
+      if (sub < kScaleRows && k < b.rows && at < a + lim) v[i] = __ldg(reinterpret_cast<const uint4*>(at));
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kScaleLoads; ++i) {
-      const int k = i * 6 + sub;
+      const int k = i * kScaleRows + sub;
       v[i] = make_uint4(0u, 0u, 0u, 0u);
       const uintptr_t a = first + k * pitch, at = (a & ~(uintptr_t)15) + piece * 16;
-      if (sub < 6 && k < b.rows && at < a + lim) v[i] = load_within(at, lo, hi);
+      if (sub < kScaleRows && k < b.rows && at < a + lim) v[i] = load_within(at, lo, hi);
     }
   }
 }
@@ -230,25 +261,25 @@ __device__ __forceinline__ void load_scale_rows(uint4* v, const ScaleRows& b, in
 __device__ __forceinline__ void put_scale_rows(unsigned char* block, const uint4* v,
                                                const ScaleRows& b, int64_t pitch,
                                                int quarter, int lane) {
-  const int piece = lane % 5, sub = lane / 5;
-  const int lim = b.left < 64 ? b.left : 64;
+  const int piece = lane % kScalePieces, sub = lane / kScalePieces;
+  const int lim = b.left < kTcScaleRow ? b.left : kTcScaleRow;
   const uint32_t low = (uint32_t)(uintptr_t)b.src, step = (uint32_t)pitch;
 #pragma unroll
   for (int i = 0; i < kScaleLoads; ++i) {
-    const int k = i * 6 + sub;
+    const int k = i * kScaleRows + sub;
     const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, v[i].x, 1);
     const uint32_t off = (low + k * step) & 15u, by = 8 * (off & 3u);
     const uint32_t w[5] = {v[i].x, v[i].y, v[i].z, v[i].w, next};
     const int b0 = piece * 16 - (int)(off & 12u);
     const int to = k * 16 + quarter * 4 + b0 * 128;
-    const bool mine = sub < 6 && k < 32;
+    const bool mine = sub < kScaleRows && k < 32;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int at = b0 + 4 * j;
       uint32_t word = __funnelshift_r(w[j], w[j + 1], by);
-      if (lim < 64 && at + 4 > lim)
+      if (lim < kTcScaleRow && at + 4 > lim)
         word = at >= lim ? 0u : word & ((1u << (8 * (lim - at))) - 1u);
-      if (mine && (uint32_t)at < 64u) *reinterpret_cast<uint32_t*>(block + to + 512 * j) = word;
+      if (mine && (uint32_t)at < (uint32_t)kTcScaleRow) *reinterpret_cast<uint32_t*>(block + to + 512 * j) = word;
     }
   }
 }
@@ -310,15 +341,15 @@ __device__ __forceinline__ void store_turned(const TcParams& t, uint32_t tmem, u
   __syncwarp();
 }
 
-template <bool FP4, int CG, int BN, bool GATHER>
-__global__ void __launch_bounds__(TcShape<FP4, CG, BN, GATHER>::kWarps * 32, 1)
+template <bool FP4, int CG, int BN, bool GATHER, bool COPY>
+__global__ void __launch_bounds__(TcShape<FP4, CG, BN, GATHER, COPY>::kWarps * 32, 1)
 farn_product_tc_kernel(const __grid_constant__ TcParams t,
                        const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ CUtensorMap map_x,
                        const __grid_constant__ CUtensorMap map_part,
                        const __grid_constant__ CUtensorMap map_ws,
                        const __grid_constant__ CUtensorMap map_xs) {
-  using Sh = TcShape<FP4, CG, BN, GATHER>;
+  using Sh = TcShape<FP4, CG, BN, GATHER, COPY>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const ProductParams& p = t.p;
   const uint32_t base = (tc::smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -347,7 +378,9 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull0 + 8 * i, 1);
       mbar_init(tempty0 + 8 * i, 4 * CG);
-      mbar_init(sfull0 + 8 * i, (t.tma_scales ? 1 : kTcScaleWarps) * (1 + Sh::kSlotBlocks) * CG);
+    }
+    for (int i = 0; i < kTcScaleSlots; ++i) {
+      mbar_init(sfull0 + 8 * i, Sh::kScaleWarps * (1 + Sh::kSlotBlocks) * CG);
       mbar_init(sempty0 + 8 * i, 1);
       for (int u = 0; u < 3; ++u) mbar_init(sraw0 + 8 * (i * 3 + u), 1);
     }
@@ -364,7 +397,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       tc::prefetch_map(&map_x);
       tc::prefetch_map(&map_part);
     }
-    if (FP4 && t.tma_scales) {
+    if (FP4 && !COPY) {
       tc::prefetch_map(&map_ws);
       tc::prefetch_map(&map_xs);
     }
@@ -375,12 +408,12 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
   tc::fence_before();
   if (csize > 1) tc::cluster_sync(); else __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = bb->tmem;
+  const uint32_t tmem = uniform(bb->tmem);
 
   constexpr int kTileWeights = kTcWeights * CG;
   const int wts = (int)((p.N + kTileWeights - 1) / kTileWeights);
-  const int64_t tiles = (int64_t)g.tile[p.E] * wts;
-  const int64_t t0 = blockIdx.x / csize, tstep = gridDim.x / csize;
+  const int32_t tiles = g.tile[p.E] * wts;
+  const int32_t t0 = blockIdx.x / csize, tstep = gridDim.x / csize;
   const int chunks = (int)((p.H + Sh::kChunk - 1) / Sh::kChunk);
   const int c0 = CG == 2 ? 0 : (int)((int64_t)chunks * rank / csize);
   const int c1 = CG == 2 ? chunks : (int)((int64_t)chunks * (rank + 1) / csize);
@@ -388,41 +421,28 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
   const int w_rank = CG == 2 ? (int)rank : 0;      // this CTA's part of a tile's weights
 
   if (warp == 4) {
-    // ---------------------------------------------------------- producer
-    const uint32_t bar_rank = CG == 2 ? 0 : rank;
+    // ------------------------------------------------- weights' producer
+    // The slots' rows have a producer of their own: one warp for both took
+    // 640 cycles per stage to issue them, more than the NVFP4 products take.
+    const uint32_t bar0 = tc::map_rank(full0, CG == 2 ? 0 : rank);
     RingPos at;
     uint32_t armed = 0;        // stages given to TMA, all but the last NS done
     bool ok = true;
     if (t.p.stall_test && blockIdx.x == 0)
       ok = tc_wait_warp(tc::smem_addr(&bb->never), 0, abort_flag, p.err, kErrTcEmpty);
-    for (int64_t tile = t0; ok && tile < tiles; tile += tstep) {
+    for (int32_t tile = t0; ok && tile < tiles; tile += tstep) {
       const Tile w = find_tile(g, p.E, tile, wts, BN);
-      const int n_eff = (w.n + Sh::kStep - 1) / Sh::kStep * Sh::kStep;
-      const int rows = n_eff / CG;                       // of this CTA, a multiple of 16
-      const int first = w.slot0 + w_rank * rows;
-      // whole tiles with one box, others with boxes of a few rows
-      const bool whole = rows > Sh::kRows - Sh::kBox;
-      const int loads = GATHER ? 0 : whole ? 1 : (rows + Sh::kBox - 1) / Sh::kBox;
-      const uint32_t bytes = (uint32_t)loads * (whole ? Sh::kRows : Sh::kBox) * kTcRowBytes;
+      const SlotRows r = slot_rows<Sh, CG>(w, w_rank);
+      const uint32_t bytes = CG * (Sh::kABytes + (GATHER ? 0 : r.bytes));
       const int n0 = w.wt * kTileWeights + w_rank * kTcWeights;
       for (int c = c0; c < c1; ++c, at.next(NS), ++armed) {
         const uint32_t s = at.stage;
         ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
         if (!ok) break;
-        const uint32_t a = base + s * Sh::kStageBytes, b = a + Sh::kABytes;
-        const uint32_t bar = tc::map_rank(full0 + 8 * s, bar_rank);
-        const int x = c * (FP4 ? kTcRowBytes : Sh::kChunk);
         if (tc::elect_one()) {
-          if (w_rank == 0)
-            mbar_arrive_expect_tx(full0 + 8 * s, CG * (Sh::kABytes + bytes));
-          tc::load_3d<CG>(a, &map_w, x, n0, w.e, bar);
-          if (!GATHER && whole) {
-            tc::load_2d<CG>(b, &map_x, x, first, bar);
-          } else if constexpr (!GATHER) {
-            for (int i = 0; i < loads; ++i)
-              tc::load_2d<CG>(b + i * Sh::kBox * kTcRowBytes, &map_part, x, first + i * Sh::kBox,
-                              bar);
-          }
+          if (w_rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, bytes);
+          tc::load_3d<CG>(base + s * Sh::kStageBytes, &map_w, c * Sh::kMapStep, n0, w.e,
+                          bar0 + 8 * s);
         }
         __syncwarp();
       }
@@ -445,7 +465,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       const uint64_t scale0 = tc::scale_desc(base + t.scales_at);
       uint32_t ng = 0;           // groups of scales so far
       const uint32_t sf_a = tmem + 2 * BN, sf_b = sf_a + 16;
-      for (int64_t tile = t0; ok && tile < tiles; tile += tstep, ++nt) {
+      for (int32_t tile = t0; ok && tile < tiles; tile += tstep, ++nt) {
         const Tile w = find_tile(g, p.E, tile, wts, BN);
         const int n_eff = (w.n + Sh::kStep - 1) / Sh::kStep * Sh::kStep;
         const uint32_t idesc = FP4 ? tc::idesc_nvfp4(kTileWeights, n_eff)
@@ -454,44 +474,57 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         ok = tc_wait_warp(tempty0 + 8 * acc, ((nt >> 1) & 1) ^ 1, abort_flag, p.err, kErrTcTile);
         if (!ok) break;
         tc::fence_after();
-        for (int c = 0; c < nc; ++c, at.next(NS)) {
-          const uint32_t s = at.stage, ph = at.phase;
-          ok = tc_wait_warp(full0 + 8 * s, ph, abort_flag, p.err, kErrTcFull);
-          if (FP4 && ok && c % kTcScaleStages == 0)
-            ok = tc_wait_warp(sfull0 + 8 * (ng & 1), (ng >> 1) & 1, abort_flag, p.err,
-                              kErrTcFull);
-          if (!ok) break;
-          tc::fence_after();
-          const uint64_t da = desc0 + (s * Sh::kStageBytes >> 4), db = da + (Sh::kABytes >> 4);
-          if (tc::elect_one()) {
+        // Few instructions per stage: a dependent one costs this warp about
+        // ten cycles, and a stage's NVFP4 products take 450.
+        uint32_t more = 0;                 // 0 before the tile's first product
+        for (int c = 0; ok && c < nc;) {
+          uint64_t sc = 0;
+          int end = nc;
           if constexpr (FP4) {
-            const uint64_t sc = scale0 + ((ng & 1) * Sh::kScaleSlot >> 4) +
-                                (c % kTcScaleStages) * (2048 >> 4);
+            const uint32_t slot = ng % kTcScaleSlots;
+            ok = tc_wait_warp(sfull0 + 8 * slot, ng / kTcScaleSlots & 1, abort_flag, p.err,
+                              kErrTcFull);
+            sc = scale0 + (slot * Sh::kScaleSlot >> 4);
+            end = min(nc, c + kTcScaleStages);
+          }
+          for (; ok && c < end; ++c) {
+            const uint32_t s = at.stage;
+            ok = tc_wait_warp(full0 + 8 * s, at.phase, abort_flag, p.err, kErrTcFull);
+            if (!ok) break;
+            tc::fence_after();
+            const uint64_t da = desc0 + (s * Sh::kStageBytes >> 4), db = da + (Sh::kABytes >> 4);
+            if (tc::elect_one()) {
+              if constexpr (FP4) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              tc::copy_scales<CG>(sf_a + 4 * k, sc + (512 >> 4) * k);
+                for (int k = 0; k < 4; ++k) {
+                  tc::copy_scales<CG>(sf_a + 4 * k, sc + (512 >> 4) * k);
 #pragma unroll
-              for (int j = 0; j < Sh::kSlotBlocks; ++j)
-                if (j == 0 || n_eff > 128)
-                  tc::copy_scales<CG>(sf_b + (k * Sh::kSlotBlocks + j) * 4,
-                                      sc + (kTcScaleBlock >> 4) * (1 + j) + (512 >> 4) * k);
+                  for (int j = 0; j < Sh::kSlotBlocks; ++j)
+                    if (j == 0 || n_eff > 128)
+                      tc::copy_scales<CG>(sf_b + (k * Sh::kSlotBlocks + j) * 4,
+                                          sc + (kTcScaleBlock >> 4) * (1 + j) + (512 >> 4) * k);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  tc::mma_nvfp4<CG>(d, da + 2 * k, db + 2 * k, idesc, sf_a + 4 * k,
+                                    sf_b + 4 * k * Sh::kSlotBlocks, k > 0 ? 1u : more);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  tc::mma_bf16<CG>(d, da + 2 * k, db + 2 * k, idesc, k > 0 ? 1u : more);
+              }
+              tc::commit<CG>(empty0 + 8 * s);
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::mma_nvfp4<CG>(d, da + 2 * k, db + 2 * k, idesc, sf_a + 4 * k,
-                                sf_b + 4 * k * Sh::kSlotBlocks, c > 0 || k > 0);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::mma_bf16<CG>(d, da + 2 * k, db + 2 * k, idesc, c > 0 || k > 0);
+            more = 1;
+            sc += 2048 >> 4;
+            at.next(NS);
           }
-          tc::commit<CG>(empty0 + 8 * s);
-          if (FP4 && (c % kTcScaleStages == kTcScaleStages - 1 || c == nc - 1))
-            tc::commit<CG>(sempty0 + 8 * (ng & 1));
-          if (c == nc - 1) tc::commit<CG>(tfull0 + 8 * acc);
+          if (!ok) break;
+          if (tc::elect_one()) {
+            if constexpr (FP4) tc::commit<CG>(sempty0 + 8 * (ng % kTcScaleSlots));
+            if (c == nc) tc::commit<CG>(tfull0 + 8 * acc);
           }
-          if (FP4 && (c % kTcScaleStages == kTcScaleStages - 1 || c == nc - 1)) ++ng;
-          __syncwarp();
+          ++ng;
         }
       }
     }
@@ -505,7 +538,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     const uint32_t part_empty = tc::smem_addr(&bb->part_empty);
     float* part = reinterpret_cast<float*>(smem + t.part_at);
     uint32_t* turn = reinterpret_cast<uint32_t*>(smem + t.part_at + warp * kTurnBytes);
-    for (int64_t tile = t0; ok && tile < tiles; tile += tstep, ++nt) {
+    for (int32_t tile = t0; ok && tile < tiles; tile += tstep, ++nt) {
       const Tile w = find_tile(g, p.E, tile, wts, BN);
       const uint32_t acc = nt & 1, d = tmem + acc * BN + ((uint32_t)warp << 21);
       const int64_t n0 = (int64_t)w.wt * kTileWeights + w_rank * kTcWeights;
@@ -558,26 +591,53 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         if (lane < csize) tc::mbar_arrive_cluster(tc::map_rank(part_empty, lane));
       }
     }
+  } else if (!GATHER && warp == 6) {
+    // --------------------------------------------------- slots' producer
+    const uint32_t bar0 = tc::map_rank(full0, CG == 2 ? 0 : rank);
+    RingPos at;
+    bool ok = true;
+    for (int32_t tile = t0; ok && tile < tiles; tile += tstep) {
+      const Tile w = find_tile(g, p.E, tile, wts, BN);
+      const SlotRows r = slot_rows<Sh, CG>(w, w_rank);
+      for (int c = c0; c < c1; ++c, at.next(NS)) {
+        const uint32_t s = at.stage;
+        ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
+        if (!ok) break;
+        const uint32_t b = base + s * Sh::kStageBytes + Sh::kABytes;
+        if (tc::elect_one()) {
+          if (r.whole) {
+            tc::load_2d<CG>(b, &map_x, c * Sh::kMapStep, r.first, bar0 + 8 * s);
+          } else {
+            for (int i = 0; i < r.loads; ++i)
+              tc::load_2d<CG>(b + i * Sh::kBox * kTcRowBytes, &map_part, c * Sh::kMapStep,
+                              r.first + i * Sh::kBox, bar0 + 8 * s);
+          }
+        }
+        __syncwarp();
+      }
+    }
   } else if constexpr (FP4) {
     // ------------------------------------------------------- block scales
-    const int u = (warp - 6) / kTcScaleWarps, quarter = (warp - 6) % kTcScaleWarps;
+    const int u = (warp - Sh::kFirstAux) / Sh::kScaleWarps;             // block
+    const int quarter = (warp - Sh::kFirstAux) % Sh::kScaleWarps;       // its warp
     const int64_t pitch = p.H / 16;
     const int groups = (nc + kTcScaleStages - 1) / kTcScaleStages;
     unsigned char* block0 = smem + t.scales_at + u * kTcScaleBlock;
     bool ok = true;
-    if (t.tma_scales) {
+    if constexpr (!COPY) {
       // TMA brings a block as it lies and one warp turns it; the next group's
       // copy is on its way while this one's products run.  Both CTAs of a
       // pair need all slots' scales, so each loads one block for both.
       const bool mine = CG == 1 || u == 0 || u - 1 == w_rank;
-      int64_t tile = t0;
+      int32_t tile = t0;
       int gi = 0;                             // group of the tile
       uint32_t asked = 0, done = 0;           // groups so far
+      Tile w = {};
       auto ask = [&]() {                      // false: no more, or gave up
         if (tile >= tiles) return false;
-        const Tile w = find_tile(g, p.E, tile, wts, BN);
-        const uint32_t slot = asked & 1;
-        if (!tc_wait_warp(sempty0 + 8 * slot, ((asked >> 1) & 1) ^ 1, abort_flag, p.err,
+        if (gi == 0) w = find_tile(g, p.E, tile, wts, BN);
+        const uint32_t slot = asked % kTcScaleSlots;
+        if (!tc_wait_warp(sempty0 + 8 * slot, (asked / kTcScaleSlots & 1) ^ 1, abort_flag, p.err,
                           kErrTcEmpty)) {
           ok = false;
           return false;
@@ -602,39 +662,38 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         if (++gi == groups) { gi = 0; tile += tstep; }
         return true;
       };
-      if (quarter == 0) {
-        uint32_t phase[2] = {0, 0};
-        bool more = ask() && ask();
-        for (int64_t at = t0; ok && at < tiles; at += tstep) {
-          const Tile w = find_tile(g, p.E, at, wts, BN);
+      {
+        uint32_t phases = 0;        // of each slot's raw barrier, a bit each
+        bool more = true;
+        for (int i = 0; more && i < kTcScaleSlots; ++i) more = ask();
+        for (int32_t at = t0; ok && at < tiles; at += tstep) {
+          const int n = find_tile(g, p.E, at, wts, BN).n;
           for (int i = 0; ok && i < groups; ++i, ++done) {
-            const uint32_t slot = done & 1;
-            if (u < 2 || w.n > 128) {
-              ok = tc_wait_warp(sraw0 + 8 * (slot * 3 + u), slot ? phase[1] : phase[0],
-                                abort_flag, p.err, kErrTcFull);
+            const uint32_t slot = done % kTcScaleSlots;
+            if (u < 2 || n > 128) {
+              ok = tc_wait_warp(sraw0 + 8 * (slot * 3 + u), phases >> slot & 1, abort_flag,
+                                p.err, kErrTcFull);
               if (!ok) break;
-              phase[0] ^= slot == 0;
-              phase[1] ^= slot == 1;
+              phases ^= 1u << slot;
               turn_scales(block0 + slot * Sh::kScaleSlot, lane);
               tc::fence_async_shared();
             }
             __syncwarp();
             if (lane == 0)
               tc::mbar_arrive_cluster(tc::map_rank(sfull0 + 8 * slot, CG == 2 ? 0 : rank));
-            // the next group but one goes into the slot of the one before
-            // this, when its products are done; this one is turned by then
+            // the last slot is the one of the group before this, when its
+            // products are done; this one is turned by then
             if (more && done > 0) more = ask();
           }
         }
         // after an abort: what was asked for lands before the CTA leaves
         for (; done < asked; ++done) {
-          const uint32_t slot = done & 1;
+          const uint32_t slot = done % kTcScaleSlots;
           const uint64_t begin = globaltimer_ns();
-          while (!tc::mbar_wait_some<true>(sraw0 + 8 * (slot * 3 + u),
-                                           slot ? phase[1] : phase[0], kTcSleepNs) &&
+          while (!tc::mbar_wait_some<true>(sraw0 + 8 * (slot * 3 + u), phases >> slot & 1,
+                                           kTcSleepNs) &&
                  globaltimer_ns() - begin < kWaitLimitNs) {}
-          phase[0] ^= slot == 0;
-          phase[1] ^= slot == 1;
+          phases ^= 1u << slot;
         }
       }
     } else {
@@ -642,10 +701,11 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       const uintptr_t hi = lo + (u ? p.n_a : p.N) * pitch;
       // The next group's rows are on their way while the warp waits for a
       // slot.
-      int64_t tile = t0;
+      int32_t tile = t0;
       int gi = 0;
+      Tile w = {};
       auto next = [&]() {
-        const Tile w = find_tile(g, p.E, tile, wts, BN);
+        if (gi == 0) w = find_tile(g, p.E, tile, wts, BN);
         const int64_t n0 = (int64_t)w.wt * kTileWeights + w_rank * kTcWeights;
         const int first = (u ? (u - 1) * 128 : 0) + quarter * 32;
         const int64_t x = (int64_t)(c0 + gi * kTcScaleStages) * 16;
@@ -653,7 +713,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         b.src = (u ? p.a_scale + ((int64_t)w.slot0 + first) * pitch
                    : p.b_scale + (n0 + first) * pitch) + x;
         b.rows = (int)min((u ? (int64_t)w.n : p.N - n0) - first, (int64_t)32);
-        b.left = (int)min(pitch - x, (int64_t)64);
+        b.left = (int)min(pitch - x, (int64_t)kTcScaleRow);
         if (++gi == groups) { gi = 0; tile += tstep; }
         return b;
       };
@@ -665,8 +725,8 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         load_scale_rows(v, b, pitch, lo, hi, lane);
       }
       for (uint32_t ng = 0; more; ++ng) {
-        const uint32_t slot = ng & 1;
-        ok = tc_wait_warp(sempty0 + 8 * slot, ((ng >> 1) & 1) ^ 1, abort_flag, p.err,
+        const uint32_t slot = ng % kTcScaleSlots;
+        ok = tc_wait_warp(sempty0 + 8 * slot, (ng / kTcScaleSlots & 1) ^ 1, abort_flag, p.err,
                           kErrTcEmpty);
         if (!ok) break;
         put_scale_rows(block0 + slot * Sh::kScaleSlot, v, b, pitch, quarter, lane);
@@ -684,21 +744,21 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
   }
 
   if constexpr (GATHER) {
-    if (warp >= 6) {
+    if (warp >= Sh::kFirstAux) {
       // ------------------------------------------------------ gathered rows
       // Warp i takes every sixth stage, so that a stage's copies have the whole
       // ring's time to land.  Eight lanes copy a row's 128 bytes, in the
       // swizzled layout that TMA would write: 16-byte column j of row r at
       // j ^ (r & 7).  Lane l knows the rows l, l + 32, l + 64 and l + 96.
       constexpr int kHeld = (Sh::kRows + 31) / 32;
-      const int mine = warp - 6, col = lane & 7, sub = lane >> 3;
+      const int mine = warp - Sh::kFirstAux, col = lane & 7, sub = lane >> 3;
       const char* x = static_cast<const char*>(p.a) + col * 16;
       const uint64_t pitch = (uint64_t)p.H * 2;
       RingPos at;
       at.skip(mine, NS);
       int ahead = mine;
       bool ok = true;
-      for (int64_t tile = t0; ok && tile < tiles; tile += tstep) {
+      for (int32_t tile = t0; ok && tile < tiles; tile += tstep) {
         const Tile w = find_tile(g, p.E, tile, wts, BN);
         const int n_eff = (w.n + Sh::kStep - 1) / Sh::kStep * Sh::kStep;
         const int rows = n_eff / CG;           // a multiple of 16
