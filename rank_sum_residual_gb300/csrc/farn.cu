@@ -695,6 +695,10 @@ int farn_create(farn_ctx** out, int device) {
     else if (!strcmp(v, "bulk")) c->force_variant = kVariantBulk;
     else if (!strcmp(v, "stage")) c->force_variant = kVariantStage;
   }
+  c->tc_tile = env_int("FARN_TC_TILE", 0);
+  if (c->tc_tile != 64 && c->tc_tile != 256) c->tc_tile = 0;
+  c->tc_split = env_int("FARN_TC_SPLIT", 0);
+  if (c->tc_split != 1 && c->tc_split != 2 && c->tc_split != 4) c->tc_split = 0;
   c->stage = env_int("FARN_STAGE", 1) != 0;
   c->stage_r = env_int("FARN_STAGE_R", 0);
   c->stage_ctas = env_int("FARN_STAGE_CTAS", 0);

@@ -14,7 +14,6 @@ enum {
   kVariantBulk = 3,
   kVariantStage = 4,
   kVariantCombine = 5,   // the MoE combine's one-CTA-per-row gather kernel
-  kVariantTensor = 6,    // the products' tensor-core kernels
   kVariantAuto = -1
 };
 
@@ -41,8 +40,11 @@ struct farn_ctx {
   int fault_launch;    // FARN_FAULT_INJECT=launch at create: every launch fails
   int stall_test;      // FARN_FAULT_INJECT=stall at create: the TMA-staged kernel's
                        // CTA 0 runs its bounded waits out (a test of the status word)
+  int tc_tile;         // 0 = choose; else the products' tiles: 64 slots by one CTA, or 256
+                       // (NVFP4: 224) by a pair
+  int tc_split;        // 0 = choose; else CTAs that split a row: 1, 2 or 4
   void* encode_tiled;  // the driver's tensor-map encoder (the products' kernels)
-  int max_clusters[4]; // clusters of 1, 2, 4 and 8 such CTAs that fit the device at a time
+  int max_clusters[3]; // clusters of 1, 2 and 4 of their CTAs that fit the device at a time
 };
 
 namespace farn_host {

@@ -68,22 +68,16 @@ TcKind kind() {
 }
 
 const TcKind kKinds[] = {
-    kind<false, 1, 16, false, false>(),  kind<false, 1, 16, true, false>(),
-    kind<false, 1, 32, false, false>(),  kind<false, 1, 32, true, false>(),
     kind<false, 1, 64, false, false>(),  kind<false, 1, 64, true, false>(),
-    kind<false, 1, 128, false, false>(), kind<false, 1, 128, true, false>(),
     kind<false, 2, 256, false, false>(), kind<false, 2, 256, true, false>(),
-    kind<true, 1, 16, false, false>(),   kind<true, 1, 16, false, true>(),
-    kind<true, 1, 32, false, false>(),   kind<true, 1, 32, false, true>(),
     kind<true, 1, 64, false, false>(),   kind<true, 1, 64, false, true>(),
-    kind<true, 1, 128, false, false>(),  kind<true, 1, 128, false, true>(),
     kind<true, 2, 224, false, false>(),  kind<true, 2, 224, false, true>(),
 };
 
 // copy: an NVFP4 call whose block scales TMA cannot read
-const TcKind* find_kind(bool fp4, int cg, int bn, bool gather, bool copy) {
+const TcKind* find_kind(bool fp4, int cg, bool gather, bool copy) {
   for (const TcKind& k : kKinds)
-    if (k.fp4 == fp4 && k.cg == cg && k.bn == bn && k.gather == gather && k.copy == copy)
+    if (k.fp4 == fp4 && k.cg == cg && k.gather == gather && k.copy == copy)
       return &k;
   return nullptr;
 }
@@ -104,7 +98,7 @@ bool fit(const farn_ctx* ctx, const TcKind* k, int E, int ks, TcPlan* pl) {
   const uint32_t barriers = ((uint32_t)sizeof(farn::TcBarriers) + 15u) / 16 * 16;
   const uint32_t groups = (farn::groups_bytes(E) + 15u) / 16 * 16;
   const uint32_t fixed = 1024 + k->scale_bytes + barriers + groups + part;
-  int stages = ((int)ctx->max_smem - (int)fixed) / k->stage_bytes;
+  int stages = (ctx->max_smem - (int)fixed) / k->stage_bytes;
   if (stages > farn::kTcMaxStages) stages = farn::kTcMaxStages;
   if (stages < 2 || (k->gather && stages < farn::kTcAuxGather)) return false;
   pl->kind = k;
@@ -118,7 +112,7 @@ bool fit(const farn_ctx* ctx, const TcKind* k, int E, int ks, TcPlan* pl) {
   return true;
 }
 
-int log2_of(int v) { return v >= 8 ? 3 : v >= 4 ? 2 : v >= 2 ? 1 : 0; }
+int log2_of(int v) { return v >= 4 ? 2 : v >= 2 ? 1 : 0; }
 
 // The kernel for a call of S slots in E groups.
 bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, TcPlan* pl) {
@@ -127,27 +121,43 @@ bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, TcPlan* pl) 
   const bool copy = fp4 && (((uintptr_t)p.a_scale | (uintptr_t)p.b_scale |
                              (uintptr_t)(p.H / 16)) & 15u) != 0;
   const int64_t groups = p.E < p.S ? p.E : p.S;
-  const int64_t avg = (p.S + groups - 1) / groups;     // slots of a group that has some
-  int cg = 1, bn = 128;
-  if (avg <= 8) bn = 16;
-  else if (avg <= 24) bn = 32;
-  else if (avg <= 64) bn = 64;
-  else if (avg <= 128 || p.N <= 128) bn = 128;
-  else { cg = 2; bn = fp4 ? 224 : 256; }
-  const int64_t wts = (p.N + cg * farn::kTcWeights - 1) / (cg * farn::kTcWeights);
-  const int64_t tiles = (p.S / bn + groups) * wts;
-  if (tiles > 0x7FFFFFFF / 2) return false;
   const int64_t chunks = (p.H + (fp4 ? 255 : 63)) / (fp4 ? 256 : 64);
-  int ks = 1;
-  if (cg == 1)
-    while (ks < 8 && tiles * ks * 2 <= ctx->num_sms && chunks >= ks * 4) ks *= 2;
-  // the parts of a split row take room from the ring: fewer, if it is short
-  while (!fit(ctx, find_kind(fp4, cg, bn, gather, copy), p.E, ks, pl)) {
-    if (ks == 1) return false;
-    ks = 1;
-  }
-  const int csize = cg == 2 ? 2 : ks;
-  const int64_t most = ctx->max_clusters[log2_of(csize)];
+  // Slot tiles of `bn`: exact for one group, else every group's rest counted
+  // as one more (the offsets are on the device).
+  auto tiles_of = [&](int bn, int weights) {
+    const int64_t slots = p.E == 1 ? (p.S + bn - 1) / bn : p.S / bn + groups;
+    return slots * ((p.N + weights - 1) / weights);
+  };
+  const TcKind* one = find_kind(fp4, 1, gather, copy);
+  const TcKind* pair = find_kind(fp4, 2, gather, copy);
+  const int64_t tiles1 = tiles_of(one->bn, farn::kTcWeights);
+  const int64_t tiles2 = tiles_of(pair->bn, 2 * farn::kTcWeights);
+  if (tiles1 > 0x7FFFFFFF / 2 || tiles2 > 0x7FFFFFFF / 2) return false;
+  // One CTA per tile of 128 weights by 64 slots, with the row split over as
+  // many CTAs as there are SMs to spare, or a pair of CTAs per tile of 256 by
+  // 256 (NVFP4: 224): whichever has fewer stages one after the other.  A stage
+  // takes much the same time in all of them, as it is bound by its
+  // synchronisation (one CTA) or made to be (the pair's tensor work); joining
+  // a split row costs about six.  Measured (us, one CTA / pair): NVFP4
+  // 8192 x 8192, 8 tokens 13.4 / 14.2, 128 tokens 16.5 / 15.6, 512 tokens 46 /
+  // 26; 64 experts 2048 -> 7168 of 16 slots each 274 / 277, of 64 321 / 287, of
+  // 256 853 / 365.  Tiles of 16 and of 32 slots were never faster than of 64
+  // (16 slots each: 304 and 281), tiles of 128 for one CTA hardly.
+  int ks = 1;      // 8 CTAs to a row were never faster than 4
+  while (ks < farn::kTcMaxSplit && tiles1 * ks * 2 <= ctx->num_sms && chunks >= ks * 4) ks *= 2;
+  if (ctx->tc_split) ks = ctx->tc_split;
+  const int64_t sms = ctx->num_sms, pairs = ctx->max_clusters[1];
+  const int64_t cost1 =
+      (tiles1 * ks + sms - 1) / sms * ((chunks + ks - 1) / ks) + (ks > 1 ? 6 : 0);
+  const int64_t cost2 = (tiles2 + pairs - 1) / pairs * chunks;
+  bool use_pair = cost2 < cost1 || (cost2 == cost1 && p.S > 32 * groups);
+  if (ctx->tc_tile) use_pair = ctx->tc_tile == 256;
+  if (use_pair) ks = 1;
+  // the parts of a split row take room from the ring: none, if it is short
+  const TcKind* k = use_pair ? pair : one;
+  if (!fit(ctx, k, p.E, ks, pl) && !fit(ctx, k, p.E, 1, pl)) return false;
+  const int csize = use_pair ? 2 : pl->ks;
+  const int64_t most = ctx->max_clusters[log2_of(csize)], tiles = use_pair ? tiles2 : tiles1;
   if (most < 1) return false;
   pl->grid = (unsigned)((tiles < most ? tiles : most) * csize);
   return true;
@@ -293,9 +303,9 @@ bool product_setup(farn_ctx* ctx) {
     if (cudaFuncSetAttribute((const void*)k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ctx->max_smem) != cudaSuccess)
       return false;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 3; ++i) {
     // one CTA per SM, as any of the kernels takes it
-    const TcKind* k = find_kind(false, 1, 16, false, false);
+    const TcKind* k = find_kind(false, 1, false, false);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(1 << i), 1, 1);
     cfg.blockDim = dim3((unsigned)k->warps * 32, 1, 1);

@@ -32,6 +32,7 @@
 namespace farn {
 
 constexpr int kTcMaxStages = 12;
+constexpr int kTcMaxSplit = 4;         // CTAs that split a row
 constexpr int kTcRowBytes = 128;       // bytes of a row per stage: one swizzle span
 constexpr int kTcWeights = 128;        // weights per CTA and tile
 // Further warps for gathered rows.  Each takes every sixth stage.  They may
@@ -576,16 +577,46 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         if (lane < csize) tc::mbar_arrive_cluster(tc::map_rank(part_full, lane));
         ok = tc_wait_warp<true>(part_full, nt & 1, abort_flag, p.err, kErrTcJoin);
         if (!ok) break;
+        // each CTA sums its share of the tile, four weights to a thread, the
+        // parts in rank order; two quads' loads are in flight together
         const uint32_t mine = tc::smem_addr(part);
-        for (int i = (int)rank * 128 + tid; i < w.n * 128; i += csize * 128) {
-          const int j = i >> 7, k = i & 127;
-          float sum = 0.0f;
-          for (int q = 0; q < csize; ++q)
-            sum += tc::ld_cluster_f32(tc::map_rank(mine, q) + (j * kPartPitch + k) * 4);
-          const int64_t s = (int64_t)w.slot0 + j;
-          bool live = true;
-          if constexpr (GATHER) live = p.rows[s] >= 0 && p.rows[s] < p.n_a;
-          if (n0 + k < p.N) out[s * p.N + n0 + k] = live ? to_bf16(sum * p.alpha) : (uint16_t)0;
+        const int quads = w.n * (kTcWeights / 4), step = csize * 128;
+        for (int i0 = (int)rank * 128 + tid; i0 < quads; i0 += 2 * step) {
+          float4 v[2][kTcMaxSplit];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int i = i0 + h * step;
+            const uint32_t at = ((i >> 5) * kPartPitch + (i & 31) * 4) * 4;
+#pragma unroll
+            for (int q = 0; q < kTcMaxSplit; ++q)
+              if (q < csize && i < quads) v[h][q] = tc::ld_cluster_v4(tc::map_rank(mine, q) + at);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int i = i0 + h * step;
+            if (i >= quads) break;
+            float4 sum = v[h][0];
+#pragma unroll
+            for (int q = 1; q < kTcMaxSplit; ++q)
+              if (q < csize) {
+                sum.x += v[h][q].x; sum.y += v[h][q].y; sum.z += v[h][q].z; sum.w += v[h][q].w;
+              }
+            const int64_t s = (int64_t)w.slot0 + (i >> 5), n = n0 + (i & 31) * 4;
+            if constexpr (GATHER)
+              if (p.rows[s] < 0 || p.rows[s] >= p.n_a) sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            const uint32_t e[2] = {pack_bf16x2(sum.x * p.alpha, sum.y * p.alpha),
+                                   pack_bf16x2(sum.z * p.alpha, sum.w * p.alpha)};
+            uint16_t* o = out + s * p.N + n;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if (t.store_bytes >= 4) {
+                if (n + 2 * k < p.N) reinterpret_cast<uint32_t*>(o)[k] = e[k];
+              } else {
+                if (n + 2 * k < p.N) o[2 * k] = (uint16_t)(e[k] & 0xFFFFu);
+                if (n + 2 * k + 1 < p.N) o[2 * k + 1] = (uint16_t)(e[k] >> 16);
+              }
+            }
+          }
         }
         __syncwarp();
         if (lane < csize) tc::mbar_arrive_cluster(tc::map_rank(part_empty, lane));
