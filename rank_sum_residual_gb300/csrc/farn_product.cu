@@ -146,6 +146,7 @@ bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, TcPlan* pl) 
   int ks = 1;      // 8 CTAs to a row were never faster than 4
   while (ks < farn::kTcMaxSplit && tiles1 * ks * 2 <= ctx->num_sms && chunks >= ks * 4) ks *= 2;
   if (ctx->tc_split) ks = ctx->tc_split;
+  while (ks > chunks) ks /= 2;      // every CTA has a part of the row
   const int64_t sms = ctx->num_sms, pairs = ctx->max_clusters[1];
   const int64_t cost1 =
       (tiles1 * ks + sms - 1) / sms * ((chunks + ks - 1) / ks) + (ks > 1 ? 6 : 0);

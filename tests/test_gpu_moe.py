@@ -27,8 +27,16 @@ def dev():
 
 @pytest.fixture(scope="module")
 def ctxs(dev):
-    """The library's own choice, and the kernel for any shape."""
-    return {"auto": farn.Context(0), "generic": make_ctx(FARN_VARIANT="generic")}
+    """The library's own choice, the kernel for any shape, and every shape of
+    tile of the others."""
+    return {"auto": farn.Context(0), "generic": make_ctx(FARN_VARIANT="generic"),
+            "pair": make_ctx(FARN_TC_TILE=256),
+            "one": make_ctx(FARN_TC_TILE=64, FARN_TC_SPLIT=1),
+            "split2": make_ctx(FARN_TC_TILE=64, FARN_TC_SPLIT=2),
+            "split4": make_ctx(FARN_TC_TILE=64, FARN_TC_SPLIT=4)}
+
+
+ALL = ["auto", "generic", "pair", "one", "split2", "split4"]
 
 
 # ---------------------------------------------------------------- router
@@ -195,7 +203,7 @@ def check_exact(got, want, offsets, what):
     assert torch.equal(got[lo:hi], want[lo:hi].float().to(torch.bfloat16)), what
 
 
-@pytest.mark.parametrize("which", ["auto", "generic"])
+@pytest.mark.parametrize("which", ALL)
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("counts,N,H", GROUPS)
 def test_grouped_exact(dev, ctxs, which, gather, counts, N, H):
@@ -214,7 +222,7 @@ def test_grouped_exact(dev, ctxs, which, gather, counts, N, H):
     check_exact(got, want, offsets, (counts, N, H))
 
 
-@pytest.mark.parametrize("which", ["auto", "generic"])
+@pytest.mark.parametrize("which", ALL)
 @pytest.mark.parametrize("counts,N,H", [([5, 0, 11], 72, 520), ([300, 20], 264, 2056),
                                         ([1, 1], 512, 7168), ([130] * 4, 300, 1000)])
 def test_grouped_rounding(dev, ctxs, which, counts, N, H):
@@ -261,7 +269,7 @@ def test_grouped_any_alignment(dev, ctxs):
             check_exact(got, want, offsets, (dx, dw))
 
 
-@pytest.mark.parametrize("which", ["auto", "generic"])
+@pytest.mark.parametrize("which", ALL)
 @pytest.mark.parametrize("per", [2, 40, 300])
 def test_grouped_rows_behind_are_left(dev, ctxs, which, per):
     """Slots before the first expert's and behind the last expert's keep what
@@ -277,7 +285,7 @@ def test_grouped_rows_behind_are_left(dev, ctxs, which, per):
     assert (buf[:5 * N] == 5.5).all() and (buf[-7 * N:] == 5.5).all()
 
 
-@pytest.mark.parametrize("which", ["auto", "generic"])
+@pytest.mark.parametrize("which", ALL)
 @pytest.mark.parametrize("per", [3, 200])
 def test_grouped_rows_that_do_not_exist(dev, ctxs, which, per):
     """A slot whose row is outside x gets zeros, whatever the weights hold,
@@ -306,7 +314,7 @@ def test_grouped_offsets_out_of_range_stay_inside(dev, ctxs):
     S, N, H = 40, 64, 64
     x, w = integer((S, H), dev, 13), integer((4, N, H), dev, 14)
     for bad in ([-5, 10, 4, 100, 2 ** 31 - 1], [40, 30, 20, 10, 0], [0, 2 ** 31 - 1, 0, 0, 40]):
-        for which in ("auto", "generic"):
+        for which in ALL:
             buf = torch.full(((S + 4) * N,), 5.5, dtype=torch.bfloat16, device=dev)
             farn.grouped_matmul(x, w, torch.tensor(bad, dtype=torch.int32, device=dev),
                                 out=buf[2 * N:-2 * N].view(S, N), ctx=ctxs[which])
@@ -335,6 +343,68 @@ def test_grouped_same_bits_twice(dev):
     a = farn.grouped_matmul(x, w, offsets)
     for _ in range(3):
         assert torch.equal(farn.grouped_matmul(x, w, offsets), a)
+
+
+@pytest.mark.parametrize("which", ALL)
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_many_experts(dev, ctxs, which, gather):
+    """The most experts, most of them with a slot or none."""
+    E, N, H = 1024, 136, 72
+    counts = np.random.RandomState(3).choice([0, 0, 1, 2, 5, 130], size=E, p=[.3, .2, .3, .1, .08, .02])
+    offsets = make_groups(counts)
+    S = int(offsets[-1])
+    x = integer((S if not gather else 300, H), dev, 21)
+    w = integer((E, N, H), dev, 22)
+    rows = None
+    if gather:
+        g = torch.Generator(device=dev).manual_seed(23)
+        rows = torch.randint(0, 300, (S,), device=dev, generator=g, dtype=torch.int32)
+    got = farn.grouped_matmul(x, w, torch.from_numpy(offsets).to(dev), rows, ctx=ctxs[which])
+    want, _ = grouped_reference(x, w, offsets, rows, S)
+    check_exact(got, want, offsets, which)
+
+
+@pytest.mark.parametrize("which", ["pair", "one"])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_beyond_4_gib(dev, ctxs, which, gather):
+    """Rows of x and of the output whose byte offsets pass 32 bits."""
+    S, N, H = 70001, 32776, 32768
+    x = torch.zeros(S, H, dtype=torch.bfloat16, device=dev)
+    some = torch.tensor([0, 1, 32767, 65535, 65536, 65537, 69999, 70000], device=dev)
+    x[some] = integer((some.numel(), H), dev, 24)
+    w = torch.zeros(1, N, H, dtype=torch.bfloat16, device=dev)
+    wsome = torch.tensor([0, 5, 127, 128, 32767, 32775], device=dev)
+    w[0, wsome] = integer((wsome.numel(), H), dev, 25)
+    rows = torch.arange(S, device=dev, dtype=torch.int32).flip(0).contiguous() if gather else None
+    off = torch.tensor([0, S], dtype=torch.int32, device=dev)
+    got = farn.grouped_matmul(x, w, off, rows, ctx=ctxs[which])
+    want = (x[some].double() @ w[0, wsome].double().t()).float().to(torch.bfloat16)
+    at = S - 1 - some if gather else some
+    assert torch.equal(got[at][:, wsome], want)
+    assert int((got != 0).sum()) == int((want != 0).sum())
+    del x, w, got
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("env", [dict(FARN_TC_TILE=256), dict(FARN_TC_TILE=64, FARN_TC_SPLIT=1),
+                                 dict(FARN_TC_TILE=64, FARN_TC_SPLIT=4)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_waits_are_bounded(dev, env, gather):
+    """With FARN_FAULT_INJECT=stall the first CTA's weights never come: its
+    waits and those of the CTAs that work with it run out (2 s), the call
+    ends and the status word says so.  Other calls are unharmed."""
+    ctx = make_ctx(FARN_FAULT_INJECT="stall", **env)
+    offsets = torch.tensor([0, 70, 200], dtype=torch.int32, device=dev)
+    x, w = integer((200, 1024), dev, 26), integer((2, 512, 1024), dev, 27)
+    rows = torch.arange(200, device=dev, dtype=torch.int32) if gather else None
+    farn.grouped_matmul(x, w, offsets, rows, ctx=ctx)
+    torch.cuda.synchronize()
+    assert farn.farn_device_status(ctx.handle) & (16 | 32 | 64 | 128)
+    assert farn.farn_device_status(ctx.handle) == 0
+    ctx.close()
+    got = farn.grouped_matmul(x, w, offsets, rows)
+    want, _ = grouped_reference(x, w, offsets.cpu().numpy(), rows, 200)
+    check_exact(got, want, offsets, "after")
 
 
 # ------------------------------------------------------------- together

@@ -32,7 +32,14 @@ def O():
 
 @pytest.fixture(scope="module")
 def ctxs(dev):
-    return {"auto": farn.Context(0), "generic": make_ctx(FARN_VARIANT="generic")}
+    return {"auto": farn.Context(0), "generic": make_ctx(FARN_VARIANT="generic"),
+            "pair": make_ctx(FARN_TC_TILE=256),
+            "one": make_ctx(FARN_TC_TILE=64, FARN_TC_SPLIT=1),
+            "split2": make_ctx(FARN_TC_TILE=64, FARN_TC_SPLIT=2),
+            "split4": make_ctx(FARN_TC_TILE=64, FARN_TC_SPLIT=4)}
+
+
+ALL = ["auto", "generic", "pair", "one", "split2", "split4"]
 
 
 def values(codes, scales):
@@ -133,7 +140,7 @@ SHAPES = [(1, 1, 16), (1, 8, 32), (1, 128, 64), (2, 130, 96), (15, 127, 256), (1
           (449, 1030, 608), (1000, 300, 1024)]
 
 
-@pytest.mark.parametrize("which", ["auto", "generic"])
+@pytest.mark.parametrize("which", ALL)
 @pytest.mark.parametrize("T,N,H", SHAPES)
 def test_product_exact(dev, ctxs, which, T, N, H):
     """Scales 1, 2, 4 and 0: products are multiples of 1/4 and at most 576,
@@ -148,7 +155,7 @@ def test_product_exact(dev, ctxs, which, T, N, H):
     assert torch.equal(got, want.float().to(torch.bfloat16))
 
 
-@pytest.mark.parametrize("which", ["auto", "generic"])
+@pytest.mark.parametrize("which", ALL)
 @pytest.mark.parametrize("T,N,H", [(1, 512, 8192), (20, 300, 4096), (130, 260, 5120),
                                    (520, 300, 2080)])
 def test_product_rounding(dev, ctxs, which, T, N, H):
@@ -167,7 +174,7 @@ def test_product_rounding(dev, ctxs, which, T, N, H):
     assert ((got.double() - want).abs() <= tol).all()
 
 
-@pytest.mark.parametrize("which", ["auto", "generic"])
+@pytest.mark.parametrize("which", ALL)
 @pytest.mark.parametrize("T", [3, 300])
 def test_product_nan_scale_stays_with_its_row(dev, ctxs, which, T):
     N, H = 200, 512
@@ -197,6 +204,52 @@ def test_product_any_alignment_and_nothing_behind(dev, ctxs, T):
         want = (values(*a0) @ values(*b).t()).float().to(torch.bfloat16)
         assert torch.equal(out, want)
         assert (buf[:d] == 7.0).all() and (buf[d + T * N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("which", ["pair", "one", "split2"])
+@pytest.mark.parametrize("H", [256, 288])
+def test_product_scales_at_any_byte(dev, ctxs, which, H):
+    """Block scales that start at any byte, in rows of whole 16-byte pieces and
+    not; the bytes before and behind them would show as NaN."""
+    T, N = 70, 300
+    a, b = random_tensor(dev, T, H, 15, [0x38, 0x40]), random_tensor(dev, N, H, 16, [0x38, 0x40])
+    want = (values(*a) @ values(*b).t()).float().to(torch.bfloat16)
+    for d in (0, 1, 2, 3, 4, 6, 15):
+        def moved(t):
+            buf = torch.full((t.numel() + 32,), 0x7F, dtype=torch.uint8, device=dev)
+            v = buf[d:d + t.numel()].view(t.shape)
+            v.copy_(t)
+            return v
+        got = farn.nvfp4_matmul(a[0], moved(a[1]), 1.0, b[0], moved(b[1]), 1.0, ctx=ctxs[which])
+        assert torch.equal(got, want), d
+
+
+@pytest.mark.parametrize("which", ["pair", "one"])
+def test_product_beyond_4_gib(dev, ctxs, which):
+    """Output rows whose byte offsets pass 32 bits."""
+    T, N, H = 70001, 32776, 64
+    a, b = random_tensor(dev, T, H, 17, [0x38]), random_tensor(dev, N, H, 18, [0x38])
+    got = farn.nvfp4_matmul(*a, 1.0, *b, 1.0, ctx=ctxs[which])
+    some = torch.tensor([0, 65535, 65536, 69999, 70000], device=dev)
+    want = (values(a[0][some], a[1][some]) @ values(*b).t()).float().to(torch.bfloat16)
+    assert torch.equal(got[some], want)
+    del got
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("env", [dict(FARN_TC_TILE=256), dict(FARN_TC_TILE=64, FARN_TC_SPLIT=2)])
+@pytest.mark.parametrize("H", [2048, 2080])
+def test_product_waits_are_bounded(dev, env, H):
+    """As for the grouped product, with both ways the block scales come."""
+    ctx = make_ctx(FARN_FAULT_INJECT="stall", **env)
+    a, b = random_tensor(dev, 300, H, 19, [0x38]), random_tensor(dev, 600, H, 20, [0x38])
+    farn.nvfp4_matmul(*a, 1.0, *b, 1.0, ctx=ctx)
+    torch.cuda.synchronize()
+    assert farn.farn_device_status(ctx.handle) & (16 | 32 | 64 | 128)
+    ctx.close()
+    got = farn.nvfp4_matmul(*a, 1.0, *b, 1.0)
+    want = (values(*a) @ values(*b).t()).float().to(torch.bfloat16)
+    assert torch.equal(got, want)
 
 
 def test_norm_to_product(dev):
