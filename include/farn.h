@@ -82,11 +82,12 @@ typedef struct farn_ctx farn_ctx;
  * as it was.  The environment is read here and only here: FARN_VARIANT,
  * FARN_CLUSTER, FARN_VPT, FARN_PDL, FARN_SMALL_T, FARN_BULK,
  * FARN_BULK_CTAS, FARN_STAGE, FARN_STAGE_R, FARN_STAGE_CTAS,
- * FARN_STAGE_MIN_T and FARN_STAGE_MIN_MB override the kernel choice (tests
- * and sweeps); FARN_FAULT_INJECT injects a fault for the tests: "create"
+ * FARN_STAGE_MIN_T, FARN_STAGE_MIN_MB, FARN_TC_TILE and FARN_TC_SPLIT override
+ * the kernel choice (tests and sweeps); FARN_FAULT_INJECT injects a fault for the tests: "create"
  * fails this call, "launch" makes every launch of the context fail before
  * anything is enqueued, "stall" makes CTA 0 of every TMA-staged launch
- * wait out its time limit and report it in the status word.
+ * wait out its time limit and report it in the status word (of the
+ * tensor-core products: its weights never come).
  * Returns FARN_ERR_INVALID_ARG if out is NULL or device < 0 or not a device
  * of this process, FARN_ERR_CUDA if the device cannot be queried (or
  * FARN_FAULT_INJECT=create), FARN_ERR_NOMEM. */
@@ -148,7 +149,9 @@ int farn_check_args(const void *const *partials, int W,
  * non-zero value has one bit per kind of wait that gave up after its time
  * limit (2 s): 1 a consumer waiting for a staged segment, 2 the producer
  * waiting for a free stage, 4 a consumer in the row reduction, 8 the
- * producer draining its copies.  The kernel that gave up left its outputs
+ * producer draining its copies; in the products' tensor-core kernels 16 the
+ * wait for operands, 32 for a free stage, 64 for a finished tile, 128 for the
+ * other parts of a split row.  The kernel that gave up left its outputs
  * incomplete.  The TMA-staged kernel runs where farn_plan /
  * farn_plan_moe_combine report variant 3, and in every
  * farn_forward_noalloc call.  Returns FARN_ERR_INVALID_ARG or FARN_ERR_CUDA

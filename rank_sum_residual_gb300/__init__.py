@@ -9,8 +9,11 @@ RMSNorm tutorial" (Summary; Implementation sections 2-3), computed by the
 hand-written CUDA kernels of ``libfarn.so``.  This module is the Python
 binding of that library's C ABI (``include/farn.h``): the ``farn_*``
 functions have the C names and arguments and only marshal them through
-ctypes; ``forward`` is the same call for torch tensors.  Every arithmetic
-step runs in the CUDA kernels.  There is no CPU fallback: if the library
+ctypes; ``forward`` is the same call for torch tensors.  Next to it stand
+the operators of an expert layer and of NVFP4 projections that its outputs
+go through: ``moe_route``, ``grouped_matmul`` and ``moe_combine``;
+``nvfp4_quantize``, ``nvfp4_dequantize`` and ``nvfp4_matmul``.  Every
+arithmetic step runs in the CUDA kernels.  There is no CPU fallback: if the library
 is not built, every call raises.
 """
 from __future__ import annotations
@@ -578,18 +581,24 @@ def moe_combine(expert_out, index, gates, residual, weight, eps: float, out=None
                                stream)()
 
 
-# The calls below check their tensors on a short path (a serving step makes
-# several of them per layer, and their kernels take a few microseconds); a
-# tensor that it turns down goes through _check_tensor for the message.
+# The calls below check their tensors on a short path, one expression without
+# calls of its own (a serving step makes several of them per layer, and their
+# kernels take a few microseconds); what it turns down goes through
+# _check_tensor for the message.
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _raw_stream(stream, index):
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
-def _fits(t, dtype, index, shape):
-    return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()
+    return _torch._C._cuda_getCurrentRawStream(index)
 
 
 def _call(fn, args, name):
@@ -599,11 +608,12 @@ def _call(fn, args, name):
 
 
 def _moe_route_args(logits, top_k, renormalize, out, ctx, stream):
-    import torch
+    torch = _torch or _load_torch()
     i32, f32 = torch.int32, torch.float32
-    if logits.dim() != 2:
+    sl = logits.shape
+    if len(sl) != 2:
         raise ValueError("logits must be [T, E]")
-    T, E = logits.shape
+    T, E = sl
     K, index = int(top_k), logits.get_device()
     if index < 0 or not logits.is_contiguous() or logits.dtype not in (torch.bfloat16, f32):
         _check_tensor(logits, "logits", (T, E), logits.device, (torch.bfloat16, f32))
@@ -613,9 +623,10 @@ def _moe_route_args(logits, top_k, renormalize, out, ctx, stream):
         raise ValueError(f"top_k must be 1..{min(E, FARN_MAX_W)}, got {K}")
     if out is None:
         dev = logits.device
-        out = (torch.empty((T, K), dtype=i32, device=dev),
-               torch.empty((T, K), dtype=f32, device=dev),
-               torch.empty((T, K), dtype=i32, device=dev),
+        pairs = (T, K)
+        out = (torch.empty(pairs, dtype=i32, device=dev),
+               torch.empty(pairs, dtype=f32, device=dev),
+               torch.empty(pairs, dtype=i32, device=dev),
                torch.empty((T * K,), dtype=i32, device=dev),
                torch.empty((E + 1,), dtype=i32, device=dev))
     else:
@@ -627,6 +638,8 @@ def _moe_route_args(logits, top_k, renormalize, out, ctx, stream):
                                       (i32, f32, i32, i32, i32)):
             _check_tensor(t, name, shape, logits.device, (dt,))
     c = ctx if ctx is not None else _context_for(index)
+    if c.device != index:
+        raise ValueError(f"the context is for device {c.device}, the tensors are on {index}")
     return (c.handle, logits.data_ptr(), FARN_F32 if logits.dtype is f32 else FARN_BF16, T, E, K,
             1 if renormalize else 0, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
             out[3].data_ptr(), out[4].data_ptr(), _raw_stream(stream, index)), out, c
@@ -651,30 +664,35 @@ def moe_route(logits, top_k: int, renormalize: bool = True, out=None, ctx=None, 
 
 
 def _grouped_args(x, weights, offsets, rows, out, ctx, stream):
-    import torch
+    torch = _torch or _load_torch()
     bf, i32 = torch.bfloat16, torch.int32
-    if x.dim() != 2 or weights.dim() != 3:
+    sx, sw, index = x.shape, weights.shape, x.get_device()
+    if len(sx) != 2 or len(sw) != 3:
         raise ValueError("x must be [rows, H] and weights [E, N, H]")
-    n_rows, H = x.shape
-    E, N, HW = weights.shape
-    index = x.get_device()
-    if (index < 0 or HW != H or x.dtype is not bf or not x.is_contiguous() or
-            not _fits(weights, bf, index, (E, N, H)) or
-            not _fits(offsets, i32, index, (E + 1,))):
+    n_rows, H = sx
+    E, N, HW = sw
+    if not (HW == H and index >= 0 and weights.get_device() == index and
+            offsets.get_device() == index and x.dtype is bf and weights.dtype is bf and
+            offsets.dtype is i32 and offsets.shape == (E + 1,) and x.is_contiguous() and
+            weights.is_contiguous() and offsets.is_contiguous()):
         dev = x.device
         _check_tensor(x, "x", (n_rows, H), dev)
         _check_tensor(weights, "weights", (E, N, H), dev)
         _check_tensor(offsets, "offsets", (E + 1,), dev, (i32,))
     S = n_rows
     if rows is not None:
-        S = rows.shape[0] if rows.dim() == 1 else -1
-        if not _fits(rows, i32, index, (S,)):
+        sr = rows.shape
+        S = sr[0] if len(sr) == 1 else -1
+        if not (S >= 0 and rows.dtype is i32 and rows.get_device() == index and
+                rows.is_contiguous()):
             _check_tensor(rows, "rows", (S,), x.device, (i32,))
     if out is None:
         out = torch.empty((S, N), dtype=bf, device=x.device)
-    elif not _fits(out, bf, index, (S, N)):
+    else:
         _check_tensor(out, "out", (S, N), x.device)
     c = ctx if ctx is not None else _context_for(index)
+    if c.device != index:
+        raise ValueError(f"the context is for device {c.device}, the tensors are on {index}")
     return (c.handle, x.data_ptr(), n_rows, None if rows is None else rows.data_ptr(), S,
             weights.data_ptr(), E, offsets.data_ptr(), N, H, out.data_ptr(),
             _raw_stream(stream, index)), out, c
@@ -699,29 +717,30 @@ def grouped_matmul(x, weights, offsets, rows=None, out=None, ctx=None, stream=No
 
 
 def _nvfp4_shape(codes, scales, name):
-    import torch
-    if codes.dim() != 2:
+    torch = _torch or _load_torch()
+    sc = codes.shape
+    if len(sc) != 2:
         raise ValueError(f"{name} must be [rows, H/2]")
-    T, half = codes.shape
-    H = half * 2
-    if H % 16:
-        raise ValueError(f"NVFP4 needs H % 16 == 0, got H = {H}")
+    T, half = sc
+    if half % 8:
+        raise ValueError(f"NVFP4 needs H % 16 == 0, got H = {half * 2}")
     u8, index = torch.uint8, codes.get_device()
-    if (index < 0 or codes.dtype is not u8 or not codes.is_contiguous() or
-            not _fits(scales, u8, index, (T, H // 16))):
+    if not (index >= 0 and scales.get_device() == index and codes.dtype is u8 and
+            scales.dtype is u8 and scales.shape == (T, half // 8) and codes.is_contiguous() and
+            scales.is_contiguous()):
         _check_tensor(codes, name, (T, half), codes.device, (u8,))
-        _check_tensor(scales, name + " scales", (T, H // 16), codes.device, (u8,))
-    return T, H, index
+        _check_tensor(scales, name + " scales", (T, half // 8), codes.device, (u8,))
+    return T, half * 2, index
 
 
 def _quantize_args(x, tensor_scale, out, ctx, stream):
-    import torch
+    torch = _torch or _load_torch()
     u8 = torch.uint8
-    if x.dim() != 2:
+    sx, index = x.shape, x.get_device()
+    if len(sx) != 2:
         raise ValueError("x must be [T, H]")
-    T, H = x.shape
-    index = x.get_device()
-    if index < 0 or x.dtype is not torch.bfloat16 or not x.is_contiguous():
+    T, H = sx
+    if not (index >= 0 and x.dtype is torch.bfloat16 and x.is_contiguous()):
         _check_tensor(x, "x", (T, H), x.device)
     if H % 16:
         raise ValueError(f"NVFP4 needs H % 16 == 0, got H = {H}")
@@ -736,6 +755,8 @@ def _quantize_args(x, tensor_scale, out, ctx, stream):
         _check_tensor(out[0], "codes", (T, H // 2), x.device, (u8,))
         _check_tensor(out[1], "scales", (T, H // 16), x.device, (u8,))
     c = ctx if ctx is not None else _context_for(index)
+    if c.device != index:
+        raise ValueError(f"the context is for device {c.device}, the tensors are on {index}")
     return (c.handle, x.data_ptr(), T, H, tensor_scale, out[0].data_ptr(), out[1].data_ptr(),
             _raw_stream(stream, index)), out, c
 
@@ -756,13 +777,15 @@ def nvfp4_quantize(x, tensor_scale: float, out=None, ctx=None, stream=None):
 
 
 def _dequantize_args(codes, block_scale, tensor_scale, out, ctx, stream):
-    import torch
+    torch = _torch or _load_torch()
     T, H, index = _nvfp4_shape(codes, block_scale, "codes")
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=codes.device)
-    elif not _fits(out, torch.bfloat16, index, (T, H)):
+    else:
         _check_tensor(out, "out", (T, H), codes.device)
     c = ctx if ctx is not None else _context_for(index)
+    if c.device != index:
+        raise ValueError(f"the context is for device {c.device}, the tensors are on {index}")
     return (c.handle, codes.data_ptr(), block_scale.data_ptr(), T, H, tensor_scale,
             out.data_ptr(), _raw_stream(stream, index)), out, c
 
@@ -784,21 +807,35 @@ def nvfp4_dequantize(codes, block_scale, tensor_scale: float, out=None, ctx=None
 
 def _nvfp4_matmul_args(a_codes, a_scale, a_tensor_scale, b_codes, b_scale, b_tensor_scale, out,
                        ctx, stream):
-    import torch
-    T, H, index = _nvfp4_shape(a_codes, a_scale, "a_codes")
-    N, HB, index_b = _nvfp4_shape(b_codes, b_scale, "b_codes")
-    if HB != H:
-        raise ValueError(f"a and b must have the same H, got {H} and {HB}")
-    if index_b != index:
-        raise ValueError(f"b_codes must be on {a_codes.device}, got {b_codes.device}")
+    torch = _torch or _load_torch()
+    u8, bf = torch.uint8, torch.bfloat16
+    index = a_codes.get_device()
+    sa, sb = a_codes.shape, b_codes.shape
+    half = sa[-1] if sa else 0
+    if not (len(sa) == 2 and len(sb) == 2 and half % 8 == 0 and sb[1] == half and index >= 0 and
+            b_codes.get_device() == index and a_scale.get_device() == index and
+            b_scale.get_device() == index and a_codes.dtype is u8 and b_codes.dtype is u8 and
+            a_scale.dtype is u8 and b_scale.dtype is u8 and
+            a_scale.shape == (sa[0], half // 8) and b_scale.shape == (sb[0], half // 8) and
+            a_codes.is_contiguous() and b_codes.is_contiguous() and a_scale.is_contiguous() and
+            b_scale.is_contiguous()):
+        _, H, _ = _nvfp4_shape(a_codes, a_scale, "a_codes")
+        _, HB, index_b = _nvfp4_shape(b_codes, b_scale, "b_codes")
+        if HB != H:
+            raise ValueError(f"a and b must have the same H, got {H} and {HB}")
+        if index_b != index:
+            raise ValueError(f"b_codes must be on {a_codes.device}, got {b_codes.device}")
+    T, N = sa[0], sb[0]
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=a_codes.device)
-    elif not _fits(out, torch.bfloat16, index, (T, N)):
+        out = torch.empty((T, N), dtype=bf, device=a_codes.device)
+    else:
         _check_tensor(out, "out", (T, N), a_codes.device)
     c = ctx if ctx is not None else _context_for(index)
+    if c.device != index:
+        raise ValueError(f"the context is for device {c.device}, the tensors are on {index}")
     return (c.handle, a_codes.data_ptr(), a_scale.data_ptr(), a_tensor_scale,
-            b_codes.data_ptr(), b_scale.data_ptr(), b_tensor_scale, T, N, H, out.data_ptr(),
-            _raw_stream(stream, index)), out, c
+            b_codes.data_ptr(), b_scale.data_ptr(), b_tensor_scale, T, N, half * 2,
+            out.data_ptr(), _raw_stream(stream, index)), out, c
 
 
 def prepare_nvfp4_matmul(a_codes, a_scale, a_tensor_scale: float, b_codes, b_scale,

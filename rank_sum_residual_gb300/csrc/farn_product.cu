@@ -188,8 +188,8 @@ bool encode(const farn_ctx* ctx, CUtensorMap* map, bool fp4, const void* base, i
          CUDA_SUCCESS;
 }
 
-// Block scales: 32 bytes (512 elements) of 128 rows, written with the 32-byte
-// swizzle.
+// Block scales: 64 bytes (1024 elements) of 128 rows, written with the
+// 64-byte swizzle.
 bool encode_scales(const farn_ctx* ctx, CUtensorMap* map, const void* base, int64_t pitch,
                    int64_t rows) {
   const cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)rows};
@@ -219,9 +219,8 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
   t.p = p;
   t.stages = pl.stages;
   t.ks = pl.ks;
-  t.store_bytes = p.N % 8 == 0 && aligned16(p.out)                      ? 16
-                  : p.N % 2 == 0 && ((uintptr_t)p.out & 3u) == 0 ? 4
-                                                                 : 2;
+  const uint64_t at = (uint64_t)(uintptr_t)p.out | (uint64_t)p.N * 2;   // of every row
+  t.store_bytes = at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : at % 4 == 0 ? 4 : 2;
   t.groups_at = pl.groups_at;
   t.scales_at = pl.scales_at;
   t.barriers_at = pl.barriers_at;

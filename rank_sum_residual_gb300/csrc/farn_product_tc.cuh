@@ -1,27 +1,38 @@
 // The products on the tensor cores.
 //
 // The weights are the matrix instruction's M side (128 rows per CTA) and the
-// slots its N side, so that a tile's slots can be any multiple of 16 up to
-// BN: a group's ragged end costs what it has, and a decoding batch of a few
-// rows still streams full tiles of weights.  The accumulator is transposed
-// on the way out.
+// slots its N side, so that a tile's slots can be any multiple of 16 (32) up
+// to BN: a group's ragged end costs what it has, and a decoding batch of a few
+// rows still streams full tiles of weights.  The accumulator is turned over on
+// the way out.
 //
-// A CTA has a producer warp (TMA), a warp that issues the matrix
-// instructions, four epilogue warps, and for NVFP4 four warps that bring the
-// block scales into the layout the tensor cores read, or for a gathering call
-// four warps that copy the slots' rows (cp.async: a TMA gather of four rows of
-// 128 bytes took 95 cycles, 3 times the matrix instructions' time).  The ring of stages runs on across
-// tiles, and two accumulators let the epilogue of one tile overlap the
-// products of the next.
+//   CG = 2  pairs of CTAs share a tile of 256 weights by 256 slots (NVFP4:
+//           224, so that two accumulators and the scales fit the tensor
+//           memory), each holding half of the slots' rows: long calls
+//   CG = 1  one CTA per tile of 128 weights by 64 slots; up to four CTAs of a
+//           cluster split the row and join their accumulators, in rank order,
+//           through distributed shared memory: short calls
 //
-//   CG = 2  pairs of CTAs share a tile of 256 weights, each holding half of
-//           the slots' rows: long calls, bound by the tensor cores
-//   CG = 1  one CTA per tile of 128 weights; `ks` CTAs of a cluster may split
-//           the row and join their accumulators, in rank order, through
-//           distributed shared memory: short calls, bound by reading weights
+// Warps of a CTA: four for the epilogue, one that has TMA fetch the weights,
+// one that issues the matrix instructions, one that has TMA fetch the slots'
+// rows; or, for a gathering call, six that copy the rows themselves (a TMA
+// gather of four rows of 128 bytes took 95 cycles, three times the matrix
+// instructions' time); for NVFP4 also those that bring the block scales into
+// the layout the tensor cores read.  The ring of stages (128 bytes of every
+// row) runs on across tiles, and two accumulators let the epilogue of one tile
+// overlap the products of the next.
 //
-// Every wait is bounded (see wait_phase); a CTA that gives up sets its bit in
-// the status word, waits for its own copies and leaves.
+// What bounds it (GB300, us and rates of the kernel alone): bf16 8192^3 takes
+// 545 us (2.02 PFLOP/s, 105 % of the measured library rate) with the tensor
+// pipe 93 % busy, under the power limit; NVFP4 8192^3 172 us (6.4 PFLOP/s), 69 %
+// busy: a stage's synchronisation takes about 600 cycles, its products 450.
+// 64 experts of 64 tokens, 2048 -> 7168: 279 us, the weights at 6.8 TB/s (101 %
+// of the measured copy rate).  One token, 8 experts, 7168 -> 2048: 41 us
+// (86 %).  One token, NVFP4 8192 x 8192: 13 us against 5.6 us for its bytes:
+// launch, first loads and the join of the split rows.
+//
+// Every wait is bounded (see tc_wait); a CTA that gives up sets its bit in the
+// status word, waits for its own copies and leaves.
 #pragma once
 
 #include <cuda.h>
@@ -40,11 +51,11 @@ constexpr int kTcWeights = 128;        // weights per CTA and tile
 // be within one round of the ring, or the parity of the phase it waits for
 // says nothing.
 constexpr int kTcAuxGather = 6;
-// NVFP4: block scales come for two stages at a time (32 bytes of a row), in
+// NVFP4: block scales come for four stages at a time (64 bytes of a row), in
 // blocks of 128 rows (one of weights, the others of slots) that lie in a ring
-// of four slots of their own.  With two slots of four stages a group's copy
-// could only be asked for one group ahead, and its latency with the turning
-// (about 2500 cycles) was four stages' time: 8192^3 178 us.
+// of two slots of their own.  Four slots of two stages each cost the matrix
+// warp more hand-overs (8192^3: 184 us against 172), three slots of four left
+// the ring a stage less (181 against 179).
 // Further warps to a block: one if TMA brings it, else (COPY) four, of 32 rows
 // each (two of 64 rows took longer for the shifting than the products).
 constexpr int kTcScaleStages = 4;
@@ -61,7 +72,7 @@ struct TcParams {
   ProductParams p;
   int stages;
   int ks;            // CTAs of a cluster that split the row (CG = 1)
-  int store_bytes;   // 16, 4 or 2: what N and out allow a store of a row to be
+  int store_bytes;   // 16, 8, 4 or 2: what N and out allow a store of a row to be
   uint32_t groups_at;  // shared-memory offsets
   uint32_t scales_at;  // NVFP4: the slots of block scales
   uint32_t barriers_at;
@@ -135,7 +146,8 @@ __device__ __forceinline__ SlotRows slot_rows(const Tile& w, int w_rank) {
 }
 
 // Bounded phase wait.  JOIN: what other CTAs of the cluster wrote before they
-// arrived is read afterwards.
+// arrived is read afterwards.  A waiting thread sleeps: nine warps polling took
+// the matrix warp's issue slots (bf16 8192^3 768 us).
 constexpr uint32_t kTcSleepNs = 1000000;
 
 template <bool JOIN = false>
@@ -179,11 +191,11 @@ __device__ __forceinline__ bool tc_wait_warp(uint32_t bar, uint32_t parity,
 
 // Block scales in shared memory, as the tensor cores read them: 128 rows by
 // 4 bytes (64 elements) are an atom of 512 bytes, in which row r's four bytes
-// are word r / 32 of the 16-byte entry r % 32.  A block of 128 rows by 32
-// bytes is 8 atoms, in the order of the row.
+// are word r / 32 of the 16-byte entry r % 32.  A block of 128 rows by 64
+// bytes is 16 atoms, in the order of the row.
 //
-// A block that TMA wrote as it lies in memory (32-byte rows under the 32-byte
-// swizzle, which moves 16-byte piece q of row r to q ^ (r / 4 % 2)), turned
+// A block that TMA wrote as it lies in memory (64-byte rows under the 64-byte
+// swizzle, which moves 16-byte piece q of row r to q ^ (r / 2 % 4)), turned
 // into atoms in place by one warp: lane l holds the rows l, l + 32, ...
 __device__ __forceinline__ void turn_scales(unsigned char* block, int lane) {
   uint4 v[4][4];
@@ -218,8 +230,8 @@ __device__ __noinline__ uint4 load_within(uintptr_t at, uintptr_t lo, uintptr_t 
 }
 
 // 32 rows of a block whose rows in memory start at any byte (H not a multiple
-// of 256), by one warp: three lanes read the three aligned 16-byte pieces that
-// 32 bytes can touch, ten rows to a load and all four loads in flight; the
+// of 256), by one warp: five lanes read the five aligned 16-byte pieces that
+// 64 bytes can touch, six rows to a load and all six loads in flight; the
 // words are then shifted into place with the next lane's first.
 struct ScaleRows {
   const uint8_t* src;    // the first of the rows
@@ -325,6 +337,9 @@ __device__ __forceinline__ void store_turned(const TcParams& t, uint32_t tmem, u
       uint16_t* o = static_cast<uint16_t*>(p.out) + (slot + s) * p.N + col;
       if (t.store_bytes == 16) {
         *reinterpret_cast<uint4*>(o) = w[i];
+      } else if (t.store_bytes == 8) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(w[i].x, w[i].y);
+        if (col + 4 < p.N) reinterpret_cast<uint2*>(o)[1] = make_uint2(w[i].z, w[i].w);
       } else {
         const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
@@ -423,8 +438,6 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
 
   if (warp == 4) {
     // ------------------------------------------------- weights' producer
-    // The slots' rows have a producer of their own: one warp for both took
-    // 640 cycles per stage to issue them, more than the NVFP4 products take.
     const uint32_t bar0 = tc::map_rank(full0, CG == 2 ? 0 : rank);
     RingPos at;
     uint32_t armed = 0;        // stages given to TMA, all but the last NS done
@@ -777,7 +790,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
   if constexpr (GATHER) {
     if (warp >= Sh::kFirstAux) {
       // ------------------------------------------------------ gathered rows
-      // Warp i takes every sixth stage, so that a stage's copies have the whole
+      // A warp takes every sixth stage, so that a stage's copies have the whole
       // ring's time to land.  Eight lanes copy a row's 128 bytes, in the
       // swizzled layout that TMA would write: 16-byte column j of row r at
       // j ^ (r & 7).  Lane l knows the rows l, l + 32, l + 64 and l + 96.

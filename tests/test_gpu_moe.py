@@ -187,7 +187,8 @@ GROUPS = [
     ([17, 15, 1], 130, 136), ([31, 33, 32], 256, 200), ([64, 65, 63], 257, 320),
     ([0, 127, 129, 0, 128], 300, 264), ([255, 257, 0, 256, 1], 384, 512),
     ([300, 5, 0, 700], 512, 1032), ([2050], 264, 128), ([1] * 100, 200, 256),
-    ([2, 1, 0, 3] * 16, 640, 2048), ([9, 4], 1, 4096),
+    ([2, 1, 0, 3] * 16, 640, 2048), ([9, 4], 1, 4096), ([40, 300], 260, 128),
+    ([70, 1], 258, 128), ([70, 1], 259, 128),
 ]
 
 
@@ -498,6 +499,18 @@ def test_moe_layer_in_a_graph_and_on_streams(dev):
     for n, r in enumerate(results):
         for a, b in zip(r, eager[n % 2]):
             assert torch.equal(a, b)
+
+
+def test_context_of_another_device_is_refused(dev):
+    x, logits, up, *_ = layer_inputs(dev, 4, 4, 64, 64, 1)
+    off = torch.tensor([0, 1, 2, 3, 4], dtype=torch.int32, device=dev)
+    other = farn.Context(0)
+    other.device = 1
+    for call in (lambda: farn.moe_route(logits, 2, ctx=other),
+                 lambda: farn.grouped_matmul(x, up, off, ctx=other),
+                 lambda: farn.nvfp4_quantize(x, 1.0, ctx=other)):
+        with pytest.raises(ValueError, match="device"):
+            call()
 
 
 def test_launch_fault_reaches_the_caller(dev):
