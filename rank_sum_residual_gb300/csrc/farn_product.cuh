@@ -31,8 +31,8 @@ struct ProductParams {
 
 // The groups' slots and tiles, in shared memory: first[e] .. first[e] +
 // count[e] - 1 are the slots of group e, tile[e] the number of slot tiles
-// before it.  Offsets are clamped to 0..S and to be ascending, so that no
-// value of them leads outside the tensors.
+// before it.  Offsets are clamped to 0..S and to what came before them, so
+// that the groups are disjoint and no value of them leads outside the tensors.
 struct Groups {
   int32_t* first;   // [E]
   int32_t* count;   // [E]
@@ -46,32 +46,41 @@ __device__ __forceinline__ Groups groups_at(void* smem, int E) {
 
 // By all threads of the block (a multiple of 32, at least 64).
 __device__ __forceinline__ void load_groups(const Groups& g, const ProductParams& p, int bn) {
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
-  for (int e = tid; e < p.E; e += nt) {
-    int64_t lo = 0, hi = p.S;
-    if (p.offsets) {
-      lo = min(max((int64_t)p.offsets[e], (int64_t)0), p.S);
-      hi = min(max((int64_t)p.offsets[e + 1], lo), p.S);
-    }
-    g.first[e] = (int32_t)lo;
-    g.count[e] = (int32_t)(hi - lo);
-  }
+  const int tid = threadIdx.x, lane = tid & 31;
+  // the end of every group first: the loads of all are in flight together
+  for (int e = tid; e < p.E; e += blockDim.x)
+    g.count[e] = (int32_t)(p.offsets ? min(max((int64_t)p.offsets[e + 1], (int64_t)0), p.S) : p.S);
+  int32_t end =
+      (int32_t)(p.offsets ? min(max((int64_t)p.offsets[0], (int64_t)0), p.S) : (int64_t)0);
   __syncthreads();
-  if (tid < 32) {   // a warp scans the tile counts, 32 groups at a time
-    int32_t at = 0;
+  if (tid < 32) {   // a warp scans the ends (their maximum) and the tiles, 32 groups at a time
+    int32_t tiles = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      const int32_t n = e < p.E ? (int32_t)(((int64_t)g.count[e] + bn - 1) / bn) : 0;
+      int32_t hi = max(end, e < p.E ? g.count[e] : 0);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xFFFFFFFFu, hi, o);
+        if (lane >= o) hi = max(hi, y);
+      }
+      int32_t lo = __shfl_up_sync(0xFFFFFFFFu, hi, 1);
+      if (lane == 0) lo = end;
+      const int32_t n = e < p.E ? (int32_t)(((int64_t)hi - lo + bn - 1) / bn) : 0;
       int32_t inc = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
         if (lane >= o) inc += y;
       }
-      if (e < p.E) g.tile[e] = at + inc - n;
-      at += __shfl_sync(0xFFFFFFFFu, inc, 31);
+      if (e < p.E) {
+        g.first[e] = lo;
+        g.count[e] = hi - lo;
+        g.tile[e] = tiles + inc - n;
+      }
+      end = __shfl_sync(0xFFFFFFFFu, hi, 31);
+      tiles += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
-    if (lane == 0) g.tile[p.E] = at;
+    if (lane == 0) g.tile[p.E] = tiles;
   }
   __syncthreads();
 }

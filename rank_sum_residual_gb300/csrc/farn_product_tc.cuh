@@ -117,14 +117,12 @@ struct TcShape {
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kScaleSlot = FP4 ? kTcScaleBlock * (1 + kSlotBlocks) : 0;
   static constexpr int kScaleCols = FP4 ? 16 * (1 + kSlotBlocks) : 0;
-  // the epilogue reads 32 columns at a time
-  static constexpr int kColsUsed = (2 * BN + kScaleCols) < BN + 32 ? BN + 32 : 2 * BN + kScaleCols;
-  static constexpr int kCols = kColsUsed <= 32 ? 32 : kColsUsed <= 64 ? 64
-                               : kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
+  static constexpr int kColsUsed = 2 * BN + kScaleCols;
+  static constexpr int kCols = kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
   static constexpr int kChunk = FP4 ? 256 : 64;              // elements of a row per stage
   static constexpr int kMapStep = FP4 ? kTcRowBytes : kChunk;  // the same in map elements
   static constexpr int kStep = 16 * CG;                      // granularity of a tile's slots
-  static_assert(kColsUsed <= 512 && kBBytes % 1024 == 0, "");
+  static_assert(kColsUsed <= 512 && kBBytes % 1024 == 0 && BN % 32 == 0, "");
 };
 
 // A tile's slots as one CTA's part of the matrix instruction's N side.
@@ -257,7 +255,8 @@ __device__ __forceinline__ void load_scale_rows(uint4* v, const ScaleRows& b, in
       const int k = i * kScaleRows + sub;
       v[i] = make_uint4(0u, 0u, 0u, 0u);
       const uintptr_t a = first + k * pitch, at = (a & ~(uintptr_t)15) + piece * 16;
-      if (sub < kScaleRows && k < b.rows && at < a + lim) v[i] = __ldg(reinterpret_cast<const uint4*>(at));
+      if (sub < kScaleRows && k < b.rows && at < a + lim)
+        v[i] = __ldg(reinterpret_cast<const uint4*>(at));
     }
   } else {
 #pragma unroll
@@ -292,7 +291,8 @@ __device__ __forceinline__ void put_scale_rows(unsigned char* block, const uint4
       uint32_t word = __funnelshift_r(w[j], w[j + 1], by);
       if (lim < kTcScaleRow && at + 4 > lim)
         word = at >= lim ? 0u : word & ((1u << (8 * (lim - at))) - 1u);
-      if (mine && (uint32_t)at < (uint32_t)kTcScaleRow) *reinterpret_cast<uint32_t*>(block + to + 512 * j) = word;
+      if (mine && (uint32_t)at < (uint32_t)kTcScaleRow)
+        *reinterpret_cast<uint32_t*>(block + to + 512 * j) = word;
     }
   }
 }

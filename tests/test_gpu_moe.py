@@ -314,7 +314,8 @@ def test_grouped_offsets_out_of_range_stay_inside(dev, ctxs):
     outside the output is written."""
     S, N, H = 40, 64, 64
     x, w = integer((S, H), dev, 13), integer((4, N, H), dev, 14)
-    for bad in ([-5, 10, 4, 100, 2 ** 31 - 1], [40, 30, 20, 10, 0], [0, 2 ** 31 - 1, 0, 0, 40]):
+    for bad in ([-5, 10, 4, 100, 2 ** 31 - 1], [40, 30, 20, 10, 0], [0, 2 ** 31 - 1, 0, 0, 40],
+                [0, 40, 0, 40, 0], [-2 ** 31, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, 7]):
         for which in ALL:
             buf = torch.full(((S + 4) * N,), 5.5, dtype=torch.bfloat16, device=dev)
             farn.grouped_matmul(x, w, torch.tensor(bad, dtype=torch.int32, device=dev),
