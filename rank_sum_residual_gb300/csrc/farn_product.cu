@@ -220,7 +220,7 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
   t.stages = pl.stages;
   t.ks = pl.ks;
   const uint64_t at = (uint64_t)(uintptr_t)p.out | (uint64_t)p.N * 2;   // of every row
-  t.store_bytes = at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : at % 4 == 0 ? 4 : 2;
+  t.store_bytes = at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : 2;
   t.groups_at = pl.groups_at;
   t.scales_at = pl.scales_at;
   t.barriers_at = pl.barriers_at;

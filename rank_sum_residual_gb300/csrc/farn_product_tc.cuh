@@ -72,7 +72,7 @@ struct TcParams {
   ProductParams p;
   int stages;
   int ks;            // CTAs of a cluster that split the row (CG = 1)
-  int store_bytes;   // 16, 8, 4 or 2: what N and out allow a store of a row to be
+  int store_bytes;   // 16, 8 or 2: what N and out allow a store of a row to be
   uint32_t groups_at;  // shared-memory offsets
   uint32_t scales_at;  // NVFP4: the slots of block scales
   uint32_t barriers_at;
@@ -300,7 +300,7 @@ __device__ __forceinline__ void put_scale_rows(unsigned char* block, const uint4
 // Up to 32 slots by the warp's 32 weights, from the accumulator's columns at
 // `tmem` to rows of the output.  The accumulator has a weight per lane; the
 // warp turns it over in shared memory, two slots to a word, and writes runs
-// of eight weights (about 110 instructions for 1024 values; one warp per
+// of eight weights if rows are so aligned (about 110 instructions for 1024 values; one warp per
 // scheduler issues one in 4 to 5 cycles, so their number is the time).
 // n: slots; live: those whose row exists; first: the warp's first weight.
 template <bool GATHER>
@@ -312,6 +312,21 @@ __device__ __forceinline__ void store_turned(const TcParams& t, uint32_t tmem, u
   tc::tmem_ld32(tmem, v);
   tc::tmem_ld_wait();
   const float alpha = p.alpha;
+  if (t.store_bytes == 2) {
+    // Rows that start anywhere: straight from the registers, a store being one
+    // slot's run of the warp's 32 weights (in runs of eight, element by
+    // element, such an N took twice the time; turned and in words 16 % more).
+    const int64_t w = first + lane;
+    uint16_t* o = static_cast<uint16_t*>(p.out) + slot * p.N + w;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j < n && w < p.N)
+        *o = GATHER && !((live >> j) & 1u) ? (uint16_t)0 : to_bf16(__uint_as_float(v[j]) * alpha);
+      o += p.N;
+      asm volatile("" : "+l"(o));     // one address at a time, not 32 in registers
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 16; ++j)
     turn[j * kTurnPitch + lane] = pack_bf16x2(__uint_as_float(v[2 * j]) * alpha,
@@ -337,20 +352,9 @@ __device__ __forceinline__ void store_turned(const TcParams& t, uint32_t tmem, u
       uint16_t* o = static_cast<uint16_t*>(p.out) + (slot + s) * p.N + col;
       if (t.store_bytes == 16) {
         *reinterpret_cast<uint4*>(o) = w[i];
-      } else if (t.store_bytes == 8) {
+      } else {
         *reinterpret_cast<uint2*>(o) = make_uint2(w[i].x, w[i].y);
         if (col + 4 < p.N) reinterpret_cast<uint2*>(o)[1] = make_uint2(w[i].z, w[i].w);
-      } else {
-        const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (t.store_bytes == 4) {
-            if (col + 2 * k < p.N) reinterpret_cast<uint32_t*>(o)[k] = e[k];
-          } else {
-            if (col + 2 * k < p.N) o[2 * k] = (uint16_t)(e[k] & 0xFFFFu);
-            if (col + 2 * k + 1 < p.N) o[2 * k + 1] = (uint16_t)(e[k] >> 16);
-          }
-        }
       }
     }
   }
@@ -622,7 +626,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
             uint16_t* o = out + s * p.N + n;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              if (t.store_bytes >= 4) {
+              if (t.store_bytes >= 8) {
                 if (n + 2 * k < p.N) reinterpret_cast<uint32_t*>(o)[k] = e[k];
               } else {
                 if (n + 2 * k < p.N) o[2 * k] = (uint16_t)(e[k] & 0xFFFFu);
