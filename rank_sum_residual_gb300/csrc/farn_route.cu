@@ -145,18 +145,24 @@ __device__ __forceinline__ void select_token(const RouteParams& p, int64_t t, in
                                              uint32_t* mask, int lane) {
   typedef Candidate<BF16> C;
   typename C::Word v[EPL];
+  float x[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = j * 32 + lane;
-    v[j] = C::make(e < p.E ? order_key(logit_at<BF16>(p.logits, t * p.E + e)) : 0u, e);
+    x[j] = e < p.E ? logit_at<BF16>(p.logits, t * p.E + e) : -INFINITY;
+    if (!(x[j] > -INFINITY)) x[j] = -INFINITY;        // NaN is masked too
+    v[j] = C::make(order_key(x[j]), e);
   }
   sort_descending<EPL>(v);
   typename C::Word top = C::warp_max(v[0]);
   const float m = key_value(C::key(top));
   float all = 0.0f;
   if (!p.renorm) {
+    // exp by its power of two: the differences are exact where they are small,
+    // so the terms that make up the sum keep their last bits
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) all += v[j] ? weight_of(C::key(v[j]), m) : 0.0f;
+    for (int j = 0; j < EPL; ++j)
+      all += x[j] == m ? 1.0f : exp2f((x[j] - m) * 1.44269504f);
     all = farn::warp_sum(all);
   }
   typename C::Word mine = 0;
