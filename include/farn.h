@@ -406,7 +406,8 @@ int farn_nvfp4_dequantize(const farn_ctx *ctx, const void *codes,
  *   a_codes uint8 [T, H/2], a_scale uint8 [T, H/16]; b_codes, b_scale the
  *   same with N rows; out bf16 [T, N]
  *   H a multiple of 16; T, N, H < 2^31; T == 0 launches nothing
- * The fast kernels need the codes 16-byte aligned and H a multiple of 32;
+ * The fast kernels need the codes 16-byte aligned and H a multiple of 32 (they
+ * are faster still with H a multiple of 256 and the scales 16-byte aligned);
  * other shapes are served by a slower kernel.  Returns FARN_ERR_INVALID_ARG
  * (also for an alpha that fp32 cannot hold), FARN_ERR_ALIAS or
  * FARN_ERR_CUDA. */

@@ -585,20 +585,21 @@ def moe_combine(expert_out, index, gates, residual, weight, eps: float, out=None
 # calls of its own (a serving step makes several of them per layer, and their
 # kernels take a few microseconds); what it turns down goes through
 # _check_tensor for the message.
-_torch = None
+_torch = _current_raw_stream = None
 
 
 def _load_torch():
-    global _torch
+    global _torch, _current_raw_stream
     import torch
+    # the handle alone, without a Stream object around it, where torch has it
+    _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
     _torch = torch
     return torch
 
 
 def _raw_stream(stream, index):
-    if stream is not None:
-        return stream.cuda_stream
-    return _torch._C._cuda_getCurrentRawStream(index)
+    return _current_raw_stream(index) if stream is None else stream.cuda_stream
 
 
 def _call(fn, args, name):

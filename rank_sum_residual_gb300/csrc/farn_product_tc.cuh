@@ -390,24 +390,26 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
   const uint32_t rank = cluster_ctarank();
   const int csize = CG == 2 ? 2 : t.ks;
 
-  if (tid == 0) {
-    for (uint32_t s = 0; s < NS; ++s) {
-      mbar_init(full0 + 8 * s, GATHER ? 1 + CG : 1);   // TMA; gathered rows
-      mbar_init(empty0 + 8 * s, 1);
+  if (warp == 0) {        // a lane per barrier
+    if (lane < (int)NS) {
+      mbar_init(full0 + 8 * lane, GATHER ? 1 + CG : 1);   // TMA; gathered rows
+      mbar_init(empty0 + 8 * lane, 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(tfull0 + 8 * i, 1);
-      mbar_init(tempty0 + 8 * i, 4 * CG);
+    if (lane < 2) {
+      mbar_init(tfull0 + 8 * lane, 1);
+      mbar_init(tempty0 + 8 * lane, 4 * CG);
     }
-    for (int i = 0; i < kTcScaleSlots; ++i) {
-      mbar_init(sfull0 + 8 * i, Sh::kScaleWarps * (1 + Sh::kSlotBlocks) * CG);
-      mbar_init(sempty0 + 8 * i, 1);
-      for (int u = 0; u < 3; ++u) mbar_init(sraw0 + 8 * (i * 3 + u), 1);
+    if (FP4 && lane < kTcScaleSlots) {
+      mbar_init(sfull0 + 8 * lane, Sh::kScaleWarps * (1 + Sh::kSlotBlocks) * CG);
+      mbar_init(sempty0 + 8 * lane, 1);
+      for (int u = 0; u < 3; ++u) mbar_init(sraw0 + 8 * (lane * 3 + u), 1);
     }
-    mbar_init(tc::smem_addr(&bb->part_full), 4 * csize);
-    mbar_init(tc::smem_addr(&bb->part_empty), 4 * csize);
-    mbar_init(tc::smem_addr(&bb->never), 1);
-    bb->abort_flag = 0;
+    if (lane == 0) {
+      mbar_init(tc::smem_addr(&bb->part_full), 4 * csize);
+      mbar_init(tc::smem_addr(&bb->part_empty), 4 * csize);
+      mbar_init(tc::smem_addr(&bb->never), 1);
+      bb->abort_flag = 0;
+    }
     tc::mbar_init_fence();
   }
   if (warp == 5) tc::tmem_alloc<CG>(tc::smem_addr(&bb->tmem), Sh::kCols);

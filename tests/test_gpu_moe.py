@@ -514,6 +514,50 @@ def test_context_of_another_device_is_refused(dev):
             call()
 
 
+def test_long_route_in_a_graph(dev):
+    """The three kernels of a long routing call, captured and replayed on new
+    logits, twice in one graph."""
+    T, E, K = 3000, 40, 4
+    x = normal(dev, T, E, 41, torch.float32)
+    y = normal(dev, T, E, 42, torch.float32)
+    farn.moe_route(x, K)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        a, b = farn.moe_route(x, K), farn.moe_route(y, K, renormalize=False)
+    x.copy_(normal(dev, T, E, 43, torch.float32))
+    y[::3] = -INF
+    graph.replay()
+    torch.cuda.synchronize()
+    for got, want in ((a, farn.moe_route(x, K)), (b, farn.moe_route(y, K, renormalize=False))):
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+
+
+def test_two_threads_with_one_context(dev):
+    """Calls of two host threads on streams of their own share a context."""
+    import threading
+    ins = [layer_inputs(dev, 40 + 90 * i, 8, 256, 512, 51 + i) for i in range(2)]
+    want = [[t.clone() for t in moe_layer(*i, 2)] for i in ins]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(n):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                got = moe_layer(*ins[n], 2)
+                s.synchronize()
+                if not all(torch.equal(g, w) for g, w in zip(got, want[n])):
+                    bad.append(n)
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def test_launch_fault_reaches_the_caller(dev):
     bad = make_ctx(FARN_FAULT_INJECT="launch")
     x, logits, up, *_ = layer_inputs(dev, 4, 4, 64, 64, 1)
