@@ -417,6 +417,25 @@ int farn_nvfp4_matmul(const farn_ctx *ctx, const void *a_codes,
                       float b_tensor_scale, int64_t T, int64_t N, int64_t H,
                       void *out, cudaStream_t stream);
 
+/* Which kernel farn_grouped_matmul or farn_nvfp4_matmul would launch for these
+ * sizes and pointers, without launching (only alignment and whether rows is
+ * NULL matter of the pointers): 2 generic (any H or alignment), 6 tensor (the
+ * tensor cores, a tile of 128 weights by 64 slots per CTA, *ctas of them
+ * splitting the row), 7 pair (the tensor cores, two CTAs per tile of 256 by 256,
+ * NVFP4 224, slots).  *ctas receives the CTAs per tile, *threads the threads per
+ * CTA.  Returns a farn_status (FARN_ERR_INVALID_ARG for a bad or empty shape or
+ * a NULL pointer; aliasing is not checked). */
+int farn_plan_grouped_matmul(const farn_ctx *ctx, const void *x, int64_t n_rows,
+                             const int32_t *rows, int64_t n_slots,
+                             const void *weights, int E, int64_t N, int64_t H,
+                             const void *out, int *variant, int *ctas,
+                             int *threads);
+int farn_plan_nvfp4_matmul(const farn_ctx *ctx, const void *a_codes,
+                           const void *a_scale, const void *b_codes,
+                           const void *b_scale, int64_t T, int64_t N, int64_t H,
+                           const void *out, int *variant, int *ctas,
+                           int *threads);
+
 /* Flags of farn_plan_typed. */
 #define FARN_PLAN_FP8_OUT 1   /* the call also writes the FP8 norm output */
 #define FARN_PLAN_NVFP4_OUT 2 /* the call also writes the NVFP4 norm output */

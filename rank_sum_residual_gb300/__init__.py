@@ -33,6 +33,7 @@ __all__ = [
     "farn_grouped_matmul", "grouped_matmul",
     "farn_nvfp4_quantize", "nvfp4_quantize", "farn_nvfp4_dequantize", "nvfp4_dequantize",
     "farn_nvfp4_matmul", "nvfp4_matmul",
+    "farn_plan_grouped_matmul", "farn_plan_nvfp4_matmul",
     "FARN_BF16", "FARN_F32",
     "forward", "VARIANTS",
 ]
@@ -45,7 +46,8 @@ FARN_ERR_UNSUPPORTED = -2
 FARN_ERR_ALIAS = -3
 FARN_ERR_CUDA = -4
 FARN_ERR_NOMEM = -5
-VARIANTS = {0: "row", 1: "cluster", 2: "generic", 3: "bulk", 4: "stage", 5: "combine"}
+VARIANTS = {0: "row", 1: "cluster", 2: "generic", 3: "bulk", 4: "stage", 5: "combine",
+            6: "tensor", 7: "pair"}
 FARN_BF16, FARN_F32 = 0, 1
 
 _lib = None
@@ -96,6 +98,13 @@ def _load():
         lib.farn_nvfp4_dequantize.restype = i32
         lib.farn_nvfp4_matmul.argtypes = [vp, cvp, cvp, f32, cvp, cvp, f32, i64, i64, i64, vp, vp]
         lib.farn_nvfp4_matmul.restype = i32
+        pi = ctypes.POINTER(i32)
+        lib.farn_plan_grouped_matmul.argtypes = [vp, cvp, i64, cvp, i64, cvp, i32, i64, i64, cvp,
+                                                 pi, pi, pi]
+        lib.farn_plan_grouped_matmul.restype = i32
+        lib.farn_plan_nvfp4_matmul.argtypes = [vp, cvp, cvp, cvp, cvp, i64, i64, i64, cvp, pi, pi,
+                                               pi]
+        lib.farn_plan_nvfp4_matmul.restype = i32
         lib.farn_check_args.argtypes = [pvp, i32, cvp, cvp, f32, i64, i64,
                                         cvp, cvp, cvp]
         lib.farn_check_args.restype = i32
@@ -335,6 +344,28 @@ def farn_plan_moe_combine(ctx, K, T, H, expert_out, residual, weight, reduced_ou
     if st != FARN_OK:
         raise FarnError(st, "farn_plan_moe_combine")
     return VARIANTS[variant.value], thr.value
+
+
+def _plan(fn, name, *args):
+    variant, ctas, thr = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
+    st = fn(*args, ctypes.byref(variant), ctypes.byref(ctas), ctypes.byref(thr))
+    if st != FARN_OK:
+        raise FarnError(st, name)
+    return VARIANTS[variant.value], ctas.value, thr.value
+
+
+def farn_plan_grouped_matmul(ctx, x, n_rows, rows, n_slots, weights, E, N, H, out):
+    """C ``farn_plan_grouped_matmul``: (variant name, CTAs per tile, threads per CTA)."""
+    return _plan(_load().farn_plan_grouped_matmul, "farn_plan_grouped_matmul", _addr(ctx),
+                 _addr(x), int(n_rows), _addr(rows), int(n_slots), _addr(weights), int(E),
+                 int(N), int(H), _addr(out))
+
+
+def farn_plan_nvfp4_matmul(ctx, a_codes, a_scale, b_codes, b_scale, T, N, H, out):
+    """C ``farn_plan_nvfp4_matmul``: (variant name, CTAs per tile, threads per CTA)."""
+    return _plan(_load().farn_plan_nvfp4_matmul, "farn_plan_nvfp4_matmul", _addr(ctx),
+                 _addr(a_codes), _addr(a_scale), _addr(b_codes), _addr(b_scale), int(T), int(N),
+                 int(H), _addr(out))
 
 
 class Context:

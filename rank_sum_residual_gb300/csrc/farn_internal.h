@@ -14,6 +14,8 @@ enum {
   kVariantBulk = 3,
   kVariantStage = 4,
   kVariantCombine = 5,   // the MoE combine's one-CTA-per-row gather kernel
+  kVariantTensor = 6,    // the products: tensor cores, one CTA per tile (and part of a row)
+  kVariantPair = 7,      // the products: tensor cores, a pair of CTAs per tile
   kVariantAuto = -1
 };
 

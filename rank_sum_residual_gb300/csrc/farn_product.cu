@@ -279,6 +279,21 @@ int launch(const farn_ctx* ctx, const ProductParams& p, bool fp4, cudaStream_t s
   return launch_plain(ctx, p, fp4, stream);
 }
 
+int report_plan(const farn_ctx* ctx, const ProductParams& p, bool fp4, int* variant, int* ctas,
+                int* threads) {
+  TcPlan pl;
+  if (tc_takes(ctx, p, fp4) && plan_tc(ctx, p, fp4, &pl)) {
+    *variant = pl.kind->cg == 2 ? kVariantPair : kVariantTensor;
+    *ctas = pl.kind->cg == 2 ? 2 : pl.ks;
+    *threads = pl.kind->warps * 32;
+  } else {
+    *variant = kVariantGeneric;
+    *ctas = 1;
+    *threads = farn::kPlainThreads;
+  }
+  return FARN_OK;
+}
+
 // Slots are 32-bit numbers, and a row of weights fits 31 bits.
 bool sizes_ok(int64_t S, int64_t N, int64_t H) {
   return S >= 0 && S <= 0x7FFFFFFF && N >= 1 && N <= 0x7FFFFFFF && H >= 1 && H <= 0x7FFFFFFF &&
@@ -364,6 +379,50 @@ int farn_grouped_matmul(const farn_ctx* ctx, const void* x, int64_t n_rows, cons
   p.err = ctx->d_status;
   p.stall_test = ctx->stall_test;
   return launch(ctx, p, false, stream);
+}
+
+int farn_plan_grouped_matmul(const farn_ctx* ctx, const void* x, int64_t n_rows,
+                             const int32_t* rows, int64_t n_slots, const void* weights, int E,
+                             int64_t N, int64_t H, const void* out, int* variant, int* ctas,
+                             int* threads) {
+  if (!ctx || !variant || !ctas || !threads || n_rows < 0 || n_rows > 0x7FFFFFFF ||
+      !sizes_ok(n_slots, N, H) || n_slots < 1 || E < 1 || E > FARN_MAX_EXPERTS ||
+      !product_fits(n_rows, 2 * H) || !product_fits(2 * N * H, E) ||
+      (!rows && n_rows != n_slots) || !weights || !out)
+    return FARN_ERR_INVALID_ARG;
+  ProductParams p;
+  memset(&p, 0, sizeof p);
+  p.a = x;
+  p.b = weights;
+  p.rows = rows;
+  p.out = const_cast<void*>(out);
+  p.n_a = n_rows;
+  p.S = n_slots;
+  p.N = N;
+  p.H = H;
+  p.E = E;
+  return report_plan(ctx, p, false, variant, ctas, threads);
+}
+
+int farn_plan_nvfp4_matmul(const farn_ctx* ctx, const void* a_codes, const void* a_scale,
+                           const void* b_codes, const void* b_scale, int64_t T, int64_t N,
+                           int64_t H, const void* out, int* variant, int* ctas, int* threads) {
+  if (!ctx || !variant || !ctas || !threads || !sizes_ok(T, N, H) || T < 1 || H % 16 != 0 ||
+      !product_fits(N, H) || !a_codes || !a_scale || !b_codes || !b_scale || !out)
+    return FARN_ERR_INVALID_ARG;
+  ProductParams p;
+  memset(&p, 0, sizeof p);
+  p.a = a_codes;
+  p.a_scale = static_cast<const uint8_t*>(a_scale);
+  p.b = b_codes;
+  p.b_scale = static_cast<const uint8_t*>(b_scale);
+  p.out = const_cast<void*>(out);
+  p.n_a = T;
+  p.S = T;
+  p.N = N;
+  p.H = H;
+  p.E = 1;
+  return report_plan(ctx, p, true, variant, ctas, threads);
 }
 
 int farn_nvfp4_matmul(const farn_ctx* ctx, const void* a_codes, const void* a_scale,

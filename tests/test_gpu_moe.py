@@ -409,6 +409,27 @@ def test_grouped_waits_are_bounded(dev, env, gather):
     check_exact(got, want, offsets, "after")
 
 
+def test_grouped_plans(dev, ctxs):
+    """Rows that TMA can read take the tensor cores: few slots one CTA per tile
+    with the row split, long calls pairs; others the kernel for any shape."""
+    a = 1 << 32
+
+    def plan(S, E, N, H, x=a, gather=False, which="auto"):
+        return farn.farn_plan_grouped_matmul(
+            ctxs[which].handle, x, S, 3 * a if gather else 0, S, 2 * a, E, N, H, 4 * a)[:2]
+    assert plan(8, 64, 2048, 7168, gather=True) == ("tensor", 1)
+    assert plan(1, 64, 2048, 7168, gather=True) == ("tensor", 4)
+    assert plan(2, 8, 1024, 2048) == ("tensor", 4)
+    assert plan(32768, 64, 4096, 7168, gather=True) == ("pair", 2)
+    assert plan(32768, 1024, 4096, 7168, gather=True) == ("pair", 2)
+    assert plan(8192, 1, 8192, 8192) == ("pair", 2)
+    assert plan(64, 4, 512, 1001) == ("generic", 1)
+    assert plan(64, 4, 512, 1000, x=a + 2) == ("generic", 1)
+    assert plan(64, 4, 512, 1000, which="generic") == ("generic", 1)
+    assert plan(64, 1024, 512, 1000, which="pair") == ("pair", 2)
+    assert plan(64, 1024, 512, 1000, gather=True, which="split4") == ("tensor", 4)
+
+
 # ------------------------------------------------------------- together
 def moe_layer(x, logits, up, down, residual, weight, K, out=None):
     experts, gates, index, rows, offsets = farn.moe_route(logits, K)

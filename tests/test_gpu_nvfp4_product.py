@@ -252,6 +252,22 @@ def test_product_waits_are_bounded(dev, env, H):
     assert torch.equal(got, want)
 
 
+def test_product_plans(dev, ctxs):
+    a = 1 << 32
+
+    def plan(T, N, H, codes=a, which="auto"):
+        return farn.farn_plan_nvfp4_matmul(ctxs[which].handle, codes, 2 * a, 3 * a, 4 * a + 1, T,
+                                           N, H, 5 * a)[:2]
+    assert plan(1, 8192, 8192) == ("tensor", 2)
+    assert plan(64, 2048, 8192) == ("tensor", 4)
+    assert plan(8192, 8192, 8192) == ("pair", 2)
+    assert plan(300, 8192, 2080) == ("pair", 2)
+    assert plan(64, 512, 1008) == ("generic", 1)
+    assert plan(64, 512, 1024, codes=a + 8) == ("generic", 1)
+    assert plan(64, 512, 1024, which="generic") == ("generic", 1)
+    assert plan(64, 512, 1024, which="split2") == ("tensor", 2)
+
+
 def test_norm_to_product(dev):
     """The norm's NVFP4 copy into a projection of quantised weights, captured
     and replayed."""

@@ -134,6 +134,20 @@ def test_product_no_rows_launches_nothing(ctx):
     assert product(ctx, T=0, a_codes=0, a_scale=0, out=0) == farn.FARN_OK
 
 
+def test_plan_queries_refuse(ctx):
+    good = dict(x=A, n_rows=4, rows=B, n_slots=8, weights=C, E=3, N=32, H=64, out=E_)
+    for kw in (dict(n_slots=0), dict(N=0), dict(E=1025), dict(weights=0), dict(out=0),
+               dict(rows=0)):
+        with pytest.raises(farn.FarnError) as e:
+            farn.farn_plan_grouped_matmul(ctx, *(good | kw).values())
+        assert e.value.status == INVALID
+    good = dict(a=A, sa=B, b=C, sb=D, T=4, N=32, H=64, out=E_)
+    for kw in (dict(T=0), dict(H=40), dict(a=0), dict(sb=0), dict(out=0)):
+        with pytest.raises(farn.FarnError) as e:
+            farn.farn_plan_nvfp4_matmul(ctx, *(good | kw).values())
+        assert e.value.status == INVALID
+
+
 def test_null_context():
     farn.build_library()
     assert route(0) == grouped(0) == quantize(0) == dequantize(0) == product(0) == INVALID
