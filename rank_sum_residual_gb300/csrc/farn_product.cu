@@ -133,24 +133,35 @@ bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, TcPlan* pl) 
   const int64_t tiles1 = tiles_of(one->bn, farn::kTcWeights);
   const int64_t tiles2 = tiles_of(pair->bn, 2 * farn::kTcWeights);
   if (tiles1 > 0x7FFFFFFF / 2 || tiles2 > 0x7FFFFFFF / 2) return false;
-  // One CTA per tile of 128 weights by 64 slots, with the row split over as
-  // many CTAs as there are SMs to spare, or a pair of CTAs per tile of 256 by
-  // 256 (NVFP4: 224): whichever has fewer stages one after the other.  A stage
-  // takes much the same time in all of them, as it is bound by its
-  // synchronisation (one CTA) or made to be (the pair's tensor work); joining
-  // a split row costs about six.  Measured (us, one CTA / pair): NVFP4
+  // One CTA per tile of 128 weights by 64 slots, with the row split over up to
+  // four of them, or a pair of CTAs per tile of 256 by 256 (NVFP4: 224):
+  // whichever has fewer stages one after the other.  A stage takes much the
+  // same time in all of them, as it is bound by its synchronisation (one CTA)
+  // or made to be (the pair's tensor work); joining a split row costs about one
+  // and a half.  With several groups the number of tiles is an estimate, so the
+  // last round of CTAs counts half.  Measured (us, one CTA / pair): NVFP4
   // 8192 x 8192, 8 tokens 13.4 / 14.2, 128 tokens 16.5 / 15.6, 512 tokens 46 /
   // 26; 64 experts 2048 -> 7168 of 16 slots each 274 / 277, of 64 321 / 287, of
-  // 256 853 / 365.  Tiles of 16 and of 32 slots were never faster than of 64
-  // (16 slots each: 304 and 281), tiles of 128 for one CTA hardly.
-  int ks = 1;      // 8 CTAs to a row were never faster than 4
-  while (ks < farn::kTcMaxSplit && tiles1 * ks * 2 <= ctx->num_sms && chunks >= ks * 4) ks *= 2;
+  // 256 853 / 365.  Splitting: 30 slots of 32 experts, 5000 -> 1200: 51 whole,
+  // 44 by 2, 41 by 4; 512 slots of 64 experts, 2048 -> 7168: 283 whole, 289 by
+  // 4.  Tiles of 16 and of 32 slots were never faster than of 64 (16 slots each:
+  // 304 and 281), tiles of 128 for one CTA hardly, splits by 8 not.
+  auto stages_of = [&](int64_t tiles, int64_t at_a_time, double per_tile) {
+    const double rounds = (double)tiles / (double)at_a_time;
+    if (rounds <= 1.0) return per_tile;
+    return (p.E == 1 ? ceil(rounds) : rounds + 0.5) * per_tile;
+  };
+  auto cost_of_split = [&](int ks) {
+    return stages_of(tiles1 * ks, ctx->num_sms,
+                     (double)((chunks + ks - 1) / ks) + (ks > 1 ? 1.5 : 0.0));
+  };
+  int ks = 1;
+  for (int k = 2; k <= farn::kTcMaxSplit && chunks >= k * 2; k *= 2)
+    if (cost_of_split(k) < cost_of_split(ks)) ks = k;
   if (ctx->tc_split) ks = ctx->tc_split;
   while (ks > chunks) ks /= 2;      // every CTA has a part of the row
-  const int64_t sms = ctx->num_sms, pairs = ctx->max_clusters[1];
-  const int64_t cost1 =
-      (tiles1 * ks + sms - 1) / sms * ((chunks + ks - 1) / ks) + (ks > 1 ? 6 : 0);
-  const int64_t cost2 = (tiles2 + pairs - 1) / pairs * chunks;
+  const double cost1 = cost_of_split(ks);
+  const double cost2 = stages_of(tiles2, ctx->max_clusters[1], (double)chunks);
   bool use_pair = cost2 < cost1 || (cost2 == cost1 && p.S > 32 * groups);
   if (ctx->tc_tile) use_pair = ctx->tc_tile == 256;
   if (use_pair) ks = 1;

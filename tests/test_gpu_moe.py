@@ -420,6 +420,7 @@ def test_grouped_plans(dev, ctxs):
     assert plan(8, 64, 2048, 7168, gather=True) == ("tensor", 1)
     assert plan(1, 64, 2048, 7168, gather=True) == ("tensor", 4)
     assert plan(2, 8, 1024, 2048) == ("tensor", 4)
+    assert plan(30, 32, 1200, 5000, gather=True) == ("tensor", 4)
     assert plan(32768, 64, 4096, 7168, gather=True) == ("pair", 2)
     assert plan(32768, 1024, 4096, 7168, gather=True) == ("pair", 2)
     assert plan(8192, 1, 8192, 8192) == ("pair", 2)
