@@ -346,6 +346,7 @@ route_scan_kernel(const RouteParams p) {
   __shared__ int32_t part[kGroups][kScanE];
   __shared__ int32_t total[kMaxE + 1];
   __shared__ int32_t ws[33];
+  farn::cluster_arrive_release();     // this CTA runs: the others may write to its memory
   farn::pdl_wait();
   farn::pdl_trigger();
   cg::cluster_group cluster = cg::this_cluster();
@@ -362,6 +363,7 @@ route_scan_kernel(const RouteParams p) {
     part[warp][i] = sum;
   }
   __syncthreads();
+  farn::cluster_wait_acquire();       // all CTAs run
   if (e0 + (int)threadIdx.x < e1) {
     int32_t sum = 0;
     for (int w = 0; w < kGroups; ++w) {
