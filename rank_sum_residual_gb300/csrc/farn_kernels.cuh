@@ -355,6 +355,9 @@ farn_vec_kernel(const __grid_constant__ Params p) {
   __shared__ float cluster_ss[2][CS];   // [row parity][CTA rank in cluster]
   __shared__ float warp_mx[2][32];      // FP8 output only: row amax
   __shared__ float cluster_mx[2][CS];
+  // This CTA runs; before the first push into another's shared memory it
+  // waits for all of them (the loads of the row come in between).
+  if (CS > 1) cluster_arrive_release();
 
   const uint4* __restrict__ wv4 = reinterpret_cast<const uint4*>(p.weight) + (int64_t)slice * sv;
   // One-row calls and two vectors per thread: the weight is fetched with
@@ -536,6 +539,7 @@ farn_vec_kernel(const __grid_constant__ Params p) {
       // it; the row-parity double buffer keeps the next row's pushes off
       // slots a slower peer is still reading.
       float* slots = cluster_ss[it & 1];
+      if (it == 0) cluster_wait_acquire();
       if (tid < CS) st_dsmem_f32(&slots[slice], (uint32_t)tid, tot);
       cluster_arrive_release();
       cluster_wait_acquire();

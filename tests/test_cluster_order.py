@@ -35,7 +35,7 @@ def kernels(text):
         yield name.group(1), text[start:at]
 
 
-@pytest.mark.parametrize("name", ["farn_route.cu", "farn_product_tc.cuh"])
+@pytest.mark.parametrize("name", ["farn_kernels.cuh", "farn_route.cu", "farn_product_tc.cuh"])
 def test_blocks_have_started_before_their_memory_is_touched(name):
     """A block's shared memory may be accessed by others of its cluster only
     once it is known to run: a cluster barrier comes first."""
