@@ -143,18 +143,18 @@ __device__ __forceinline__ SlotRows slot_rows(const Tile& w, int w_rank) {
   return r;
 }
 
-// Bounded phase wait.  JOIN: what other CTAs of the cluster wrote before they
-// arrived is read afterwards.  A waiting thread sleeps: nine warps polling took
-// the matrix warp's issue slots (bf16 8192^3 768 us).
+// Bounded phase wait.  CLUSTER: other CTAs of the cluster arrive on the barrier
+// too, so the wait acquires at the cluster's scope.  A waiting thread sleeps:
+// nine warps polling took the matrix warp's issue slots (bf16 8192^3 768 us).
 constexpr uint32_t kTcSleepNs = 1000000;
 
-template <bool JOIN = false>
+template <bool CLUSTER>
 __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                         int* err, int code) {
-  if (tc::mbar_wait_some<JOIN>(bar, parity, kTcSleepNs)) return true;
+  if (tc::mbar_wait_some<CLUSTER>(bar, parity, kTcSleepNs)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-    if (tc::mbar_wait_some<JOIN>(bar, parity, kTcSleepNs)) return true;
+    if (tc::mbar_wait_some<CLUSTER>(bar, parity, kTcSleepNs)) return true;
     if (*abort_flag) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       *abort_flag = 1;
@@ -181,10 +181,10 @@ struct RingPos {
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // The same by a whole warp, whose lanes go on or give up together.
-template <bool JOIN = false>
+template <bool CLUSTER>
 __device__ __forceinline__ bool tc_wait_warp(uint32_t bar, uint32_t parity,
                                              volatile int* abort_flag, int* err, int code) {
-  return __all_sync(0xFFFFFFFFu, tc_wait<JOIN>(bar, parity, abort_flag, err, code));
+  return __all_sync(0xFFFFFFFFu, tc_wait<CLUSTER>(bar, parity, abort_flag, err, code));
 }
 
 // Block scales in shared memory, as the tensor cores read them: 128 rows by
@@ -433,6 +433,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
   const uint32_t tmem = uniform(bb->tmem);
 
   constexpr int kTileWeights = kTcWeights * CG;
+  constexpr bool kPair = CG == 2;   // the other CTA arrives on a tile's barriers too
   const int wts = (int)((p.N + kTileWeights - 1) / kTileWeights);
   const int32_t tiles = g.tile[p.E] * wts;
   const int32_t t0 = blockIdx.x / csize, tstep = gridDim.x / csize;
@@ -449,7 +450,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     uint32_t armed = 0;        // stages given to TMA, all but the last NS done
     bool ok = true;
     if (t.p.stall_test && blockIdx.x == 0)
-      ok = tc_wait_warp(tc::smem_addr(&bb->never), 0, abort_flag, p.err, kErrTcEmpty);
+      ok = tc_wait_warp<false>(tc::smem_addr(&bb->never), 0, abort_flag, p.err, kErrTcEmpty);
     for (int32_t tile = t0; ok && tile < tiles; tile += tstep) {
       const Tile w = find_tile(g, p.E, tile, wts, BN);
       const SlotRows r = slot_rows<Sh, CG>(w, w_rank);
@@ -457,7 +458,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       const int n0 = w.wt * kTileWeights + w_rank * kTcWeights;
       for (int c = c0; c < c1; ++c, at.next(NS), ++armed) {
         const uint32_t s = at.stage;
-        ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
+        ok = tc_wait_warp<kPair>(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
         if (!ok) break;
         if (tc::elect_one()) {
           if (w_rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, bytes);
@@ -491,7 +492,8 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         const uint32_t idesc = FP4 ? tc::idesc_nvfp4(kTileWeights, n_eff)
                                    : tc::idesc_bf16(kTileWeights, n_eff);
         const uint32_t acc = nt & 1, d = tmem + acc * BN;
-        ok = tc_wait_warp(tempty0 + 8 * acc, ((nt >> 1) & 1) ^ 1, abort_flag, p.err, kErrTcTile);
+        ok = tc_wait_warp<kPair>(tempty0 + 8 * acc, ((nt >> 1) & 1) ^ 1, abort_flag, p.err,
+                                 kErrTcTile);
         if (!ok) break;
         tc::fence_after();
         // Few instructions per stage: a dependent one costs this warp about
@@ -502,14 +504,14 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
           int end = nc;
           if constexpr (FP4) {
             const uint32_t slot = ng % kTcScaleSlots;
-            ok = tc_wait_warp(sfull0 + 8 * slot, ng / kTcScaleSlots & 1, abort_flag, p.err,
-                              kErrTcFull);
+            ok = tc_wait_warp<kPair>(sfull0 + 8 * slot, ng / kTcScaleSlots & 1, abort_flag, p.err,
+                                     kErrTcFull);
             sc = scale0 + (slot * Sh::kScaleSlot >> 4);
             end = min(nc, c + kTcScaleStages);
           }
           for (; ok && c < end; ++c) {
             const uint32_t s = at.stage;
-            ok = tc_wait_warp(full0 + 8 * s, at.phase, abort_flag, p.err, kErrTcFull);
+            ok = tc_wait_warp<kPair>(full0 + 8 * s, at.phase, abort_flag, p.err, kErrTcFull);
             if (!ok) break;
             tc::fence_after();
             const uint64_t da = desc0 + (s * Sh::kStageBytes >> 4), db = da + (Sh::kABytes >> 4);
@@ -562,7 +564,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       const Tile w = find_tile(g, p.E, tile, wts, BN);
       const uint32_t acc = nt & 1, d = tmem + acc * BN + ((uint32_t)warp << 21);
       const int64_t n0 = (int64_t)w.wt * kTileWeights + w_rank * kTcWeights;
-      ok = tc_wait_warp(tfull0 + 8 * acc, (nt >> 1) & 1, abort_flag, p.err, kErrTcTile);
+      ok = tc_wait_warp<kPair>(tfull0 + 8 * acc, (nt >> 1) & 1, abort_flag, p.err, kErrTcTile);
       if (!ok) break;
       tc::fence_after();
       const bool split = CG == 1 && csize > 1;
@@ -591,7 +593,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       }
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(tempty0 + 8 * acc, CG == 2 ? 0 : rank));
+      if (lane == 0) tc::mbar_arrive_first<CG>(tempty0 + 8 * acc);
       if (split) {
         if (lane < csize) tc::mbar_arrive_cluster(tc::map_rank(part_full, lane));
         ok = tc_wait_warp<true>(part_full, nt & 1, abort_flag, p.err, kErrTcJoin);
@@ -651,7 +653,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       const SlotRows r = slot_rows<Sh, CG>(w, w_rank);
       for (int c = c0; c < c1; ++c, at.next(NS)) {
         const uint32_t s = at.stage;
-        ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
+        ok = tc_wait_warp<kPair>(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
         if (!ok) break;
         const uint32_t b = base + s * Sh::kStageBytes + Sh::kABytes;
         if (tc::elect_one()) {
@@ -687,8 +689,8 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         if (tile >= tiles) return false;
         if (gi == 0) w = find_tile(g, p.E, tile, wts, BN);
         const uint32_t slot = asked % kTcScaleSlots;
-        if (!tc_wait_warp(sempty0 + 8 * slot, (asked / kTcScaleSlots & 1) ^ 1, abort_flag, p.err,
-                          kErrTcEmpty)) {
+        if (!tc_wait_warp<kPair>(sempty0 + 8 * slot, (asked / kTcScaleSlots & 1) ^ 1, abort_flag,
+                                 p.err, kErrTcEmpty)) {
           ok = false;
           return false;
         }
@@ -721,8 +723,8 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
           for (int i = 0; ok && i < groups; ++i, ++done) {
             const uint32_t slot = done % kTcScaleSlots;
             if (u < 2 || n > 128) {
-              ok = tc_wait_warp(sraw0 + 8 * (slot * 3 + u), phases >> slot & 1, abort_flag,
-                                p.err, kErrTcFull);
+              ok = tc_wait_warp<kPair>(sraw0 + 8 * (slot * 3 + u), phases >> slot & 1, abort_flag,
+                                       p.err, kErrTcFull);
               if (!ok) break;
               phases ^= 1u << slot;
               turn_scales(block0 + slot * Sh::kScaleSlot, lane);
@@ -730,7 +732,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
             }
             __syncwarp();
             if (lane == 0)
-              tc::mbar_arrive_cluster(tc::map_rank(sfull0 + 8 * slot, CG == 2 ? 0 : rank));
+              tc::mbar_arrive_first<CG>(sfull0 + 8 * slot);
             // the last slot is the one of the group before this, when its
             // products are done; this one is turned by then
             if (more && done > 0) more = ask();
@@ -776,14 +778,14 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       }
       for (uint32_t ng = 0; more; ++ng) {
         const uint32_t slot = ng % kTcScaleSlots;
-        ok = tc_wait_warp(sempty0 + 8 * slot, (ng / kTcScaleSlots & 1) ^ 1, abort_flag, p.err,
-                          kErrTcEmpty);
+        ok = tc_wait_warp<kPair>(sempty0 + 8 * slot, (ng / kTcScaleSlots & 1) ^ 1, abort_flag,
+                                 p.err, kErrTcEmpty);
         if (!ok) break;
         put_scale_rows(block0 + slot * Sh::kScaleSlot, v, b, pitch, quarter, lane);
         tc::fence_async_shared();
         __syncwarp();
         if (lane == 0)
-          tc::mbar_arrive_cluster(tc::map_rank(sfull0 + 8 * slot, CG == 2 ? 0 : rank));
+          tc::mbar_arrive_first<CG>(sfull0 + 8 * slot);
         more = tile < tiles;
         if (more) {           // after the fence, which waits for loads too
           b = next();
@@ -823,7 +825,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         int c = c0 + ahead;
         for (; c < c1; c += Sh::kAux, at.skip(Sh::kAux, NS)) {
           const uint32_t s = at.stage;
-          ok = tc_wait_warp(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
+          ok = tc_wait_warp<kPair>(empty0 + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
           if (!ok) break;
           const uint32_t b = base + s * Sh::kStageBytes + Sh::kABytes + sub * kTcRowBytes;
           const bool in_row = (int64_t)c * Sh::kChunk + col * 8 < p.H;
@@ -843,7 +845,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
           tc::fence_async_shared();
           __syncwarp();
           if (lane == 0)
-            tc::mbar_arrive_cluster(tc::map_rank(full0 + 8 * s, CG == 2 ? 0 : rank));
+            tc::mbar_arrive_first<CG>(full0 + 8 * s);
         }
         ahead = c - c1;
       }

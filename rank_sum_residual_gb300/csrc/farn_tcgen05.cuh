@@ -30,9 +30,31 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Arrivals that hand something to another CTA of the cluster; `cluster_addr`
+// is the barrier's address in the cluster's window.  Without a scope an arrival
+// releases to its own CTA only, so both say the cluster's.
+//
+// For what the thread read or wrote anywhere (and what reached it through a
+// barrier of its warp): once or twice per tile.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];"
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
                :: "r"(cluster_addr) : "memory");
+}
+// For what lies in this CTA's own shared memory: the fence leaves out global
+// memory, where a warp that feeds the tensor cores or stores a tile has much
+// in flight.
+__device__ __forceinline__ void mbar_arrive_cluster_smem(uint32_t cluster_addr) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n\t"
+               "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
+               :: "r"(cluster_addr) : "memory");
+}
+// Arrive on the barrier at `bar` of the first of the CG CTAs that share a tile.
+template <int CG>
+__device__ __forceinline__ void mbar_arrive_first(uint32_t bar) {
+  if constexpr (CG == 1)
+    mbar_arrive(bar);
+  else
+    mbar_arrive_cluster_smem(map_rank(bar, 0));
 }
 __device__ __forceinline__ void mbar_init_fence() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -50,11 +72,12 @@ __device__ __forceinline__ bool elect_one() {
 
 // A phase wait that lets the thread sleep for up to `ns` nanoseconds: warps
 // that wait take neither issue slots nor shared-memory cycles from the one
-// that feeds the tensor cores.  JOIN: with acquire order over the cluster.
-template <bool JOIN>
+// that feeds the tensor cores.  CLUSTER: other CTAs of the cluster arrive on
+// the barrier, and what they did before is ordered before what follows.
+template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_wait_some(uint32_t bar, uint32_t parity, uint32_t ns) {
   uint32_t ok;
-  if constexpr (JOIN)
+  if constexpr (CLUSTER)
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"

@@ -47,3 +47,47 @@ def test_blocks_have_started_before_their_memory_is_touched(name):
         seen += 1
         assert re.search(BARRIER, body[:first.start()]), kernel
     assert seen
+
+
+def asm_statements(text):
+    """The instructions of every asm statement, its string parts joined."""
+    for m in re.finditer(r"\basm\s+volatile\s*\(", text):
+        parts = re.match(r'\s*((?:"(?:[^"\\]|\\.)*"\s*)+)', text[m.end():])
+        yield "".join(re.findall(r'"((?:[^"\\]|\\.)*)"', parts.group(1)))
+
+
+def test_arrivals_at_other_blocks_release_to_the_cluster():
+    """An arrival on another block's barrier hands over what came before it
+    only if it releases at the cluster's scope (without a scope: its own
+    block's), itself or by a fence in front of it."""
+    seen = 0
+    for code in asm_statements(source("farn_tcgen05.cuh")):
+        for m in re.finditer(r"mbarrier\.arrive[.\w]*(?:::\w+[.\w]*)*", code):
+            name = m.group(0)
+            if "shared::cluster" not in name:
+                continue
+            seen += 1
+            if ".release.cluster" in name:
+                continue
+            assert ".relaxed.cluster" in name, name
+            assert re.search(r"fence\.(release|acq_rel)[.\w:]*\.cluster;", code[:m.start()]), name
+    assert seen
+
+
+def test_waits_for_other_blocks_acquire_from_the_cluster():
+    """The other half: a wait says whether other blocks arrive on its barrier,
+    and one for them acquires at the cluster's scope."""
+    waits = [c for c in asm_statements(source("farn_tcgen05.cuh")) if "try_wait" in c]
+    assert any(".acquire.cluster" in c for c in waits)
+    text = source("farn_product_tc.cuh")
+    # how the kernel waits on each of its barriers: always, or in a pair of
+    # blocks only, with the cluster's scope
+    scope = {"part_full": "true", "part_empty": "true", "full0": "kPair", "empty0": "kPair",
+             "sfull0": "kPair", "sempty0": "kPair", "tfull0": "kPair", "tempty0": "kPair"}
+    found = set()
+    for m in re.finditer(r"tc_wait_warp(?:<(\w+)>)?\(\s*(?!uint32_t)(\w+)", text):
+        if m.group(2) in scope:
+            assert m.group(1) == scope[m.group(2)], m.group(0)
+            found.add(m.group(2))
+    assert found == set(scope)
+    assert re.search(r"kPair = CG == 2;", text)
