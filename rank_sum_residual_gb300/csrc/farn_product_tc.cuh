@@ -679,8 +679,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
     if constexpr (!COPY) {
       // TMA brings a block as it lies and one warp turns it; the next group's
       // copy is on its way while this one's products run.  Both CTAs of a
-      // pair need all slots' scales, so each loads one block for both.
-      const bool mine = CG == 1 || u == 0 || u - 1 == w_rank;
+      // pair need all slots' scales, and each loads them for itself.
       int32_t tile = t0;
       int gi = 0;                             // group of the tile
       uint32_t asked = 0, done = 0;           // groups so far
@@ -703,10 +702,8 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
             mbar_arrive_expect_tx(bar, kTcScaleBlock);
             if (u == 0)
               tc::load_2d<1>(dst, &map_ws, x, w.wt * kTileWeights + w_rank * kTcWeights, bar);
-            else if (CG == 1)
-              tc::load_2d<1>(dst, &map_xs, x, w.slot0, bar);
-            else if (mine)
-              tc::load_2d_to(dst, &map_xs, x, w.slot0 + (u - 1) * 128, bar, 3);
+            else
+              tc::load_2d<1>(dst, &map_xs, x, w.slot0 + (u - 1) * 128, bar);
           }
           __syncwarp();
         }
@@ -723,7 +720,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
           for (int i = 0; ok && i < groups; ++i, ++done) {
             const uint32_t slot = done % kTcScaleSlots;
             if (u < 2 || n > 128) {
-              ok = tc_wait_warp<kPair>(sraw0 + 8 * (slot * 3 + u), phases >> slot & 1, abort_flag,
+              ok = tc_wait_warp<false>(sraw0 + 8 * (slot * 3 + u), phases >> slot & 1, abort_flag,
                                        p.err, kErrTcFull);
               if (!ok) break;
               phases ^= 1u << slot;

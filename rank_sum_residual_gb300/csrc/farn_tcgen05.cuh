@@ -129,15 +129,6 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const void* map, int x, in
         " [%0], [%1, {%2, %3}], [%4];"
         :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
-// The same into the CTAs of `mask`, at the same place in each, counted on
-// the barrier at the same place in each.
-__device__ __forceinline__ void load_2d_to(uint32_t dst, const void* map, int x, int y,
-                                           uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;"
-      :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar), "h"(mask) : "memory");
-}
 // 16 bytes by the thread itself, or zeros where `bytes` is 0 (nothing is
 // read then).  Both addresses are 16-byte aligned.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {

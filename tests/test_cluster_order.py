@@ -91,3 +91,12 @@ def test_waits_for_other_blocks_acquire_from_the_cluster():
             found.add(m.group(2))
     assert found == set(scope)
     assert re.search(r"kPair = CG == 2;", text)
+
+
+@pytest.mark.parametrize("name", sorted(os.path.basename(p) for p in _build.DEPENDS))
+def test_copies_go_to_one_block(name):
+    """Operands may lie in any memory that the device can read, so a copy to
+    shared memory goes to one block: none is multicast over a cluster."""
+    path = next(p for p in _build.DEPENDS if os.path.basename(p) == name)
+    for code in asm_statements(source(path)):
+        assert not ("cp.async.bulk" in code and "multicast" in code), code
