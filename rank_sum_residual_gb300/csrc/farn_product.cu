@@ -144,7 +144,9 @@ bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, TcPlan* pl) 
   // 26; 64 experts 2048 -> 7168 of 16 slots each 274 / 277, of 64 321 / 287, of
   // 256 853 / 365.  Splitting: 30 slots of 32 experts, 5000 -> 1200: 51 whole,
   // 44 by 2, 41 by 4; 512 slots of 64 experts, 2048 -> 7168: 283 whole, 289 by
-  // 4.  Tiles of 16 and of 32 slots were never faster than of 64 (16 slots each:
+  // 4.  Clusters of four leave 8 of the 152 SMs out; counting them so changed the
+  // choice of 58 in 1500 calls, 21 of which were faster by 5 % and 12 slower.
+  // Tiles of 16 and of 32 slots were never faster than of 64 (16 slots each:
   // 304 and 281), tiles of 128 for one CTA hardly, splits by 8 not.
   auto stages_of = [&](int64_t tiles, int64_t at_a_time, double per_tile) {
     const double rounds = (double)tiles / (double)at_a_time;
@@ -157,9 +159,10 @@ bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, TcPlan* pl) 
   };
   int ks = 1;
   for (int k = 2; k <= farn::kTcMaxSplit && chunks >= k * 2; k *= 2)
-    if (cost_of_split(k) < cost_of_split(ks)) ks = k;
+    if (ctx->max_clusters[log2_of(k)] >= 1 && cost_of_split(k) < cost_of_split(ks)) ks = k;
   if (ctx->tc_split) ks = ctx->tc_split;
-  while (ks > chunks) ks /= 2;      // every CTA has a part of the row
+  // every CTA has a part of the row, and the device has room for the cluster
+  while (ks > 1 && (ks > chunks || ctx->max_clusters[log2_of(ks)] < 1)) ks /= 2;
   const double cost1 = cost_of_split(ks);
   const double cost2 = stages_of(tiles2, ctx->max_clusters[1], (double)chunks);
   bool use_pair = cost2 < cost1 || (cost2 == cost1 && p.S > 32 * groups);
