@@ -87,7 +87,10 @@ typedef struct farn_ctx farn_ctx;
  * fails this call, "launch" makes every launch of the context fail before
  * anything is enqueued, "stall" makes CTA 0 of every TMA-staged launch
  * wait out its time limit and report it in the status word (of the
- * tensor-core products: its weights never come).
+ * tensor-core products: its weights never come), "setup" makes the set-up of
+ * the router and of the products' tensor-core kernels fail.  Where that set-up
+ * fails the context serves the rest: farn_moe_route returns FARN_ERR_CUDA, and
+ * the products take their slower kernel (see farn_plan_grouped_matmul).
  * Returns FARN_ERR_INVALID_ARG if out is NULL or device < 0 or not a device
  * of this process, FARN_ERR_CUDA if the device cannot be queried (or
  * FARN_FAULT_INJECT=create), FARN_ERR_NOMEM. */

@@ -635,7 +635,8 @@ int farn_create(farn_ctx** out, int device) {
   // call, "launch" makes every launch of the new context fail (before
   // anything is enqueued), "stall" makes CTA 0 of every TMA-staged launch
   // of the new context wait out its time limit (2 s) and report it in the
-  // status word.  No per-call environment lookups.
+  // status word, "setup" makes the set-up of the router and of the products'
+  // tensor-core kernels fail.  No per-call environment lookups.
   const char* inject = getenv("FARN_FAULT_INJECT");
   if (inject && strcmp(inject, "create") == 0) return FARN_ERR_CUDA;
   const bool inject_launch = inject && strcmp(inject, "launch") == 0;
@@ -758,11 +759,13 @@ int farn_create(farn_ctx** out, int device) {
       if (fa.numRegs > regs) regs = fa.numRegs;
     }
   }
-  if (!farn_host::route_setup(c) || !farn_host::product_setup(c)) {
-    delete c;
-    cudaGetLastError();
-    return FARN_ERR_CUDA;
-  }
+  // The router and the products' tensor-core kernels: a context without them
+  // still serves everything else.
+  const bool inject_setup = inject && strcmp(inject, "setup") == 0;
+  c->route_ok = !inject_setup && farn_host::route_setup(c) ? 1 : 0;
+  c->encode_tiled = nullptr;
+  if (!inject_setup) farn_host::product_setup(c);
+  cudaGetLastError();
   // The bulk kernel's status word: set on a bounded-wait timeout, read and
   // cleared by farn_device_status.
   if (cudaMalloc((void**)&c->d_status, 256) != cudaSuccess ||

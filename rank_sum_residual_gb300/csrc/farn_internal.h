@@ -45,13 +45,16 @@ struct farn_ctx {
   int tc_tile;         // 0 = choose; else the products' tiles: 64 slots by one CTA, or 256
                        // (NVFP4: 224) by a pair
   int tc_split;        // 0 = choose; else CTAs that split a row: 1, 2 or 4
-  void* encode_tiled;  // the driver's tensor-map encoder (the products' kernels)
+  int route_ok;        // the router's kernels are set up
+  void* encode_tiled;  // the driver's tensor-map encoder; null: the products' tensor-core
+                       // kernels are not set up, and the plain one takes every call
   int max_clusters[3]; // clusters of 1, 2 and 4 of their CTAs that fit the device at a time
 };
 
 namespace farn_host {
 
-// One-time kernel set-up on the current device (farn_create).
+// One-time kernel set-up on the current device (farn_create).  False: the
+// router, or the products' tensor-core kernels, cannot be had.
 bool route_setup(const farn_ctx* ctx);
 bool product_setup(farn_ctx* ctx);
 

@@ -517,7 +517,7 @@ extern "C" int farn_moe_route(const farn_ctx* ctx, const void* logits, int logit
         if (overlaps(outs[i], bytes[i], outs[j], bytes[j])) return FARN_ERR_ALIAS;
     }
   }
-  if (ctx->fault_launch) return FARN_ERR_CUDA;
+  if (ctx->fault_launch || !ctx->route_ok) return FARN_ERR_CUDA;
 
   RouteParams p;
   p.logits = logits;

@@ -580,6 +580,38 @@ def test_two_threads_with_one_context(dev):
     assert not bad
 
 
+def test_context_without_the_tensor_cores(dev):
+    """Where the set-up of the router and of the tensor-core kernels fails the
+    context serves the rest: the norm's bits are the same, the products take
+    their slower kernel, the router says that it is not there."""
+    ctx = make_ctx(FARN_FAULT_INJECT="setup")
+    x, logits, up, _, res, weight = layer_inputs(dev, 40, 4, 64, 72, 2)
+    for a, b in zip(farn.forward([x, x], res, weight, 1e-6, ctx=ctx),
+                    farn.forward([x, x], res, weight, 1e-6)):
+        assert torch.equal(a, b)
+    with pytest.raises(farn.FarnError) as e:
+        farn.moe_route(logits, 2, ctx=ctx)
+    assert e.value.status == farn.FARN_ERR_CUDA
+    offsets = make_groups([10, 0, 25, 5])
+    w = integer((4, 72, 64), dev, 28)
+    a = 1 << 32
+    assert farn.farn_plan_grouped_matmul(ctx.handle, a, 40, 0, 40, 2 * a, 4, 72, 64,
+                                         3 * a)[0] == "generic"
+    xi = integer((40, 64), dev, 29)
+    got = farn.grouped_matmul(xi, w, torch.from_numpy(offsets).to(dev), ctx=ctx)
+    want, _ = grouped_reference(xi, w, offsets, None, 40)
+    check_exact(got, want, offsets, "no tensor cores")
+    # scales of 1: products are multiples of 1/4 and exact
+    q = torch.randint(0, 256, (40, 32), device=dev, dtype=torch.uint8,
+                      generator=torch.Generator(device=dev).manual_seed(30))
+    s = torch.full((40, 4), 0x38, device=dev, dtype=torch.uint8)
+    assert torch.equal(farn.nvfp4_matmul(q, s, 1.0, q, s, 1.0, ctx=ctx),
+                       farn.nvfp4_matmul(q, s, 1.0, q, s, 1.0))
+    for a, b in zip(farn.nvfp4_quantize(x, 100.0, ctx=ctx), farn.nvfp4_quantize(x, 100.0)):
+        assert torch.equal(a, b)
+    ctx.close()
+
+
 def test_launch_fault_reaches_the_caller(dev):
     bad = make_ctx(FARN_FAULT_INJECT="launch")
     x, logits, up, *_ = layer_inputs(dev, 4, 4, 64, 64, 1)
