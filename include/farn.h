@@ -370,7 +370,8 @@ int farn_moe_route(const farn_ctx *ctx, const void *logits, int logits_dtype,
  *            nothing
  * The fast kernels need x and weights 16-byte aligned and H a multiple of 8;
  * other shapes are served by a slower kernel.  Returns FARN_ERR_INVALID_ARG,
- * FARN_ERR_ALIAS (out over an input) or FARN_ERR_CUDA. */
+ * FARN_ERR_ALIAS (out over an input), FARN_ERR_UNSUPPORTED (2^30 or more tiles
+ * of 64 slots of one expert by 64 columns) or FARN_ERR_CUDA. */
 int farn_grouped_matmul(const farn_ctx *ctx, const void *x, int64_t n_rows,
                         const int32_t *rows, int64_t n_slots,
                         const void *weights, int E, const int32_t *offsets,
@@ -384,7 +385,7 @@ int farn_grouped_matmul(const farn_ctx *ctx, const void *x, int64_t n_rows,
  *   tensor_scale finite, > 0;  H a multiple of 16;  T == 0 launches nothing
  * x 16-byte and codes 8-byte aligned take the fast kernel.  Returns
  * FARN_ERR_INVALID_ARG, FARN_ERR_ALIAS, FARN_ERR_UNSUPPORTED (more than
- * 2^41 elements) or FARN_ERR_CUDA. */
+ * 2^45 - 2^14 elements) or FARN_ERR_CUDA. */
 int farn_nvfp4_quantize(const farn_ctx *ctx, const void *x, int64_t T, int64_t H,
                         float tensor_scale, void *codes, void *block_scale,
                         cudaStream_t stream);
@@ -412,7 +413,8 @@ int farn_nvfp4_dequantize(const farn_ctx *ctx, const void *codes,
  * The fast kernels need the codes 16-byte aligned and H a multiple of 32 (they
  * are faster still with H a multiple of 256 and the scales 16-byte aligned);
  * other shapes are served by a slower kernel.  Returns FARN_ERR_INVALID_ARG
- * (also for an alpha that fp32 cannot hold), FARN_ERR_ALIAS or
+ * (also for an alpha that fp32 cannot hold), FARN_ERR_ALIAS,
+ * FARN_ERR_UNSUPPORTED (2^30 or more tiles of 64 rows by 64 columns) or
  * FARN_ERR_CUDA. */
 int farn_nvfp4_matmul(const farn_ctx *ctx, const void *a_codes,
                       const void *a_scale, float a_tensor_scale,
@@ -427,7 +429,8 @@ int farn_nvfp4_matmul(const farn_ctx *ctx, const void *a_codes,
  * splitting the row), 7 pair (the tensor cores, two CTAs per tile of 256 by 256,
  * NVFP4 224, slots).  *ctas receives the CTAs per tile, *threads the threads per
  * CTA.  Returns a farn_status (FARN_ERR_INVALID_ARG for a bad or empty shape or
- * a NULL pointer; aliasing is not checked). */
+ * a NULL pointer, FARN_ERR_UNSUPPORTED as the call itself; aliasing is not
+ * checked). */
 int farn_plan_grouped_matmul(const farn_ctx *ctx, const void *x, int64_t n_rows,
                              const int32_t *rows, int64_t n_slots,
                              const void *weights, int E, int64_t N, int64_t H,

@@ -23,13 +23,18 @@ namespace {
 
 typedef void (*ProductKernel)(const ProductParams);
 
+// No more tiles than this: their numbers are 32-bit, with room for a step.
+constexpr int64_t kMaxTiles = 0x7FFFFFFF / 2;
+
+int64_t plain_tiles(const ProductParams& p) {
+  const int64_t slot_tiles = p.S / farn::kPlainTile + (p.E < p.S ? p.E : p.S);
+  return slot_tiles * ((p.N + farn::kPlainTile - 1) / farn::kPlainTile);
+}
+
 int launch_plain(const farn_ctx* ctx, const ProductParams& p, bool fp4, cudaStream_t stream) {
   // no fewer blocks than tiles for a small call; a long one walks
-  const int64_t slot_tiles = p.S / farn::kPlainTile + (p.E < p.S ? p.E : p.S);
-  const int64_t tiles =
-      slot_tiles * ((p.N + farn::kPlainTile - 1) / farn::kPlainTile);
+  const int64_t tiles = plain_tiles(p);
   const int64_t most = (int64_t)ctx->num_sms * 4;
-  if (tiles > 0x7FFFFFFF / 2) return FARN_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles < most ? tiles : most), 1, 1);
   cfg.blockDim = dim3(farn::kPlainThreads, 1, 1);
@@ -132,7 +137,7 @@ bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, TcPlan* pl) 
   const TcKind* pair = find_kind(fp4, 2, gather, copy);
   const int64_t tiles1 = tiles_of(one->bn, farn::kTcWeights);
   const int64_t tiles2 = tiles_of(pair->bn, 2 * farn::kTcWeights);
-  if (tiles1 > 0x7FFFFFFF / 2 || tiles2 > 0x7FFFFFFF / 2) return false;
+  if (tiles1 > kMaxTiles || tiles2 > kMaxTiles) return false;
   // One CTA per tile of 128 weights by 64 slots, with the row split over up to
   // four of them, or a pair of CTAs per tile of 256 by 256 (NVFP4: 224):
   // whichever has fewer stages one after the other.  A stage takes much the
@@ -285,12 +290,12 @@ int launch_tc(const farn_ctx* ctx, const ProductParams& p, bool fp4, const TcPla
 }
 
 int launch(const farn_ctx* ctx, const ProductParams& p, bool fp4, cudaStream_t stream) {
+  TcPlan pl;
+  const bool tc = tc_takes(ctx, p, fp4) && plan_tc(ctx, p, fp4, &pl);
+  if (!tc && plain_tiles(p) > kMaxTiles) return FARN_ERR_UNSUPPORTED;
   DeviceGuard dg(ctx->device);
   if (!dg.ok) { cudaGetLastError(); return FARN_ERR_CUDA; }
-  TcPlan pl;
-  if (tc_takes(ctx, p, fp4) && plan_tc(ctx, p, fp4, &pl))
-    return launch_tc(ctx, p, fp4, pl, stream);
-  return launch_plain(ctx, p, fp4, stream);
+  return tc ? launch_tc(ctx, p, fp4, pl, stream) : launch_plain(ctx, p, fp4, stream);
 }
 
 int report_plan(const farn_ctx* ctx, const ProductParams& p, bool fp4, int* variant, int* ctas,
@@ -300,6 +305,8 @@ int report_plan(const farn_ctx* ctx, const ProductParams& p, bool fp4, int* vari
     *variant = pl.kind->cg == 2 ? kVariantPair : kVariantTensor;
     *ctas = pl.kind->cg == 2 ? 2 : pl.ks;
     *threads = pl.kind->warps * 32;
+  } else if (plain_tiles(p) > kMaxTiles) {
+    return FARN_ERR_UNSUPPORTED;
   } else {
     *variant = kVariantGeneric;
     *ctas = 1;

@@ -134,6 +134,31 @@ def test_product_no_rows_launches_nothing(ctx):
     assert product(ctx, T=0, a_codes=0, a_scale=0, out=0) == farn.FARN_OK
 
 
+def test_too_many_tiles(ctx):
+    """More tiles than 32-bit numbers hold are refused before the device is
+    touched, by the call and by its plan query."""
+    n, far = (1 << 21) + 64, 1 << 46        # outputs of over 2^43 bytes
+    assert grouped(ctx, n_rows=n, rows=0, n_slots=n, E=1, N=n, H=1, out=far) == \
+        farn.FARN_ERR_UNSUPPORTED
+    assert product(ctx, T=n, N=n, H=16, out=far) == farn.FARN_ERR_UNSUPPORTED
+    with pytest.raises(farn.FarnError) as e:
+        farn.farn_plan_grouped_matmul(ctx, A, n, 0, n, C, 1, n, 1, far)
+    assert e.value.status == farn.FARN_ERR_UNSUPPORTED
+    with pytest.raises(farn.FarnError) as e:
+        farn.farn_plan_nvfp4_matmul(ctx, A, B, C, D, n, n, 16, far)
+    assert e.value.status == farn.FARN_ERR_UNSUPPORTED
+
+
+def test_too_many_elements(ctx):
+    """The conversions take 2^31 - 1 thread blocks of 2^14 elements."""
+    T = ((1 << 45) - (1 << 14)) // 16 + 1
+    far = dict(T=T, H=16)
+    assert quantize(ctx, x=1 << 50, codes=1 << 48, block_scale=1 << 47, **far) == \
+        farn.FARN_ERR_UNSUPPORTED
+    assert dequantize(ctx, out=1 << 50, codes=1 << 48, block_scale=1 << 47, **far) == \
+        farn.FARN_ERR_UNSUPPORTED
+
+
 def test_plan_queries_refuse(ctx):
     good = dict(x=A, n_rows=4, rows=B, n_slots=8, weights=C, E=3, N=32, H=64, out=E_)
     for kw in (dict(n_slots=0), dict(N=0), dict(E=1025), dict(weights=0), dict(out=0),
