@@ -683,6 +683,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
       int32_t tile = t0;
       int gi = 0;                             // group of the tile
       uint32_t asked = 0, done = 0;           // groups so far
+      uint32_t coming = 0;                    // slots whose block TMA was asked for, a bit each
       Tile w = {};
       auto ask = [&]() {                      // false: no more, or gave up
         if (tile >= tiles) return false;
@@ -694,7 +695,9 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
           return false;
         }
         // slots above 128 that the tile does not have are not loaded
+        coming &= ~(1u << slot);
         if (u < 2 || w.n > 128) {
+          coming |= 1u << slot;
           if (tc::elect_one()) {
             const uint32_t bar = sraw0 + 8 * (slot * 3 + u);
             const uint32_t dst = base + t.scales_at + slot * Sh::kScaleSlot + u * kTcScaleBlock;
@@ -738,6 +741,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
         // after an abort: what was asked for lands before the CTA leaves
         for (; done < asked; ++done) {
           const uint32_t slot = done % kTcScaleSlots;
+          if (!(coming >> slot & 1)) continue;
           const uint64_t begin = globaltimer_ns();
           while (!tc::mbar_wait_some<true>(sraw0 + 8 * (slot * 3 + u), phases >> slot & 1,
                                            kTcSleepNs) &&

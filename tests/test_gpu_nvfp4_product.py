@@ -1,6 +1,7 @@
 """NVFP4 quantisation, the way back and the product of two NVFP4 tensors on
 the GPU, against the oracle's codes and plain 64-bit definitions."""
 import math
+import time
 
 import numpy as np
 import pytest
@@ -250,6 +251,22 @@ def test_product_waits_are_bounded(dev, env, H):
     got = farn.nvfp4_matmul(*a, 1.0, *b, 1.0)
     want = (values(*a) @ values(*b).t()).float().to(torch.bfloat16)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T", [100, 300])
+def test_product_gives_up_within_its_limit(dev, T):
+    """A CTA that gave up waits for what it asked for and no longer, also where
+    a tile has so few slots that a block of their scales is not loaded: the
+    call takes one limit of 2 s, not several."""
+    ctx = make_ctx(FARN_FAULT_INJECT="stall", FARN_TC_TILE=256)
+    a, b = random_tensor(dev, T, 2048, 21, [0x38]), random_tensor(dev, 600, 2048, 22, [0x38])
+    torch.cuda.synchronize()
+    t0 = time.monotonic()
+    farn.nvfp4_matmul(*a, 1.0, *b, 1.0, ctx=ctx)
+    torch.cuda.synchronize()
+    assert time.monotonic() - t0 < 3.5
+    assert farn.farn_device_status(ctx.handle) & (16 | 32 | 64 | 128)
+    ctx.close()
 
 
 def test_product_plans(dev, ctxs):
