@@ -524,6 +524,59 @@ def test_moe_layer_in_a_graph_and_on_streams(dev):
             assert torch.equal(a, b)
 
 
+def test_prepared_layer_reuses_its_buffers(dev):
+    """Prepared calls, launched again after their inputs changed in place, give
+    the immediate calls' bits, into their own outputs or into given ones."""
+    K, E, H, F, T = 2, 8, 128, 192, 33
+    x, logits, up, *_ = layer_inputs(dev, T, E, H, F, 61)
+    other = layer_inputs(dev, T, E, H, F, 62)
+    route = farn.prepare_moe_route(logits, K, renormalize=False)
+    _, _, _, rows, offsets = route.outputs
+    given = torch.empty(T * K, F, dtype=torch.bfloat16, device=dev)
+    gather = farn.prepare_grouped_matmul(x, up, offsets, rows, out=given)
+    back = torch.empty(E, H, F, dtype=torch.bfloat16, device=dev).copy_(up.transpose(1, 2))
+    down = farn.prepare_grouped_matmul(given, back, offsets)
+    for again in range(3):
+        if again:
+            x.copy_(other[0]), logits.copy_(other[1].roll(again, 0))
+        a, h, y = route(), gather(), down()
+        assert h is given
+        b = farn.moe_route(logits, K, renormalize=False)
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+        want = farn.grouped_matmul(x, up, b[4], b[3])
+        assert torch.equal(h, want)
+        assert torch.equal(y, farn.grouped_matmul(want, back, b[4]))
+
+
+@pytest.mark.parametrize("prepared", [False, True])
+def test_layer_on_a_given_stream(dev, prepared):
+    """The calls run on the stream that they are given: behind what it has to
+    do first, here the inputs, while the current stream stays idle."""
+    K, E, H, F, T = 3, 8, 128, 72, 50
+    x, logits, up, *_ = layer_inputs(dev, T, E, H, F, 63)
+    want_r = farn.moe_route(logits, K)
+    want_h = farn.grouped_matmul(x, up, want_r[4], want_r[3])
+    late = [torch.zeros_like(t) for t in (x, logits)]
+    side = torch.cuda.Stream()
+    out = [torch.empty_like(t) for t in want_r]
+    h = torch.empty_like(want_h)
+    torch.cuda.synchronize()
+    if prepared:
+        calls = [farn.prepare_moe_route(late[1], K, out=out, stream=side),
+                 farn.prepare_grouped_matmul(late[0], up, out[4], out[3], out=h, stream=side)]
+    else:
+        calls = [lambda: farn.moe_route(late[1], K, out=out, stream=side),
+                 lambda: farn.grouped_matmul(late[0], up, out[4], out[3], out=h, stream=side)]
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+        late[0].copy_(x), late[1].copy_(logits)
+    for call in calls:
+        call()
+    assert torch.cuda.current_stream().query() and not side.query()
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(out, want_r)) and torch.equal(h, want_h)
+
+
 def test_context_of_another_device_is_refused(dev):
     x, logits, up, *_ = layer_inputs(dev, 4, 4, 64, 64, 1)
     off = torch.tensor([0, 1, 2, 3, 4], dtype=torch.int32, device=dev)

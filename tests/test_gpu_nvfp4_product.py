@@ -317,6 +317,56 @@ def test_norm_to_product(dev):
         assert torch.equal(a, b)
 
 
+def test_prepared_calls_reuse_their_buffers(dev):
+    """Prepared conversions and products, launched again after their input
+    changed in place, give the immediate calls' bits."""
+    T, H, N = 21, 512, 144
+    x, w = inputs(dev, T, H, 31), inputs(dev, N, H, 32)
+    wq, ws = farn.nvfp4_quantize(w, 200.0)
+    quantize = farn.prepare_nvfp4_quantize(x, 100.0)
+    q, s = quantize.outputs
+    given = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
+    back = farn.prepare_nvfp4_dequantize(q, s, 100.0)
+    product = farn.prepare_nvfp4_matmul(q, s, 100.0, wq, ws, 200.0, out=given)
+    for seed in (33, 34):
+        x.copy_(inputs(dev, T, H, seed))
+        quantize()
+        q2, s2 = farn.nvfp4_quantize(x, 100.0)
+        assert torch.equal(q, q2) and torch.equal(s, s2)
+        assert torch.equal(back(), farn.nvfp4_dequantize(q2, s2, 100.0))
+        assert product() is given
+        assert torch.equal(given, farn.nvfp4_matmul(q2, s2, 100.0, wq, ws, 200.0))
+
+
+@pytest.mark.parametrize("prepared", [False, True])
+def test_calls_on_a_given_stream(dev, prepared):
+    """The calls run on the stream that they are given, behind what it has to
+    do first, while the current stream stays idle."""
+    T, H, N = 40, 512, 144
+    x, w = inputs(dev, T, H, 35), inputs(dev, N, H, 36)
+    wq, ws = farn.nvfp4_quantize(w, 200.0)
+    q0, s0 = farn.nvfp4_quantize(x, 100.0)
+    want = farn.nvfp4_dequantize(q0, s0, 100.0), farn.nvfp4_matmul(q0, s0, 100.0, wq, ws, 200.0)
+    late, q, s = torch.zeros_like(x), torch.empty_like(q0), torch.empty_like(s0)
+    back, y = torch.empty_like(want[0]), torch.empty_like(want[1])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    pick = (lambda name: getattr(farn, "prepare_" + name)) if prepared else \
+        (lambda name: lambda *a, **k: lambda: getattr(farn, name)(*a, **k))
+    calls = [pick("nvfp4_quantize")(late, 100.0, out=(q, s), stream=side),
+             pick("nvfp4_dequantize")(q, s, 100.0, out=back, stream=side),
+             pick("nvfp4_matmul")(q, s, 100.0, wq, ws, 200.0, out=y, stream=side)]
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+        late.copy_(x)
+    for call in calls:
+        call()
+    assert torch.cuda.current_stream().query() and not side.query()
+    side.synchronize()
+    assert torch.equal(q, q0) and torch.equal(s, s0)
+    assert torch.equal(back, want[0]) and torch.equal(y, want[1])
+
+
 def test_launch_fault_reaches_the_caller(dev):
     bad = make_ctx(FARN_FAULT_INJECT="launch")
     x = inputs(dev, 4, 64, 1)
