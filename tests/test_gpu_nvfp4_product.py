@@ -257,7 +257,9 @@ def test_product_waits_are_bounded(dev, env, H):
 def test_product_gives_up_within_its_limit(dev, T):
     """A CTA that gave up waits for what it asked for and no longer, also where
     a tile has so few slots that a block of their scales is not loaded: the
-    call takes one limit of 2 s, not several."""
+    call takes one limit of 2 s, not several.  (A block that is not loaded is
+    left to wait for only behind a tile that gave up on one that is; no call
+    can be made to do that, so this holds the plain cases.)"""
     ctx = make_ctx(FARN_FAULT_INJECT="stall", FARN_TC_TILE=256)
     a, b = random_tensor(dev, T, 2048, 21, [0x38]), random_tensor(dev, 600, 2048, 22, [0x38])
     torch.cuda.synchronize()
