@@ -23,12 +23,13 @@
 // overlap the products of the next.
 //
 // What bounds it (GB300, us and rates of the kernel alone): bf16 8192^3 takes
-// 545 us (2.02 PFLOP/s, 105 % of the measured library rate) with the tensor
-// pipe 93 % busy, under the power limit; NVFP4 8192^3 172 us (6.4 PFLOP/s), 69 %
+// 564 us (1.95 PFLOP/s, 101 % of the measured library rate) with the tensor
+// pipe 92 % busy, under the power limit; NVFP4 8192^3 173 us (6.35 PFLOP/s; 195
+// to 200 us in a row of calls, where the power limit lowers the clock), 69 %
 // busy: a stage's synchronisation takes about 600 cycles, its products 450.
-// 64 experts of 64 tokens, 2048 -> 7168: 279 us, the weights at 6.8 TB/s (101 %
+// 64 experts of 64 tokens, 2048 -> 7168: 280 us, the weights at 6.7 TB/s (101 %
 // of the measured copy rate).  One token, 8 experts, 7168 -> 2048: 41 us
-// (86 %).  One token, NVFP4 8192 x 8192: 13 us against 5.6 us for its bytes:
+// (86 %).  One token, NVFP4 8192 x 8192: 14 us against 5.6 us for its bytes:
 // launch, first loads and the join of the split rows.
 //
 // Every wait is bounded (see tc_wait); a CTA that gives up sets its bit in the
