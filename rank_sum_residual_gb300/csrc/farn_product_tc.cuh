@@ -592,7 +592,7 @@ farn_product_tc_kernel(const __grid_constant__ TcParams t,
                                n0 + warp * 32, lane);
         }
       }
-      tc::fence_before();
+      tc::fence_before();       // orders the reads of tensor memory before the arrival
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_first<CG>(tempty0 + 8 * acc);
       if (split) {
