@@ -442,6 +442,165 @@ int farn_plan_nvfp4_matmul(const farn_ctx *ctx, const void *a_codes,
                            const void *out, int *variant, int *ctas,
                            int *threads);
 
+/* farn_fp8_quantize - E4M3 codes and fp32 scales of bf16 matrices x [E, T, H]
+ * (E = 1: one matrix), in blocks of 128 elements of a row (block_rows 1:
+ * activations) or of 128 rows by 128 columns (block_rows 128: weights); the
+ * operands of the FP8 products.  Per block, the last ones of a row or matrix
+ * being shorter:
+ *     amax  = max |x| over the block (NaN ignored)
+ *     scale = amax / 448, or 1 if amax is 0     (fp32; x ~ code * scale)
+ *     code  = E4M3(x * inv),  inv = min(448 / amax, FLT_MAX) (fp32), or 1
+ * with the conversion of farn_forward_quant (nearest even, saturating, NaN
+ * stays NaN).  A block with an infinity has scale inf and codes 0 and NaN: its
+ * values are all NaN.
+ *   codes   uint8 [E, T, H]
+ *   scales  fp32 [E, ceil(T / block_rows), ceil(H / 128)], 4-byte aligned
+ *   E == 0 or T == 0 launches nothing
+ * x 16-byte and codes 8-byte aligned with H a multiple of 8 take the fast
+ * kernel.  Returns FARN_ERR_INVALID_ARG, FARN_ERR_ALIAS, FARN_ERR_UNSUPPORTED
+ * (2^31 or more blocks of 128 rows, or 2^37 or more of one row) or
+ * FARN_ERR_CUDA. */
+int farn_fp8_quantize(const farn_ctx *ctx, const void *x, int64_t E, int64_t T,
+                      int64_t H, int block_rows, void *codes, float *scales,
+                      cudaStream_t stream);
+
+/* farn_fp8_matmul - the product of two E4M3 tensors with block scales, for
+ * example activations by weights:
+ *     out[t,n] = bf16( sum_b s[t,n,b] * sum_{h in block b} f(a[t,h]) * f(b[n,h]) )
+ *     s[t,n,b] = a_scale[t,b] * b_scale[n / 128, b],  rounded to fp32
+ * over the blocks b of 128 elements of a row, every sum in fp32 (the order is
+ * the kernel's own and the same in every call with the same arguments), one
+ * rounding to bf16.
+ *   a_codes uint8 [T, H], a_scale fp32 [T, ceil(H/128)];
+ *   b_codes uint8 [N, H], b_scale fp32 [ceil(N/128), ceil(H/128)]: what
+ *   farn_fp8_quantize makes with block_rows 1 and 128;  out bf16 [T, N]
+ *   T, N, H < 2^31; T == 0 launches nothing
+ * The fast kernels need the codes 16-byte aligned and H a multiple of 16; other
+ * shapes are served by a slower kernel.  Returns FARN_ERR_INVALID_ARG,
+ * FARN_ERR_ALIAS, FARN_ERR_UNSUPPORTED (2^30 or more tiles of 64 rows by 64
+ * columns) or FARN_ERR_CUDA. */
+int farn_fp8_matmul(const farn_ctx *ctx, const void *a_codes,
+                    const float *a_scale, const void *b_codes,
+                    const float *b_scale, int64_t T, int64_t N, int64_t H,
+                    void *out, cudaStream_t stream);
+
+/* farn_fp8_grouped_matmul - farn_grouped_matmul on E4M3 codes with block
+ * scales: x [n_rows, H] with x_scale [n_rows, ceil(H/128)], weights [E, N, H]
+ * with w_scale [E, ceil(N/128), ceil(H/128)].  Slots, rows, offsets, out and
+ * errors as there; arithmetic as in farn_fp8_matmul. */
+int farn_fp8_grouped_matmul(const farn_ctx *ctx, const void *x,
+                            const float *x_scale, int64_t n_rows,
+                            const int32_t *rows, int64_t n_slots,
+                            const void *weights, const float *w_scale, int E,
+                            const int32_t *offsets, int64_t N, int64_t H,
+                            void *out, cudaStream_t stream);
+
+/* farn_qk_norm_rope - RMSNorm of every query and key head and its rotation by
+ * position, in one pass.  For a head's elements x[0..D):
+ *     y[i] = (x[i] * rstd) * f(weight[i]),  rstd = 1 / sqrt(mean(x^2) + eps)
+ *            (y = x where the weight is NULL)
+ *     for the pairs j < R/2 of the first R elements, (a, b) = (y[j], y[j + R/2]),
+ *     or (y[2j], y[2j+1]) with `interleaved`:
+ *            (a cos w - b sin w, b cos w + a sin w),  w = positions[axis(j), t] * freqs[j]
+ *     elements from R on stay y
+ * in fp32, one rounding to bf16.  The angle is exact to 2^-31 of a turn whatever
+ * the position (|freqs| up to 2^8).
+ *   T, D        tokens (< 2^31; 0 launches nothing), elements of a head (1 .. 1024)
+ *   q           bf16 [T, q_heads, D], tokens q_stride elements apart (at least
+ *               q_heads * D): heads may be read where a projection wrote them;
+ *               k the same.  Either may have 0 heads (its pointers are not read).
+ *   q_weight, k_weight  bf16 [D] or NULL
+ *   positions   int32 [axes, T], axes 1 .. 4; freqs fp32 [R / 2], finite
+ *   sections    host array [axes]: how many pairs turn by each axis, in order;
+ *               their sum is R / 2
+ *   R           even, 0 .. D; 0: no rotation (axes, sections, positions and freqs
+ *               are not read)
+ *   q_out, k_out  bf16, with strides of their own; each may be exactly its input
+ *               (same address and stride), and rows of equal strides may lie
+ *               between each other's
+ * Fast: D and the strides multiples of 8, D <= 256, pointers 16-byte aligned, and
+ * R a multiple of 16 unless interleaved; else a slower kernel.  Returns
+ * FARN_ERR_INVALID_ARG, FARN_ERR_ALIAS or FARN_ERR_CUDA. */
+int farn_qk_norm_rope(const farn_ctx *ctx, int64_t T, int D, const void *q,
+                      int q_heads, int64_t q_stride, const void *k, int k_heads,
+                      int64_t k_stride, const void *q_weight,
+                      const void *k_weight, float eps, const int32_t *positions,
+                      int axes, const int *sections, const float *freqs, int R,
+                      int interleaved, void *q_out, int64_t q_out_stride,
+                      void *k_out, int64_t k_out_stride, cudaStream_t stream);
+
+/* Formats of a cache of keys and values. */
+#define FARN_CACHE_FP8 1    /* E4M3 codes, an fp32 scale per token and head */
+#define FARN_CACHE_NVFP4 2  /* farn_nvfp4_quantize's codes and block scales */
+
+/* A paged cache of keys and values.  Slot s of the cache, page s / page_size,
+ * holds one token's `heads` rows of head_dim values, of keys and of values.
+ *   codes   uint8 [n_pages, page_size, heads, head_dim] (FARN_CACHE_FP8) or
+ *           [.., head_dim / 2] (FARN_CACHE_NVFP4, head_dim a multiple of 16)
+ *   scale   fp32 [n_pages, page_size, heads], or uint8 [.., head_dim / 16]
+ *   tensor scales: NVFP4 only, finite, > 0
+ * n_pages * page_size < 2^31; head_dim 1 .. 1024.  A row in FARN_CACHE_FP8 is one
+ * block of farn_fp8_quantize's arithmetic. */
+typedef struct {
+    int format;
+    int page_size;
+    int64_t n_pages;
+    int heads, head_dim;
+    void *k_codes, *v_codes;
+    void *k_scale, *v_scale;
+    float k_tensor_scale, v_tensor_scale;
+} farn_kv_cache;
+
+/* farn_qk_norm_rope with keys and values written to a cache instead: the
+ * queries go to q_out, token t's keys (normed and rotated) and values (as they
+ * are) to slot slots[t], quantised from fp32.  A slot outside the cache (for
+ * example -1, padding) is skipped; its queries are written all the same.  The
+ * slots of one call have to differ: a slot that two tokens write holds codes and
+ * scales of either.  slots int32 [T]; v bf16 [T, kv_heads, D].  q_heads may be 0.
+ * Returns FARN_ERR_INVALID_ARG (also for a cache of other sizes),
+ * FARN_ERR_ALIAS or FARN_ERR_CUDA. */
+int farn_qk_norm_rope_cache(const farn_ctx *ctx, int64_t T, int D,
+                            const void *q, int q_heads, int64_t q_stride,
+                            const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, int kv_heads,
+                            const void *q_weight, const void *k_weight,
+                            float eps, const int32_t *positions, int axes,
+                            const int *sections, const float *freqs, int R,
+                            int interleaved, void *q_out, int64_t q_out_stride,
+                            const farn_kv_cache *cache, const int32_t *slots,
+                            cudaStream_t stream);
+
+/* farn_kv_write - keys and values bf16 [T, heads, head_dim] (token strides of
+ * their own) quantised into the cache's slots, as they are.  Otherwise as
+ * farn_qk_norm_rope_cache. */
+int farn_kv_write(const farn_ctx *ctx, int64_t T, const void *k,
+                  int64_t k_stride, const void *v, int64_t v_stride,
+                  const farn_kv_cache *cache, const int32_t *slots,
+                  cudaStream_t stream);
+
+/* farn_kv_read - the contexts of B sequences back in bf16, one after the
+ * other: output token n of sequence b, offsets[b] <= n < offsets[b+1], is the
+ * sequence's token i = n - offsets[b], in slot table[b, i / page_size] *
+ * page_size + i % page_size:
+ *     fp8    bf16(value(code) * scale)
+ *     nvfp4  bf16(value(code) * (value(block scale) / tensor_scale)), as
+ *            farn_nvfp4_dequantize
+ *   table    int32 [B, width];  a page outside the cache, or beyond the table,
+ *            reads as zeros
+ *   offsets  int32 [B + 1] on the device, ascending, within 0 .. n_tokens.
+ *            (Other values cannot lead outside the tensors, but the outputs
+ *            are then unspecified.)
+ *   k_out, v_out  bf16 [n_tokens, heads, head_dim]; tokens below offsets[0] and
+ *            from offsets[B] on are left as they were
+ * n_tokens == 0 or B == 0 launches nothing.  Fast: head_dim a multiple of 8,
+ * codes 8-byte (NVFP4: 4-byte) and outputs 16-byte aligned.  Returns
+ * FARN_ERR_INVALID_ARG, FARN_ERR_ALIAS, FARN_ERR_UNSUPPORTED (heads * head_dim
+ * of 2^26 or more) or FARN_ERR_CUDA. */
+int farn_kv_read(const farn_ctx *ctx, const farn_kv_cache *cache,
+                 const int32_t *table, int B, int64_t width,
+                 const int32_t *offsets, int64_t n_tokens, void *k_out,
+                 void *v_out, cudaStream_t stream);
+
 /* Flags of farn_plan_typed. */
 #define FARN_PLAN_FP8_OUT 1   /* the call also writes the FP8 norm output */
 #define FARN_PLAN_NVFP4_OUT 2 /* the call also writes the NVFP4 norm output */

@@ -34,6 +34,11 @@ __all__ = [
     "farn_nvfp4_quantize", "nvfp4_quantize", "farn_nvfp4_dequantize", "nvfp4_dequantize",
     "farn_nvfp4_matmul", "nvfp4_matmul",
     "farn_plan_grouped_matmul", "farn_plan_nvfp4_matmul",
+    "farn_fp8_quantize", "fp8_quantize", "farn_fp8_matmul", "fp8_matmul",
+    "farn_fp8_grouped_matmul", "fp8_grouped_matmul",
+    "FARN_CACHE_FP8", "FARN_CACHE_NVFP4", "KvCache", "kv_cache",
+    "farn_qk_norm_rope", "qk_norm_rope", "farn_qk_norm_rope_cache", "qk_norm_rope_cache",
+    "farn_kv_write", "kv_write", "farn_kv_read", "kv_read",
     "FARN_BF16", "FARN_F32",
     "forward", "VARIANTS",
 ]
@@ -49,6 +54,18 @@ FARN_ERR_NOMEM = -5
 VARIANTS = {0: "row", 1: "cluster", 2: "generic", 3: "bulk", 4: "stage", 5: "combine",
             6: "tensor", 7: "pair"}
 FARN_BF16, FARN_F32 = 0, 1
+FARN_CACHE_FP8, FARN_CACHE_NVFP4 = 1, 2
+
+
+class KvCache(ctypes.Structure):
+    """C ``farn_kv_cache``: a paged cache of keys and values, as raw device
+    addresses."""
+    _fields_ = [("format", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("n_pages", ctypes.c_int64), ("heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_tensor_scale", ctypes.c_float), ("v_tensor_scale", ctypes.c_float)]
+
 
 _lib = None
 
@@ -105,6 +122,25 @@ def _load():
         lib.farn_plan_nvfp4_matmul.argtypes = [vp, cvp, cvp, cvp, cvp, i64, i64, i64, cvp, pi, pi,
                                                pi]
         lib.farn_plan_nvfp4_matmul.restype = i32
+        lib.farn_fp8_quantize.argtypes = [vp, cvp, i64, i64, i64, i32, vp, vp, vp]
+        lib.farn_fp8_quantize.restype = i32
+        lib.farn_fp8_matmul.argtypes = [vp, cvp, cvp, cvp, cvp, i64, i64, i64, vp, vp]
+        lib.farn_fp8_matmul.restype = i32
+        lib.farn_fp8_grouped_matmul.argtypes = [vp, cvp, cvp, i64, cvp, i64, cvp, cvp, i32, cvp,
+                                                i64, i64, vp, vp]
+        lib.farn_fp8_grouped_matmul.restype = i32
+        pc, pi = ctypes.POINTER(KvCache), ctypes.POINTER(i32)
+        rope = [cvp, cvp, f32, cvp, i32, pi, cvp, i32, i32]
+        lib.farn_qk_norm_rope.argtypes = [vp, i64, i32, cvp, i32, i64, cvp, i32, i64, *rope, vp,
+                                          i64, vp, i64, vp]
+        lib.farn_qk_norm_rope.restype = i32
+        lib.farn_qk_norm_rope_cache.argtypes = [vp, i64, i32, cvp, i32, i64, cvp, i64, cvp, i64,
+                                                i32, *rope, vp, i64, pc, cvp, vp]
+        lib.farn_qk_norm_rope_cache.restype = i32
+        lib.farn_kv_write.argtypes = [vp, i64, cvp, i64, cvp, i64, pc, cvp, vp]
+        lib.farn_kv_write.restype = i32
+        lib.farn_kv_read.argtypes = [vp, pc, cvp, i32, i64, cvp, i64, vp, vp, vp]
+        lib.farn_kv_read.restype = i32
         lib.farn_check_args.argtypes = [pvp, i32, cvp, cvp, f32, i64, i64,
                                         cvp, cvp, cvp]
         lib.farn_check_args.restype = i32
@@ -260,6 +296,75 @@ def farn_nvfp4_matmul(ctx, a_codes, a_scale, a_tensor_scale, b_codes, b_scale, b
         _addr(ctx), _addr(a_codes), _addr(a_scale), float(a_tensor_scale), _addr(b_codes),
         _addr(b_scale), float(b_tensor_scale), int(T), int(N), int(H), _addr(out),
         _addr(stream))
+
+
+def farn_fp8_quantize(ctx, x, E, T, H, block_rows, codes, scales, stream=0) -> int:
+    """C ``farn_fp8_quantize`` on raw device addresses (ints)."""
+    return _load().farn_fp8_quantize(_addr(ctx), _addr(x), int(E), int(T), int(H),
+                                     int(block_rows), _addr(codes), _addr(scales), _addr(stream))
+
+
+def farn_fp8_matmul(ctx, a_codes, a_scale, b_codes, b_scale, T, N, H, out, stream=0) -> int:
+    """C ``farn_fp8_matmul`` on raw device addresses (ints)."""
+    return _load().farn_fp8_matmul(_addr(ctx), _addr(a_codes), _addr(a_scale), _addr(b_codes),
+                                   _addr(b_scale), int(T), int(N), int(H), _addr(out),
+                                   _addr(stream))
+
+
+def farn_fp8_grouped_matmul(ctx, x, x_scale, n_rows, rows, n_slots, weights, w_scale, E, offsets,
+                            N, H, out, stream=0) -> int:
+    """C ``farn_fp8_grouped_matmul`` on raw device addresses (ints); rows 0 for
+    slot s reading row s."""
+    return _load().farn_fp8_grouped_matmul(
+        _addr(ctx), _addr(x), _addr(x_scale), int(n_rows), _addr(rows), int(n_slots),
+        _addr(weights), _addr(w_scale), int(E), _addr(offsets), int(N), int(H), _addr(out),
+        _addr(stream))
+
+
+def _int_array(v):
+    return None if v is None else (ctypes.c_int * max(1, len(v)))(*[int(x) for x in v])
+
+
+def farn_qk_norm_rope(ctx, T, D, q, q_heads, q_stride, k, k_heads, k_stride, q_weight, k_weight,
+                      eps, positions, axes, sections, freqs, R, interleaved, q_out, q_out_stride,
+                      k_out, k_out_stride, stream=0) -> int:
+    """C ``farn_qk_norm_rope`` on raw device addresses (ints); sections a
+    sequence of ints or None."""
+    return _load().farn_qk_norm_rope(
+        _addr(ctx), int(T), int(D), _addr(q), int(q_heads), int(q_stride), _addr(k), int(k_heads),
+        int(k_stride), _addr(q_weight), _addr(k_weight), float(eps), _addr(positions), int(axes),
+        _int_array(sections), _addr(freqs), int(R), int(interleaved), _addr(q_out),
+        int(q_out_stride), _addr(k_out), int(k_out_stride), _addr(stream))
+
+
+def _cache_ref(cache):
+    return None if cache is None else ctypes.byref(cache)
+
+
+def farn_qk_norm_rope_cache(ctx, T, D, q, q_heads, q_stride, k, k_stride, v, v_stride, kv_heads,
+                            q_weight, k_weight, eps, positions, axes, sections, freqs, R,
+                            interleaved, q_out, q_out_stride, cache, slots, stream=0) -> int:
+    """C ``farn_qk_norm_rope_cache`` on raw device addresses (ints); cache a
+    ``KvCache``."""
+    return _load().farn_qk_norm_rope_cache(
+        _addr(ctx), int(T), int(D), _addr(q), int(q_heads), int(q_stride), _addr(k),
+        int(k_stride), _addr(v), int(v_stride), int(kv_heads), _addr(q_weight), _addr(k_weight),
+        float(eps), _addr(positions), int(axes), _int_array(sections), _addr(freqs), int(R),
+        int(interleaved), _addr(q_out), int(q_out_stride), _cache_ref(cache), _addr(slots),
+        _addr(stream))
+
+
+def farn_kv_write(ctx, T, k, k_stride, v, v_stride, cache, slots, stream=0) -> int:
+    """C ``farn_kv_write`` on raw device addresses (ints); cache a ``KvCache``."""
+    return _load().farn_kv_write(_addr(ctx), int(T), _addr(k), int(k_stride), _addr(v),
+                                 int(v_stride), _cache_ref(cache), _addr(slots), _addr(stream))
+
+
+def farn_kv_read(ctx, cache, table, B, width, offsets, n_tokens, k_out, v_out, stream=0) -> int:
+    """C ``farn_kv_read`` on raw device addresses (ints); cache a ``KvCache``."""
+    return _load().farn_kv_read(_addr(ctx), _cache_ref(cache), _addr(table), int(B), int(width),
+                                _addr(offsets), int(n_tokens), _addr(k_out), _addr(v_out),
+                                _addr(stream))
 
 
 def farn_forward_noalloc(device, partials, W, residual, weight, eps, T, H,
@@ -886,4 +991,471 @@ def nvfp4_matmul(a_codes, a_scale, a_tensor_scale: float, b_codes, b_scale,
     args, out, _ = _nvfp4_matmul_args(a_codes, a_scale, a_tensor_scale, b_codes, b_scale,
                                       b_tensor_scale, out, ctx, stream)
     _call(_load().farn_nvfp4_matmul, args, "farn_nvfp4_matmul")
+    return out
+
+
+def _context_of(ctx, index):
+    c = ctx if ctx is not None else _context_for(index)
+    if c.device != index:
+        raise ValueError(f"the context is for device {c.device}, the tensors are on {index}")
+    return c
+
+
+def _fp8_quantize_args(x, block_rows, out, ctx, stream):
+    torch = _torch or _load_torch()
+    sx, index = x.shape, x.get_device()
+    if len(sx) not in (2, 3):
+        raise ValueError("x must be [T, H] or [E, T, H]")
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
+    if not (index >= 0 and x.dtype is torch.bfloat16 and x.is_contiguous()):
+        _check_tensor(x, "x", sx, x.device)
+    T, H = sx[-2:]
+    if H < 1:
+        raise ValueError("x must have at least one column")
+    shape = (*sx[:-2], -(-T // block_rows), -(-H // 128))
+    if out is None:
+        dev = x.device
+        out = (torch.empty(sx, dtype=torch.uint8, device=dev),
+               torch.empty(shape, dtype=torch.float32, device=dev))
+    else:
+        out = tuple(out)
+        if len(out) != 2:
+            raise ValueError("out must be (codes, scales)")
+        _check_tensor(out[0], "codes", sx, x.device, (torch.uint8,))
+        _check_tensor(out[1], "scales", shape, x.device, (torch.float32,))
+    c = _context_of(ctx, index)
+    return (c.handle, x.data_ptr(), sx[0] if len(sx) == 3 else 1, T, H, block_rows,
+            out[0].data_ptr(), out[1].data_ptr(), _raw_stream(stream, index)), out, c
+
+
+def prepare_fp8_quantize(x, block_rows: int = 1, out=None, ctx=None, stream=None):
+    """``fp8_quantize`` checked and marshalled once."""
+    args, out, c = _fp8_quantize_args(x, block_rows, out, ctx, stream)
+    return PreparedCall(_load().farn_fp8_quantize, args, "farn_fp8_quantize", out, (x, c))
+
+
+def fp8_quantize(x, block_rows: int = 1, out=None, ctx=None, stream=None):
+    """E4M3 codes and fp32 scales of a bf16 tensor [T,H] or [E,T,H], in blocks
+    of 128 elements of a row (block_rows 1: activations) or of 128 rows by 128
+    columns (block_rows 128: weights).  Returns (codes uint8 of x's shape,
+    scales fp32 [..,ceil(T/block_rows),ceil(H/128)]): the operands of
+    ``fp8_matmul`` and ``fp8_grouped_matmul``."""
+    args, out, _ = _fp8_quantize_args(x, block_rows, out, ctx, stream)
+    _call(_load().farn_fp8_quantize, args, "farn_fp8_quantize")
+    return out
+
+
+def _fp8_matmul_args(a_codes, a_scale, b_codes, b_scale, out, ctx, stream):
+    torch = _torch or _load_torch()
+    u8, f32 = torch.uint8, torch.float32
+    index = a_codes.get_device()
+    sa, sb = a_codes.shape, b_codes.shape
+    if len(sa) != 2 or len(sb) != 2:
+        raise ValueError("a_codes must be [T, H] and b_codes [N, H]")
+    T, H = sa
+    N = sb[0]
+    HB, NB = -(-H // 128), -(-N // 128)
+    if not (sb[1] == H and index >= 0 and b_codes.get_device() == index and
+            a_scale.get_device() == index and b_scale.get_device() == index and
+            a_codes.dtype is u8 and b_codes.dtype is u8 and a_scale.dtype is f32 and
+            b_scale.dtype is f32 and a_scale.shape == (T, HB) and b_scale.shape == (NB, HB) and
+            a_codes.is_contiguous() and b_codes.is_contiguous() and a_scale.is_contiguous() and
+            b_scale.is_contiguous()):
+        dev = a_codes.device
+        _check_tensor(a_codes, "a_codes", (T, H), dev, (u8,))
+        _check_tensor(b_codes, "b_codes", (N, H), dev, (u8,))
+        _check_tensor(a_scale, "a_scale", (T, HB), dev, (f32,))
+        _check_tensor(b_scale, "b_scale", (NB, HB), dev, (f32,))
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=a_codes.device)
+    else:
+        _check_tensor(out, "out", (T, N), a_codes.device)
+    c = _context_of(ctx, index)
+    return (c.handle, a_codes.data_ptr(), a_scale.data_ptr(), b_codes.data_ptr(),
+            b_scale.data_ptr(), T, N, H, out.data_ptr(), _raw_stream(stream, index)), out, c
+
+
+def prepare_fp8_matmul(a_codes, a_scale, b_codes, b_scale, out=None, ctx=None, stream=None):
+    """``fp8_matmul`` checked and marshalled once."""
+    args, out, c = _fp8_matmul_args(a_codes, a_scale, b_codes, b_scale, out, ctx, stream)
+    return PreparedCall(_load().farn_fp8_matmul, args, "farn_fp8_matmul", out,
+                        (a_codes, a_scale, b_codes, b_scale, c))
+
+
+def fp8_matmul(a_codes, a_scale, b_codes, b_scale, out=None, ctx=None, stream=None):
+    """The product of two E4M3 tensors with block scales, a [T,H] (scales
+    [T,ceil(H/128)]) and b [N,H] (scales [ceil(N/128),ceil(H/128)]), as
+    ``fp8_quantize`` gives them with block_rows 1 and 128, in bf16 [T,N]."""
+    args, out, _ = _fp8_matmul_args(a_codes, a_scale, b_codes, b_scale, out, ctx, stream)
+    _call(_load().farn_fp8_matmul, args, "farn_fp8_matmul")
+    return out
+
+
+def _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, ctx, stream):
+    torch = _torch or _load_torch()
+    u8, i32, f32 = torch.uint8, torch.int32, torch.float32
+    sx, sw, index = x.shape, weights.shape, x.get_device()
+    if len(sx) != 2 or len(sw) != 3:
+        raise ValueError("x must be [rows, H] and weights [E, N, H]")
+    n_rows, H = sx
+    E, N, HW = sw
+    HB, NB = -(-H // 128), -(-N // 128)
+    if not (HW == H and index >= 0 and weights.get_device() == index and
+            x_scale.get_device() == index and w_scale.get_device() == index and
+            offsets.get_device() == index and x.dtype is u8 and weights.dtype is u8 and
+            x_scale.dtype is f32 and w_scale.dtype is f32 and offsets.dtype is i32 and
+            x_scale.shape == (n_rows, HB) and w_scale.shape == (E, NB, HB) and
+            offsets.shape == (E + 1,) and x.is_contiguous() and weights.is_contiguous() and
+            x_scale.is_contiguous() and w_scale.is_contiguous() and offsets.is_contiguous()):
+        dev = x.device
+        _check_tensor(x, "x", (n_rows, H), dev, (u8,))
+        _check_tensor(x_scale, "x_scale", (n_rows, HB), dev, (f32,))
+        _check_tensor(weights, "weights", (E, N, H), dev, (u8,))
+        _check_tensor(w_scale, "w_scale", (E, NB, HB), dev, (f32,))
+        _check_tensor(offsets, "offsets", (E + 1,), dev, (i32,))
+    S = n_rows
+    if rows is not None:
+        sr = rows.shape
+        S = sr[0] if len(sr) == 1 else -1
+        if not (S >= 0 and rows.dtype is i32 and rows.get_device() == index and
+                rows.is_contiguous()):
+            _check_tensor(rows, "rows", (S,), x.device, (i32,))
+    if out is None:
+        out = torch.empty((S, N), dtype=torch.bfloat16, device=x.device)
+    else:
+        _check_tensor(out, "out", (S, N), x.device)
+    c = _context_of(ctx, index)
+    return (c.handle, x.data_ptr(), x_scale.data_ptr(), n_rows,
+            None if rows is None else rows.data_ptr(), S, weights.data_ptr(), w_scale.data_ptr(),
+            E, offsets.data_ptr(), N, H, out.data_ptr(), _raw_stream(stream, index)), out, c
+
+
+def prepare_fp8_grouped_matmul(x, x_scale, weights, w_scale, offsets, rows=None, out=None,
+                               ctx=None, stream=None):
+    """``fp8_grouped_matmul`` checked and marshalled once."""
+    args, out, c = _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, ctx,
+                                     stream)
+    return PreparedCall(_load().farn_fp8_grouped_matmul, args, "farn_fp8_grouped_matmul", out,
+                        (x, x_scale, weights, w_scale, offsets, rows, c))
+
+
+def fp8_grouped_matmul(x, x_scale, weights, w_scale, offsets, rows=None, out=None, ctx=None,
+                       stream=None):
+    """``grouped_matmul`` on E4M3 codes with block scales: x uint8 [n,H] with
+    x_scale fp32 [n,ceil(H/128)], weights uint8 [E,N,H] with w_scale fp32
+    [E,ceil(N/128),ceil(H/128)], as ``fp8_quantize`` gives them with block_rows
+    1 and 128.  Returns out bf16 [S,N]."""
+    args, out, _ = _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, ctx,
+                                     stream)
+    _call(_load().farn_fp8_grouped_matmul, args, "farn_fp8_grouped_matmul")
+    return out
+
+
+def kv_cache(n_pages: int, page_size: int, heads: int, head_dim: int, format: str = "fp8",
+             device="cuda"):
+    """The tensors of an empty paged cache of keys and values: (k_codes,
+    v_codes, k_scale, v_scale).  "fp8": codes uint8
+    [n_pages,page_size,heads,head_dim] and scales fp32
+    [n_pages,page_size,heads]; "nvfp4": codes uint8 [..,head_dim/2] and scales
+    uint8 [..,head_dim/16], as ``nvfp4_quantize`` gives them.  Zeros: every
+    slot reads as 0."""
+    torch = _torch or _load_torch()
+    base = (int(n_pages), int(page_size), int(heads))
+    D = int(head_dim)
+    if format == "fp8":
+        shapes, dt = ((*base, D), base), torch.float32
+    elif format == "nvfp4":
+        if D % 16:
+            raise ValueError(f"NVFP4 needs head_dim % 16 == 0, got {D}")
+        shapes, dt = ((*base, D // 2), (*base, D // 16)), torch.uint8
+    else:
+        raise ValueError(f'format must be "fp8" or "nvfp4", got {format!r}')
+    new = lambda s, d: torch.zeros(s, dtype=d, device=device)  # noqa: E731
+    return (new(shapes[0], torch.uint8), new(shapes[0], torch.uint8), new(shapes[1], dt),
+            new(shapes[1], dt))
+
+
+def _cache_args(cache, tensor_scales, index, dev):
+    """The C struct of a cache's four tensors."""
+    torch = _torch
+    kc, vc, ks, vs = cache
+    sc = kc.shape
+    if len(sc) != 4:
+        raise ValueError("the cache's codes must be [n_pages, page_size, heads, ..]")
+    fp8 = ks.dtype is torch.float32
+    D = sc[3] if fp8 else sc[3] * 2
+    if not fp8 and D % 16:
+        raise ValueError(f"NVFP4 needs head_dim % 16 == 0, got {D}")
+    scale_shape = sc[:3] if fp8 else (*sc[:3], D // 16)
+    scale_type = torch.float32 if fp8 else torch.uint8
+    if not (kc.dtype is torch.uint8 and vc.dtype is torch.uint8 and vc.shape == sc and
+            ks.dtype is scale_type and vs.dtype is scale_type and ks.shape == scale_shape and
+            vs.shape == scale_shape and kc.get_device() == index and vc.get_device() == index and
+            ks.get_device() == index and vs.get_device() == index and kc.is_contiguous() and
+            vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        for t, name, shape, dt in ((kc, "k_codes", sc, torch.uint8),
+                                   (vc, "v_codes", sc, torch.uint8),
+                                   (ks, "k_scale", scale_shape, scale_type),
+                                   (vs, "v_scale", scale_shape, scale_type)):
+            _check_tensor(t, "the cache's " + name, shape, dev, (dt,))
+    if fp8:
+        gk = gv = 1.0
+    elif tensor_scales is None:
+        raise ValueError("an NVFP4 cache needs tensor_scales (keys', values')")
+    else:
+        gk, gv = tensor_scales
+    return KvCache(FARN_CACHE_FP8 if fp8 else FARN_CACHE_NVFP4, sc[1], sc[0], sc[2], D,
+                   kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), gk, gv)
+
+
+def _heads_view(x, name, index, dev, T=None, D=None, heads=None):
+    """[T, heads, D] and the stride of its tokens: heads contiguous within a
+    token, tokens anywhere behind each other."""
+    sx = x.shape
+    if len(sx) != 3:
+        raise ValueError(f"{name} must be [T, heads, D]")
+    if x.get_device() != index or x.dtype is not _torch.bfloat16 or index < 0:
+        _check_tensor(x, name, sx, dev)       # what it turns down first
+    if (T is not None and sx[0] != T) or (D is not None and sx[2] != D) or \
+            (heads is not None and sx[1] != heads):
+        raise ValueError(f"{name} must be [{T}, {heads if heads is not None else 'heads'}, {D}], "
+                         f"got {tuple(sx)}")
+    st = x.stride()
+    if (sx[2] > 1 and st[2] != 1) or (sx[1] > 1 and st[1] != sx[2]):
+        raise ValueError(f"{name}'s heads must lie one after the other within a token")
+    return st[0] if sx[0] > 1 else sx[1] * sx[2]
+
+
+def _rope_args(positions, freqs, sections, T, D, index, dev):
+    torch = _torch
+    if freqs is None:
+        return None, 0, None, None, 0
+    sp = positions.shape
+    if len(sp) == 1:
+        sp = (1, *sp)
+    R = 2 * freqs.shape[0] if freqs.dim() == 1 else -1
+    if not (len(sp) == 2 and sp[1] == T and positions.dtype is torch.int32 and
+            freqs.dtype is torch.float32 and 0 < R <= D and positions.get_device() == index and
+            freqs.get_device() == index and positions.is_contiguous() and freqs.is_contiguous()):
+        if len(sp) != 2 or sp[1] != T:
+            raise ValueError(f"positions must be [T] or [axes, T] for T = {T}, got "
+                             f"{tuple(positions.shape)}")
+        if not 0 < R <= D:
+            raise ValueError(f"freqs must be [R / 2] for R in 2..{D}, got {tuple(freqs.shape)}")
+        _check_tensor(positions, "positions", positions.shape, dev, (torch.int32,))
+        _check_tensor(freqs, "freqs", (R // 2,), dev, (torch.float32,))
+    axes = sp[0]
+    if not 1 <= axes <= 4:
+        raise ValueError(f"positions must have 1..4 axes, got {axes}")
+    if sections is None:
+        if axes > 1:
+            raise ValueError("positions of several axes need sections")
+        sections = (R // 2,)
+    if len(sections) != axes or min(sections) < 0 or sum(sections) != R // 2:
+        raise ValueError(f"sections must be {axes} counts of pairs with the sum {R // 2}, got "
+                         f"{tuple(sections)}")
+    return positions, axes, (ctypes.c_int * axes)(*sections), freqs, R
+
+
+def _weight_arg(w, name, D, index, dev):
+    if w is None:
+        return None
+    if not (w.get_device() == index and w.dtype is _torch.bfloat16 and w.shape == (D,) and
+            w.is_contiguous()):
+        _check_tensor(w, name, (D,), dev)
+    return w.data_ptr()
+
+
+def _qk_args(q, k, q_weight, k_weight, eps, positions, freqs, sections, interleaved, out, ctx,
+             stream):
+    torch = _torch or _load_torch()
+    index, dev = q.get_device(), q.device
+    q_stride = _heads_view(q, "q", index, dev)
+    T, HQ, D = q.shape
+    k_stride = _heads_view(k, "k", index, dev, T, D)
+    HK = k.shape[1]
+    pos, axes, sect, fr, R = _rope_args(positions, freqs, sections, T, D, index, dev)
+    if out is None:
+        out = (torch.empty((T, HQ, D), dtype=torch.bfloat16, device=dev),
+               torch.empty((T, HK, D), dtype=torch.bfloat16, device=dev))
+        qs, ks = HQ * D, HK * D
+    else:
+        out = tuple(out)
+        if len(out) != 2:
+            raise ValueError("out must be (q, k)")
+        qs = _heads_view(out[0], "the output of q", index, dev, T, D, HQ)
+        ks = _heads_view(out[1], "the output of k", index, dev, T, D, HK)
+    c = _context_of(ctx, index)
+    return (c.handle, T, D, q.data_ptr(), HQ, q_stride, k.data_ptr(), HK, k_stride,
+            _weight_arg(q_weight, "q_weight", D, index, dev),
+            _weight_arg(k_weight, "k_weight", D, index, dev), eps,
+            None if pos is None else pos.data_ptr(), axes, sect,
+            None if fr is None else fr.data_ptr(), R, 1 if interleaved else 0,
+            out[0].data_ptr(), qs, out[1].data_ptr(), ks, _raw_stream(stream, index)), out, c
+
+
+def prepare_qk_norm_rope(q, k, q_weight, k_weight, eps: float, positions=None, freqs=None,
+                         sections=None, interleaved: bool = False, out=None, ctx=None,
+                         stream=None):
+    """``qk_norm_rope`` checked and marshalled once."""
+    args, out, c = _qk_args(q, k, q_weight, k_weight, eps, positions, freqs, sections,
+                            interleaved, out, ctx, stream)
+    return PreparedCall(_load().farn_qk_norm_rope, args, "farn_qk_norm_rope", out,
+                        (q, k, q_weight, k_weight, positions, freqs, c))
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, eps: float, positions=None, freqs=None, sections=None,
+                 interleaved: bool = False, out=None, ctx=None, stream=None):
+    """RMSNorm of every query and key head and its rotation by position, in one
+    pass: q bf16 [T,HQ,D], k bf16 [T,HK,D] (heads contiguous within a token;
+    tokens may lie further apart, as in a projection's output), weights bf16
+    [D] (None: no norm), positions int32 [T] or [axes,T], freqs fp32 [R/2]
+    (radians per position; None: no rotation), sections the number of pairs
+    that turn by each axis.  Pairs are (j, j + R/2), or neighbours with
+    `interleaved`.  out may be (q, k) themselves.  Returns (q, k)."""
+    args, out, _ = _qk_args(q, k, q_weight, k_weight, eps, positions, freqs, sections,
+                            interleaved, out, ctx, stream)
+    _call(_load().farn_qk_norm_rope, args, "farn_qk_norm_rope")
+    return out
+
+
+def _qk_cache_args(q, k, v, q_weight, k_weight, eps, positions, freqs, cache, slots,
+                   tensor_scales, sections, interleaved, out, ctx, stream):
+    torch = _torch or _load_torch()
+    index, dev = q.get_device(), q.device
+    q_stride = _heads_view(q, "q", index, dev)
+    T, HQ, D = q.shape
+    k_stride = _heads_view(k, "k", index, dev, T, D)
+    HK = k.shape[1]
+    v_stride = _heads_view(v, "v", index, dev, T, D, HK)
+    pos, axes, sect, fr, R = _rope_args(positions, freqs, sections, T, D, index, dev)
+    if not (slots.get_device() == index and slots.dtype is torch.int32 and
+            slots.shape == (T,) and slots.is_contiguous()):
+        _check_tensor(slots, "slots", (T,), dev, (torch.int32,))
+    store = _cache_args(cache, tensor_scales, index, dev)
+    if store.heads != HK or store.head_dim != D:
+        raise ValueError(f"the cache has {store.heads} heads of {store.head_dim}, k has {HK} of "
+                         f"{D}")
+    if out is None:
+        out = torch.empty((T, HQ, D), dtype=torch.bfloat16, device=dev)
+        qs = HQ * D
+    else:
+        qs = _heads_view(out, "the output of q", index, dev, T, D, HQ)
+    c = _context_of(ctx, index)
+    return (c.handle, T, D, q.data_ptr(), HQ, q_stride, k.data_ptr(), k_stride, v.data_ptr(),
+            v_stride, HK, _weight_arg(q_weight, "q_weight", D, index, dev),
+            _weight_arg(k_weight, "k_weight", D, index, dev), eps,
+            None if pos is None else pos.data_ptr(), axes, sect,
+            None if fr is None else fr.data_ptr(), R, 1 if interleaved else 0, out.data_ptr(), qs,
+            store, slots.data_ptr(), _raw_stream(stream, index)), out, c
+
+
+def prepare_qk_norm_rope_cache(q, k, v, q_weight, k_weight, eps: float, positions, freqs, cache,
+                               slots, tensor_scales=None, sections=None,
+                               interleaved: bool = False, out=None, ctx=None, stream=None):
+    """``qk_norm_rope_cache`` checked and marshalled once."""
+    args, out, c = _qk_cache_args(q, k, v, q_weight, k_weight, eps, positions, freqs, cache,
+                                  slots, tensor_scales, sections, interleaved, out, ctx, stream)
+    return PreparedCall(_load().farn_qk_norm_rope_cache, args, "farn_qk_norm_rope_cache", out,
+                        (q, k, v, q_weight, k_weight, positions, freqs, cache, slots, c))
+
+
+def qk_norm_rope_cache(q, k, v, q_weight, k_weight, eps: float, positions, freqs, cache, slots,
+                       tensor_scales=None, sections=None, interleaved: bool = False, out=None,
+                       ctx=None, stream=None):
+    """``qk_norm_rope`` with keys and values going into a cache (the four
+    tensors of ``kv_cache``): token t's keys, normed and rotated, and its values
+    v bf16 [T,HK,D], as they are, to slot slots[t] (int32 [T]; one outside the
+    cache is skipped, and no two may be the same).  tensor_scales: the keys' and
+    the values' of an NVFP4 cache.  Returns q."""
+    args, out, _ = _qk_cache_args(q, k, v, q_weight, k_weight, eps, positions, freqs, cache,
+                                  slots, tensor_scales, sections, interleaved, out, ctx, stream)
+    _call(_load().farn_qk_norm_rope_cache, args, "farn_qk_norm_rope_cache")
+    return out
+
+
+def _kv_write_args(k, v, cache, slots, tensor_scales, ctx, stream):
+    torch = _torch or _load_torch()
+    index, dev = k.get_device(), k.device
+    k_stride = _heads_view(k, "k", index, dev)
+    T, HK, D = k.shape
+    v_stride = _heads_view(v, "v", index, dev, T, D, HK)
+    if not (slots.get_device() == index and slots.dtype is torch.int32 and
+            slots.shape == (T,) and slots.is_contiguous()):
+        _check_tensor(slots, "slots", (T,), dev, (torch.int32,))
+    store = _cache_args(cache, tensor_scales, index, dev)
+    if store.heads != HK or store.head_dim != D:
+        raise ValueError(f"the cache has {store.heads} heads of {store.head_dim}, k has {HK} of "
+                         f"{D}")
+    c = _context_of(ctx, index)
+    return (c.handle, T, k.data_ptr(), k_stride, v.data_ptr(), v_stride, store, slots.data_ptr(),
+            _raw_stream(stream, index)), c
+
+
+def prepare_kv_write(k, v, cache, slots, tensor_scales=None, ctx=None, stream=None):
+    """``kv_write`` checked and marshalled once; the call returns the cache."""
+    args, c = _kv_write_args(k, v, cache, slots, tensor_scales, ctx, stream)
+    return PreparedCall(_load().farn_kv_write, args, "farn_kv_write", cache, (k, v, slots, c))
+
+
+def kv_write(k, v, cache, slots, tensor_scales=None, ctx=None, stream=None):
+    """Keys and values, bf16 [T,heads,head_dim], quantised into slots[t] of a
+    cache as they are; slots and tensor_scales as for ``qk_norm_rope_cache``.
+    Returns the cache."""
+    args, _ = _kv_write_args(k, v, cache, slots, tensor_scales, ctx, stream)
+    _call(_load().farn_kv_write, args, "farn_kv_write")
+    return cache
+
+
+def _kv_read_args(cache, table, offsets, n_tokens, tensor_scales, out, ctx, stream):
+    torch = _torch or _load_torch()
+    i32 = torch.int32
+    index, dev = cache[0].get_device(), cache[0].device
+    if index < 0:
+        _check_tensor(cache[0], "the cache's k_codes", cache[0].shape, dev, (torch.uint8,))
+    store = _cache_args(cache, tensor_scales, index, dev)
+    if table.dim() != 2:
+        raise ValueError("table must be [B, width]")
+    B, width = table.shape
+    n = int(n_tokens)
+    if n < 0:
+        raise ValueError(f"n_tokens must not be negative, got {n}")
+    if not (table.get_device() == index and offsets.get_device() == index and
+            table.dtype is i32 and offsets.dtype is i32 and offsets.shape == (B + 1,) and
+            table.is_contiguous() and offsets.is_contiguous()):
+        _check_tensor(table, "table", (B, width), dev, (i32,))
+        _check_tensor(offsets, "offsets", (B + 1,), dev, (i32,))
+    shape = (n, store.heads, store.head_dim)
+    if out is None:
+        out = (torch.empty(shape, dtype=torch.bfloat16, device=dev),
+               torch.empty(shape, dtype=torch.bfloat16, device=dev))
+    else:
+        out = tuple(out)
+        if len(out) != 2:
+            raise ValueError("out must be (k, v)")
+        _check_tensor(out[0], "the output of k", shape, dev)
+        _check_tensor(out[1], "the output of v", shape, dev)
+    c = _context_of(ctx, index)
+    return (c.handle, store, table.data_ptr(), B, width, offsets.data_ptr(), n,
+            out[0].data_ptr(), out[1].data_ptr(), _raw_stream(stream, index)), out, c
+
+
+def prepare_kv_read(cache, table, offsets, n_tokens: int, tensor_scales=None, out=None, ctx=None,
+                    stream=None):
+    """``kv_read`` checked and marshalled once."""
+    args, out, c = _kv_read_args(cache, table, offsets, n_tokens, tensor_scales, out, ctx, stream)
+    return PreparedCall(_load().farn_kv_read, args, "farn_kv_read", out,
+                        (cache, table, offsets, c))
+
+
+def kv_read(cache, table, offsets, n_tokens: int, tensor_scales=None, out=None, ctx=None,
+            stream=None):
+    """The contexts of B sequences back from a cache, in bf16, one after the
+    other: table int32 [B,width] holds each sequence's pages, offsets int32
+    [B+1] its first output token.  Returns (k, v), bf16
+    [n_tokens,heads,head_dim]; a page outside the cache reads as zeros, and
+    tokens that no sequence has are left as they were."""
+    args, out, _ = _kv_read_args(cache, table, offsets, n_tokens, tensor_scales, out, ctx, stream)
+    _call(_load().farn_kv_read, args, "farn_kv_read")
     return out

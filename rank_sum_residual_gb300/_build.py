@@ -14,10 +14,11 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libfarn.so")
 SOURCES = [os.path.join(CSRC, f) for f in
-           ("farn.cu", "farn_route.cu", "farn_nvfp4.cu", "farn_product.cu")]
+           ("farn.cu", "farn_route.cu", "farn_nvfp4.cu", "farn_product.cu", "farn_fp8.cu",
+            "farn_fp8_product.cu", "farn_heads.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in
                      ("farn_kernels.cuh", "farn_internal.h", "farn_product.cuh", "farn_product_tc.cuh",
-                      "farn_tcgen05.cuh")] + \
+                      "farn_tcgen05.cuh", "farn_fp8.cuh", "farn_fp8_product.cuh")] + \
     [os.path.join(INCLUDE, "farn.h")]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -48,6 +48,7 @@ struct farn_ctx {
   int route_ok;        // the router's kernels are set up
   void* encode_tiled;  // the driver's tensor-map encoder; null: the products' tensor-core
                        // kernels are not set up, and the plain one takes every call
+  int fp8_ok;          // the FP8 products' tensor-core kernels are set up (with encode_tiled)
   int max_clusters[3]; // clusters of 1, 2 and 4 of their CTAs that fit the device at a time
 };
 
@@ -57,6 +58,7 @@ namespace farn_host {
 // router, or the products' tensor-core kernels, cannot be had.
 bool route_setup(const farn_ctx* ctx);
 bool product_setup(farn_ctx* ctx);
+bool fp8_product_setup(const farn_ctx* ctx);
 
 inline bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
   if (na <= 0 || nb <= 0) return false;

@@ -218,7 +218,7 @@ __device__ __forceinline__ void turn_scales(unsigned char* block, int lane) {
 
 // 16 bytes at `at`, a multiple of 16, of which those outside [lo, hi) are not
 // read.
-__device__ __noinline__ uint4 load_within(uintptr_t at, uintptr_t lo, uintptr_t hi) {
+static __device__ __noinline__ uint4 load_within(uintptr_t at, uintptr_t lo, uintptr_t hi) {
   if (at >= lo && at + 16 <= hi) return __ldg(reinterpret_cast<const uint4*>(at));
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -303,17 +303,15 @@ __device__ __forceinline__ void put_scale_rows(unsigned char* block, const uint4
 // warp turns it over in shared memory, two slots to a word, and writes runs
 // of eight weights if rows are so aligned (about 110 instructions for 1024 values; one warp per
 // scheduler issues one in 4 to 5 cycles, so their number is the time).
-// n: slots; live: those whose row exists; first: the warp's first weight.
+// v[j]: slot j's product with the lane's weight; n: slots; live: those whose
+// row exists; first: the warp's first weight; store_bytes: 16, 8 or 2, what N
+// and out allow a store of a row to be.
 template <bool GATHER>
-__device__ __forceinline__ void store_turned(const TcParams& t, uint32_t tmem, uint32_t* turn,
-                                             int64_t slot, int n, uint32_t live, int64_t first,
-                                             int lane) {
-  const ProductParams& p = t.p;
-  uint32_t v[32];
-  tc::tmem_ld32(tmem, v);
-  tc::tmem_ld_wait();
+__device__ __forceinline__ void store_columns(const ProductParams& p, int store_bytes,
+                                              const uint32_t* v, uint32_t* turn, int64_t slot,
+                                              int n, uint32_t live, int64_t first, int lane) {
   const float alpha = p.alpha;
-  if (t.store_bytes == 2) {
+  if (store_bytes == 2) {
     // Rows that start anywhere: straight from the registers, a store being one
     // slot's run of the warp's 32 weights (in runs of eight, element by
     // element, such an N took twice the time; turned and in words 16 % more).
@@ -351,7 +349,7 @@ __device__ __forceinline__ void store_turned(const TcParams& t, uint32_t tmem, u
       if (s >= n || col >= p.N) continue;
       if (GATHER && !((live >> s) & 1u)) w[i] = make_uint4(0u, 0u, 0u, 0u);
       uint16_t* o = static_cast<uint16_t*>(p.out) + (slot + s) * p.N + col;
-      if (t.store_bytes == 16) {
+      if (store_bytes == 16) {
         *reinterpret_cast<uint4*>(o) = w[i];
       } else {
         *reinterpret_cast<uint2*>(o) = make_uint2(w[i].x, w[i].y);
@@ -360,6 +358,15 @@ __device__ __forceinline__ void store_turned(const TcParams& t, uint32_t tmem, u
     }
   }
   __syncwarp();
+}
+template <bool GATHER>
+__device__ __forceinline__ void store_turned(const TcParams& t, uint32_t tmem, uint32_t* turn,
+                                             int64_t slot, int n, uint32_t live, int64_t first,
+                                             int lane) {
+  uint32_t v[32];
+  tc::tmem_ld32(tmem, v);
+  tc::tmem_ld_wait();
+  store_columns<GATHER>(t.p, t.store_bytes, v, turn, slot, n, live, first, lane);
 }
 
 template <bool FP4, int CG, int BN, bool GATHER, bool COPY>
