@@ -487,13 +487,25 @@ int farn_fp8_matmul(const farn_ctx *ctx, const void *a_codes,
 /* farn_fp8_grouped_matmul - farn_grouped_matmul on E4M3 codes with block
  * scales: x [n_rows, H] with x_scale [n_rows, ceil(H/128)], weights [E, N, H]
  * with w_scale [E, ceil(N/128), ceil(H/128)].  Slots, rows, offsets, out and
- * errors as there; arithmetic as in farn_fp8_matmul. */
+ * errors as there; arithmetic as in farn_fp8_matmul.
+ *   workspace  NULL, or workspace_bytes of device memory (16-byte aligned) that
+ *              the call may overwrite, for this call alone until it has run: a
+ *              long call with `rows` lays the slots' rows side by side there
+ *              first and is then faster.  farn_fp8_grouped_workspace says how
+ *              much such a call takes; less, or none, leads to the same results
+ *              by the other kernel.  It may not overlap any tensor. */
 int farn_fp8_grouped_matmul(const farn_ctx *ctx, const void *x,
                             const float *x_scale, int64_t n_rows,
                             const int32_t *rows, int64_t n_slots,
                             const void *weights, const float *w_scale, int E,
                             const int32_t *offsets, int64_t N, int64_t H,
-                            void *out, cudaStream_t stream);
+                            void *out, void *workspace, int64_t workspace_bytes,
+                            cudaStream_t stream);
+
+/* The workspace that a farn_fp8_grouped_matmul call with `rows` and these sizes
+ * uses: *bytes, 0 if none.  Returns FARN_OK or FARN_ERR_INVALID_ARG. */
+int farn_fp8_grouped_workspace(const farn_ctx *ctx, int64_t n_slots, int E,
+                               int64_t N, int64_t H, int64_t *bytes);
 
 /* farn_qk_norm_rope - RMSNorm of every query and key head and its rotation by
  * position, in one pass.  For a head's elements x[0..D):

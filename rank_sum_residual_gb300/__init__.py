@@ -35,7 +35,7 @@ __all__ = [
     "farn_nvfp4_matmul", "nvfp4_matmul",
     "farn_plan_grouped_matmul", "farn_plan_nvfp4_matmul",
     "farn_fp8_quantize", "fp8_quantize", "farn_fp8_matmul", "fp8_matmul",
-    "farn_fp8_grouped_matmul", "fp8_grouped_matmul",
+    "farn_fp8_grouped_matmul", "fp8_grouped_matmul", "farn_fp8_grouped_workspace",
     "FARN_CACHE_FP8", "FARN_CACHE_NVFP4", "KvCache", "kv_cache",
     "farn_qk_norm_rope", "qk_norm_rope", "farn_qk_norm_rope_cache", "qk_norm_rope_cache",
     "farn_kv_write", "kv_write", "farn_kv_read", "kv_read",
@@ -127,7 +127,9 @@ def _load():
         lib.farn_fp8_matmul.argtypes = [vp, cvp, cvp, cvp, cvp, i64, i64, i64, vp, vp]
         lib.farn_fp8_matmul.restype = i32
         lib.farn_fp8_grouped_matmul.argtypes = [vp, cvp, cvp, i64, cvp, i64, cvp, cvp, i32, cvp,
-                                                i64, i64, vp, vp]
+                                                i64, i64, vp, vp, i64, vp]
+        lib.farn_fp8_grouped_workspace.argtypes = [vp, i64, i32, i64, i64, ctypes.POINTER(i64)]
+        lib.farn_fp8_grouped_workspace.restype = i32
         lib.farn_fp8_grouped_matmul.restype = i32
         pc, pi = ctypes.POINTER(KvCache), ctypes.POINTER(i32)
         rope = [cvp, cvp, f32, cvp, i32, pi, cvp, i32, i32]
@@ -312,13 +314,23 @@ def farn_fp8_matmul(ctx, a_codes, a_scale, b_codes, b_scale, T, N, H, out, strea
 
 
 def farn_fp8_grouped_matmul(ctx, x, x_scale, n_rows, rows, n_slots, weights, w_scale, E, offsets,
-                            N, H, out, stream=0) -> int:
+                            N, H, out, workspace=0, workspace_bytes=0, stream=0) -> int:
     """C ``farn_fp8_grouped_matmul`` on raw device addresses (ints); rows 0 for
     slot s reading row s."""
     return _load().farn_fp8_grouped_matmul(
         _addr(ctx), _addr(x), _addr(x_scale), int(n_rows), _addr(rows), int(n_slots),
         _addr(weights), _addr(w_scale), int(E), _addr(offsets), int(N), int(H), _addr(out),
-        _addr(stream))
+        _addr(workspace), int(workspace_bytes), _addr(stream))
+
+
+def farn_fp8_grouped_workspace(ctx, n_slots, E, N, H) -> int:
+    """C ``farn_fp8_grouped_workspace``: the bytes that a call with rows uses."""
+    n = ctypes.c_int64()
+    st = _load().farn_fp8_grouped_workspace(_addr(ctx), int(n_slots), int(E), int(N), int(H),
+                                            ctypes.byref(n))
+    if st != FARN_OK:
+        raise FarnError(st, "farn_fp8_grouped_workspace")
+    return n.value
 
 
 def _int_array(v):
@@ -1092,7 +1104,7 @@ def fp8_matmul(a_codes, a_scale, b_codes, b_scale, out=None, ctx=None, stream=No
     return out
 
 
-def _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, ctx, stream):
+def _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, workspace, ctx, stream):
     torch = _torch or _load_torch()
     u8, i32, f32 = torch.uint8, torch.int32, torch.float32
     sx, sw, index = x.shape, weights.shape, x.get_device()
@@ -1126,28 +1138,42 @@ def _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, ctx, str
     else:
         _check_tensor(out, "out", (S, N), x.device)
     c = _context_of(ctx, index)
+    if workspace is not None:
+        _check_tensor(workspace, "workspace", workspace.shape, x.device, (u8,))
+    elif rows is not None and S > 64:       # shorter calls never lay rows side by side
+        n = farn_fp8_grouped_workspace(c.handle, S, E, N, H)
+        if n:
+            workspace = torch.empty(n, dtype=u8, device=x.device)
+            if stream is not None:          # its memory is not given away before the call has run
+                workspace.record_stream(stream)
     return (c.handle, x.data_ptr(), x_scale.data_ptr(), n_rows,
             None if rows is None else rows.data_ptr(), S, weights.data_ptr(), w_scale.data_ptr(),
-            E, offsets.data_ptr(), N, H, out.data_ptr(), _raw_stream(stream, index)), out, c
+            E, offsets.data_ptr(), N, H, out.data_ptr(),
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel(),
+            _raw_stream(stream, index)), out, (c, workspace)
 
 
 def prepare_fp8_grouped_matmul(x, x_scale, weights, w_scale, offsets, rows=None, out=None,
-                               ctx=None, stream=None):
-    """``fp8_grouped_matmul`` checked and marshalled once."""
-    args, out, c = _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, ctx,
-                                     stream)
+                               workspace=None, ctx=None, stream=None):
+    """``fp8_grouped_matmul`` checked and marshalled once; the call keeps its
+    workspace."""
+    args, out, c = _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, workspace,
+                                     ctx, stream)
     return PreparedCall(_load().farn_fp8_grouped_matmul, args, "farn_fp8_grouped_matmul", out,
                         (x, x_scale, weights, w_scale, offsets, rows, c))
 
 
-def fp8_grouped_matmul(x, x_scale, weights, w_scale, offsets, rows=None, out=None, ctx=None,
-                       stream=None):
+def fp8_grouped_matmul(x, x_scale, weights, w_scale, offsets, rows=None, out=None,
+                       workspace=None, ctx=None, stream=None):
     """``grouped_matmul`` on E4M3 codes with block scales: x uint8 [n,H] with
     x_scale fp32 [n,ceil(H/128)], weights uint8 [E,N,H] with w_scale fp32
     [E,ceil(N/128),ceil(H/128)], as ``fp8_quantize`` gives them with block_rows
-    1 and 128.  Returns out bf16 [S,N]."""
-    args, out, _ = _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, ctx,
-                                     stream)
+    1 and 128.  A long call with rows lays them side by side in a workspace
+    (uint8; ``farn_fp8_grouped_workspace`` bytes), which is taken from torch if
+    none is given.  Returns out bf16 [S,N]."""
+    args, out, _ = _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, workspace,
+                                     ctx, stream)
     _call(_load().farn_fp8_grouped_matmul, args, "farn_fp8_grouped_matmul")
     return out
 

@@ -26,20 +26,20 @@ typedef void (*Kernel)(const Fp8Params, const CUtensorMap, const CUtensorMap);
 
 struct Kind {
   bool gather;
-  int cg, bn;
+  int cg, bn, warps, regs;
   Kernel kernel;
-  int stage_bytes, scale_bytes;
+  int stage_bytes, scale_bytes, part_bytes;
 };
 
-template <int CG, int BN, bool GATHER>
-Kind kind() {
-  using Sh = farn::Fp8Shape<CG, BN, GATHER>;
-  return Kind{GATHER, CG, BN, &farn::farn_fp8_product_kernel<CG, BN, GATHER>, Sh::kStageBytes,
-              farn::kF8ScaleSlots * Sh::kScaleSlot};
+template <typename Sh>
+Kind kind(bool gather, Kernel kernel) {
+  return Kind{gather, Sh::kCg, Sh::kBn, Sh::kWarps, Sh::kRegs, kernel, Sh::kStageBytes,
+              Sh::kScaleBytes, Sh::kPartBytes};
 }
 
-const Kind kKinds[] = {kind<1, 64, false>(), kind<1, 64, true>(), kind<2, 256, false>(),
-                       kind<2, 256, true>()};
+const Kind kKinds[] = {kind<farn::Fp8One<false>>(false, farn::farn_fp8_one_kernel<false>),
+                       kind<farn::Fp8One<true>>(true, farn::farn_fp8_one_kernel<true>),
+                       kind<farn::Fp8Pair>(false, farn::farn_fp8_pair_kernel)};
 
 const Kind* find_kind(int cg, bool gather) {
   for (const Kind& k : kKinds)
@@ -65,14 +65,13 @@ int log2_of(int v) { return v >= 4 ? 2 : v >= 2 ? 1 : 0; }
 // the parts that the CTAs of a split row exchange (or where the adding warps
 // turn their sums over); then 1 KB to align the ring.
 bool fit(const farn_ctx* ctx, const Kind* k, int E, int ks, Plan* pl) {
-  const uint32_t part = ks > 1 ? (uint32_t)k->bn * farn::kPartPitch * 4
-                               : farn::kF8Adders * (uint32_t)farn::kTurnBytes;
+  const uint32_t part = ks > 1 ? (uint32_t)k->bn * farn::kPartPitch * 4 : (uint32_t)k->part_bytes;
   const uint32_t barriers = ((uint32_t)sizeof(farn::Fp8Barriers) + 15u) / 16 * 16;
   const uint32_t groups = (farn::groups_bytes(E) + 15u) / 16 * 16;
   const uint32_t fixed = 1024 + k->scale_bytes + barriers + groups + part;
   int stages = (ctx->max_smem - (int)fixed) / k->stage_bytes;
   if (stages > farn::kTcMaxStages) stages = farn::kTcMaxStages;
-  if (stages < 2 || (k->gather && stages < farn::kF8Gather)) return false;
+  if (stages < 2 || (k->gather && stages <= farn::kF8Gather)) return false;
   pl->kind = k;
   pl->ks = ks;
   pl->stages = stages;
@@ -87,7 +86,8 @@ bool fit(const farn_ctx* ctx, const Kind* k, int E, int ks, Plan* pl) {
 // The kernel for a call of S slots in E groups: whichever of a pair of CTAs per
 // tile and one CTA, splitting the row or not, has fewer stages one after the
 // other, as for the other products (plan_tc).
-bool plan_tc(const farn_ctx* ctx, const ProductParams& p, Plan* pl) {
+// can_copy: gathered rows can be laid side by side first, as the pair needs them.
+bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool can_copy, Plan* pl) {
   const bool gather = p.rows != nullptr;
   const int64_t groups = p.E < p.S ? p.E : p.S;
   const int64_t chunks = (p.H + farn::kTcRowBytes - 1) / farn::kTcRowBytes;
@@ -96,7 +96,7 @@ bool plan_tc(const farn_ctx* ctx, const ProductParams& p, Plan* pl) {
     return slots * ((p.N + weights - 1) / weights);
   };
   const Kind* one = find_kind(1, gather);
-  const Kind* pair = find_kind(2, gather);
+  const Kind* pair = find_kind(2, false);
   const int64_t tiles1 = tiles_of(one->bn, farn::kTcWeights);
   const int64_t tiles2 = tiles_of(pair->bn, 2 * farn::kTcWeights);
   if (tiles1 > kMaxTiles || tiles2 > kMaxTiles) return false;
@@ -116,9 +116,10 @@ bool plan_tc(const farn_ctx* ctx, const ProductParams& p, Plan* pl) {
   // every CTA has a part of the row, and the device has room for the cluster
   while (ks > 1 && (ks > chunks || ctx->max_clusters[log2_of(ks)] < 1)) ks /= 2;
   const double cost1 = cost_of_split(ks);
-  const double cost2 = stages_of(tiles2, ctx->max_clusters[1], (double)chunks);
+  const double cost2 = 1.44 * stages_of(tiles2, ctx->max_clusters[1], (double)chunks);
   bool use_pair = cost2 < cost1 || (cost2 == cost1 && p.S > 32 * groups);
   if (ctx->tc_tile) use_pair = ctx->tc_tile == 256;
+  if (gather && !can_copy) use_pair = false;
   if (use_pair) ks = 1;
   // the parts of a split row take room from the ring: none, if it is short
   const Kind* k = use_pair ? pair : one;
@@ -191,10 +192,13 @@ int launch_kernel(const farn_ctx* ctx, void (*kernel)(A...), unsigned grid, unsi
   return FARN_OK;
 }
 
-int launch(const farn_ctx* ctx, Fp8Params t, cudaStream_t stream) {
-  const ProductParams& p = t.p;
+// Where the rows of a gathering call are laid side by side: codes, then scales.
+int64_t copied_codes(int64_t S, int64_t H) { return (S * H + 15) / 16 * 16; }
+
+int launch(const farn_ctx* ctx, Fp8Params t, void* workspace, cudaStream_t stream) {
+  ProductParams& p = t.p;
   Plan pl;
-  const bool tc = tc_takes(ctx, p) && plan_tc(ctx, p, &pl);
+  const bool tc = tc_takes(ctx, p) && plan_tc(ctx, p, workspace != nullptr, &pl);
   const int64_t tiles = plain_tiles(p);
   if (!tc && tiles > kMaxTiles) return FARN_ERR_UNSUPPORTED;
   DeviceGuard dg(ctx->device);
@@ -205,21 +209,38 @@ int launch(const farn_ctx* ctx, Fp8Params t, cudaStream_t stream) {
                          (unsigned)(tiles < most ? tiles : most), farn::kPlainThreads, 0, 1,
                          stream, t);
   }
+  const bool copy = p.rows && pl.kind->cg == 2;
+  farn::Fp8GatherParams g;
+  if (copy) {
+    g = {static_cast<const uint8_t*>(p.a), t.a_scale, p.rows, static_cast<uint8_t*>(workspace),
+         reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + copied_codes(p.S, p.H)),
+         p.n_a, p.S, p.H, t.HB};
+    t.n_rows = p.n_a;
+    p.a = g.to;
+    t.a_scale = g.to_scale;
+    p.n_a = p.S;
+  }
   t.stages = pl.stages;
   t.ks = pl.ks;
   const uint64_t at = (uint64_t)(uintptr_t)p.out | (uint64_t)p.N * 2;   // of every row
   t.store_bytes = at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : 2;
-  t.scale_vec = t.HB % 4 == 0 && aligned16(t.a_scale);
+  t.scale_vec = t.HB % 4 == 0 && aligned16(t.a_scale) && aligned16(t.b_scale);
   t.scales_at = pl.scales_at;
   t.barriers_at = pl.barriers_at;
   t.groups_at = pl.groups_at;
   t.part_at = pl.part_at;
   const Kind* k = pl.kind;
   CUtensorMap map_w, map_x;
-  if (!encode(ctx, &map_w, p.b, p.H, p.N, p.E, farn::kTcWeights)) return FARN_ERR_CUDA;
+  if (!encode(ctx, &map_w, p.b, p.H, p.N, p.E, 64)) return FARN_ERR_CUDA;
   map_x = map_w;                    // not read, unless
   if (!k->gather && !encode(ctx, &map_x, p.a, p.H, p.n_a, 0, farn::kF8Box)) return FARN_ERR_CUDA;
-  return launch_kernel(ctx, k->kernel, pl.grid, farn::kF8Warps * 32u, pl.smem,
+  if (copy) {
+    constexpr int64_t per = farn::kF8CopyThreads / 32;
+    const int st = launch_kernel(ctx, farn::fp8_gather_kernel, (unsigned)((p.S + per - 1) / per),
+                                 farn::kF8CopyThreads, 0, 1, stream, g);
+    if (st != FARN_OK) return st;
+  }
+  return launch_kernel(ctx, k->kernel, pl.grid, k->warps * 32u, pl.smem,
                        k->cg == 2 ? 2u : (unsigned)pl.ks, stream, t, map_w, map_x);
 }
 
@@ -242,7 +263,7 @@ bool fp8_product_setup(const farn_ctx* ctx) {
   for (const Kind& k : kKinds) {
     cudaFuncAttributes attr;
     if (cudaFuncGetAttributes(&attr, (const void*)k.kernel) != cudaSuccess ||
-        (k.cg == 2 && attr.numRegs < farn::kF8Regs) ||
+        attr.numRegs < k.regs ||
         cudaFuncSetAttribute((const void*)k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ctx->max_smem) != cudaSuccess)
       return false;
@@ -284,15 +305,37 @@ int farn_fp8_matmul(const farn_ctx* ctx, const void* a_codes, const float* a_sca
   t.b_scale = b_scale;
   t.HB = HB;
   t.NB = NB;
-  return launch(ctx, t, stream);
+  return launch(ctx, t, nullptr, stream);
+}
+
+int farn_fp8_grouped_workspace(const farn_ctx* ctx, int64_t n_slots, int E, int64_t N, int64_t H,
+                               int64_t* bytes) {
+  if (!ctx || !bytes || !sizes_ok(n_slots, N, H) || E < 1 || E > FARN_MAX_EXPERTS)
+    return FARN_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (n_slots == 0 || H % 16 != 0 || !ctx->fp8_ok || ctx->force_variant == kVariantGeneric)
+    return FARN_OK;
+  // what plan_tc goes by: sizes, and that the rows are gathered
+  static const int32_t some_rows = 0;
+  ProductParams p;
+  memset(&p, 0, sizeof p);
+  p.rows = &some_rows;
+  p.S = n_slots;
+  p.N = N;
+  p.H = H;
+  p.E = E;
+  Plan pl;
+  if (plan_tc(ctx, p, true, &pl) && pl.kind->cg == 2)
+    *bytes = copied_codes(n_slots, H) + n_slots * blocks_of(H) * 4;
+  return FARN_OK;
 }
 
 int farn_fp8_grouped_matmul(const farn_ctx* ctx, const void* x, const float* x_scale,
                             int64_t n_rows, const int32_t* rows, int64_t n_slots,
                             const void* weights, const float* w_scale, int E,
                             const int32_t* offsets, int64_t N, int64_t H, void* out,
-                            cudaStream_t stream) {
-  if (!ctx || n_rows < 0 || n_rows > 0x7FFFFFFF || !sizes_ok(n_slots, N, H) || E < 1 ||
+                            void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
+  if (!ctx || workspace_bytes < 0 || n_rows < 0 || n_rows > 0x7FFFFFFF || !sizes_ok(n_slots, N, H) || E < 1 ||
       E > FARN_MAX_EXPERTS || !product_fits(n_rows, 2 * H) || !product_fits(2 * N * H, E) ||
       (!rows && n_rows != n_slots))
     return FARN_ERR_INVALID_ARG;
@@ -307,6 +350,17 @@ int farn_fp8_grouped_matmul(const farn_ctx* ctx, const void* x, const float* x_s
       overlaps(out, ob, weights, N * H * E) || overlaps(out, ob, w_scale, NB * HB * E * 4) ||
       overlaps(out, ob, rows, rows ? n_slots * 4 : 0) ||
       overlaps(out, ob, offsets, (int64_t)(E + 1) * 4))
+    return FARN_ERR_ALIAS;
+  // the workspace: used if it is given, large enough and aligned
+  const int64_t need = copied_codes(n_slots, H) + n_slots * HB * 4;
+  if (!rows || !workspace || !aligned16(workspace) || workspace_bytes < need) workspace = nullptr;
+  if (workspace &&
+      (overlaps(workspace, need, out, ob) || overlaps(workspace, need, x, n_rows * H) ||
+       overlaps(workspace, need, x_scale, n_rows * HB * 4) ||
+       overlaps(workspace, need, weights, N * H * E) ||
+       overlaps(workspace, need, w_scale, NB * HB * E * 4) ||
+       overlaps(workspace, need, rows, n_slots * 4) ||
+       overlaps(workspace, need, offsets, (int64_t)(E + 1) * 4)))
     return FARN_ERR_ALIAS;
   if (ctx->fault_launch) return FARN_ERR_CUDA;
   Fp8Params t;
@@ -328,7 +382,7 @@ int farn_fp8_grouped_matmul(const farn_ctx* ctx, const void* x, const float* x_s
   t.b_scale = w_scale;
   t.HB = HB;
   t.NB = NB;
-  return launch(ctx, t, stream);
+  return launch(ctx, t, workspace, stream);
 }
 
 }  // extern "C"
