@@ -83,9 +83,16 @@ bool fit(const farn_ctx* ctx, const Kind* k, int E, int ks, Plan* pl) {
   return true;
 }
 
-// The kernel for a call of S slots in E groups: whichever of a pair of CTAs per
-// tile and one CTA, splitting the row or not, has fewer stages one after the
-// other, as for the other products (plan_tc).
+// The kernel for a call of S slots in E groups: whichever of one CTA per tile,
+// splitting the row or not, and a pair of CTAs has less to do one after the other,
+// counted in the one CTA's stages of 0.26 us.  A pair's takes 0.42 us; joining a
+// split row 2 us with few slots and twice that with a full tile.  With several
+// groups the number of tiles is an estimate, so the last round of CTAs counts
+// half.  Measured (us: one CTA, row split by 2, by 4, pair): 1 x 8192 x 8192 20.3,
+// 18.4, 19.3, 29.2; 64 x 8192 x 8192 22.3, 19.3, 22.5, 30.0; 100 x 8192 x 8192 23.4,
+// 28.7, 35.2, 30.1; 128 x 10240 x 5120 27.4, 30.7, 35.8, 22.9; 400 x 8192 x 2048
+// 19.9, 35.9, 57.9, 14.2; 700 x 1000 x 8192 22.2, 27.3, 26.5, 29.7; 64 experts of 64
+// slots 2048 -> 4096 114, 235, 392, 126, of 250 4096 -> 2048 353, 517, 757, 183.
 // can_copy: gathered rows can be laid side by side first, as the pair needs them.
 bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool can_copy, Plan* pl) {
   const bool gather = p.rows != nullptr;
@@ -105,19 +112,21 @@ bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool can_copy, Plan* p
     if (rounds <= 1.0) return per_tile;
     return (p.E == 1 ? ceil(rounds) : rounds + 0.5) * per_tile;
   };
+  const double fill = (double)p.S / (double)(groups * one->bn);
+  const double join = 7.5 * (1.0 + (fill < 1.0 ? fill : 1.0));
   auto cost_of_split = [&](int ks) {
     return stages_of(tiles1 * ks, ctx->num_sms,
-                     (double)((chunks + ks - 1) / ks) + (ks > 1 ? 1.5 : 0.0));
+                     (double)((chunks + ks - 1) / ks) + (ks > 1 ? join : 0.0));
   };
   int ks = 1;
-  for (int k = 2; k <= farn::kTcMaxSplit && chunks >= k * 2; k *= 2)
+  for (int k = 2; k <= farn::kTcMaxSplit && chunks >= k; k *= 2)
     if (ctx->max_clusters[log2_of(k)] >= 1 && cost_of_split(k) < cost_of_split(ks)) ks = k;
   if (ctx->tc_split) ks = ctx->tc_split;
   // every CTA has a part of the row, and the device has room for the cluster
   while (ks > 1 && (ks > chunks || ctx->max_clusters[log2_of(ks)] < 1)) ks /= 2;
   const double cost1 = cost_of_split(ks);
-  const double cost2 = 1.44 * stages_of(tiles2, ctx->max_clusters[1], (double)chunks);
-  bool use_pair = cost2 < cost1 || (cost2 == cost1 && p.S > 32 * groups);
+  const double cost2 = 1.65 * stages_of(tiles2, ctx->max_clusters[1], (double)chunks);
+  bool use_pair = cost2 < cost1;
   if (ctx->tc_tile) use_pair = ctx->tc_tile == 256;
   if (gather && !can_copy) use_pair = false;
   if (use_pair) ks = 1;

@@ -7,7 +7,7 @@
 // (one stage of the ring); the outer sum is fp32 multiply-adds in registers,
 // because the matrix instructions know scales of blocks of 32 with powers of
 // two only.  Each block's sums are handed to eight adding warps through tensor
-// memory, which holds two blocks' sums.
+// memory, which holds the sums of two blocks (`one`: four).
 //
 //   pair    a pair of CTAs per tile of 256 slots by 256 weights: long calls.
 //           The slots are the matrix instruction's M side, so a lane has one
@@ -98,7 +98,8 @@ struct Fp8One {
   static constexpr int kStageBytes = kABytes + kBn * kTcRowBytes;
   static constexpr int kScaleSlot = kF8ScaleBlocks * kBn * 4;
   static constexpr int kScaleBytes = kF8ScaleSlots * kScaleSlot;
-  static constexpr int kCols = 2 * kBn;                   // of tensor memory: two blocks' sums
+  static constexpr int kBufs = 4;                         // blocks' sums in tensor memory
+  static constexpr int kCols = kBufs * kBn;
   static constexpr int kPartBytes = kF8Adders * kTurnBytes;
 };
 
@@ -638,7 +639,7 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
       mbar_init(m.full + 8 * lane, GATHER ? 2 : 1);         // TMA; gathered rows
       mbar_init(m.empty + 8 * lane, 1);
     }
-    if (lane < 4) {
+    if (lane < Sh::kBufs) {
       mbar_init(m.afull + 8 * lane, 1);
       mbar_init(m.aempty + 8 * lane, kF8Adders);
     }
@@ -686,7 +687,8 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
     float* part = reinterpret_cast<float*>(smem + t.part_at);
     const uint32_t part_full = tc::smem_addr(&m.bb->part_full);
     const uint32_t part_empty = tc::smem_addr(&m.bb->part_empty);
-    uint32_t nb = 0, ng = 0, nt = 0;       // blocks, groups of scales, tiles so far
+    uint32_t ng = 0, nt = 0;               // groups of scales, tiles so far
+    uint32_t buf = 0, phase = 0;           // the next block's sums
     bool ok = true;
     for (int32_t tile = t0; ok && tile < tiles; tile += tstep, ++nt) {
       const Tile w = find_tile(g, p.E, tile, wts, Sh::kBn);
@@ -694,45 +696,45 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
       float acc[Sh::kWarpCols];
 #pragma unroll
       for (int i = 0; i < Sh::kWarpCols; ++i) acc[i] = 0.0f;
+      uint32_t asked = f8_ask(m.afull + 8 * buf, phase);
       for (int c = 0; ok && c < nc; ++ng) {
         const uint32_t slot = ng % kF8ScaleSlots;
-        ok = f8_wait(m.sfull + 8 * slot, ng / kF8ScaleSlots & 1, abort_flag, p.err,
-                                 kErrTcFull);
+        ok = f8_wait(m.sfull + 8 * slot, ng / kF8ScaleSlots & 1, abort_flag, p.err, kErrTcFull);
         if (!ok) break;
         const int end = min(nc, c + kF8ScaleBlocks);
         const float* s = scales + slot * (Sh::kScaleSlot / 4);
-        for (; c < end; ++c, ++nb, s += Sh::kBn) {
-          const uint32_t b = nb & 1;
-          ok = f8_wait(m.afull + 8 * b, (nb >> 1) & 1, abort_flag, p.err, kErrTcTile);
+        for (; c < end; ++c, s += Sh::kBn) {
+          ok = f8_answer(asked, m.afull + 8 * buf, phase, abort_flag, p.err, kErrTcTile);
           if (!ok) break;
           tc::fence_after();
-          const uint32_t d = sums + b * Sh::kBn;
+          const uint32_t d = sums + buf * Sh::kBn, bar = m.aempty + 8 * buf;
+          uint32_t v[2][16];
+#pragma unroll
+          for (int q = 0; q < Sh::kWarpCols / 16; ++q)
+            if (q * 16 < mine) tc::tmem_ld16(d + q * 16, v[q]);
+          if (++buf == Sh::kBufs) { buf = 0; phase ^= 1; }
+          if (c + 1 < nc) asked = f8_ask(m.afull + 8 * buf, phase);
+          tc::tmem_ld_wait();
+          tc::fence_before();       // orders the reads of tensor memory before the arrival
+          __syncwarp();
+          arrive_local(bar, lane);
 #pragma unroll
           for (int q = 0; q < Sh::kWarpCols / 16; ++q) {
             if (q * 16 < mine) {
-              uint32_t v[16];
-              tc::tmem_ld16(d + q * 16, v);
-              float4 sv[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                sv[j] = *reinterpret_cast<const float4*>(s + q * 16 + j * 4);
-              tc::tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
+                const float4 sv = *reinterpret_cast<const float4*>(s + q * 16 + j * 4);
                 float* to = acc + q * 16 + j * 4;
-                to[0] = fmaf(__uint_as_float(v[4 * j]), sv[j].x, to[0]);
-                to[1] = fmaf(__uint_as_float(v[4 * j + 1]), sv[j].y, to[1]);
-                to[2] = fmaf(__uint_as_float(v[4 * j + 2]), sv[j].z, to[2]);
-                to[3] = fmaf(__uint_as_float(v[4 * j + 3]), sv[j].w, to[3]);
+                to[0] = fmaf(__uint_as_float(v[q][4 * j]), sv.x, to[0]);
+                to[1] = fmaf(__uint_as_float(v[q][4 * j + 1]), sv.y, to[1]);
+                to[2] = fmaf(__uint_as_float(v[q][4 * j + 2]), sv.z, to[2]);
+                to[3] = fmaf(__uint_as_float(v[q][4 * j + 3]), sv.w, to[3]);
               }
             }
           }
-          tc::fence_before();       // orders the reads of tensor memory before the arrival
-          __syncwarp();
-          if (lane == 0) mbar_arrive(m.aempty + 8 * b);
         }
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(m.sempty + 8 * slot);
+        if (ok) arrive_local(m.sempty + 8 * slot, lane);
       }
       if (!ok) break;
       const int64_t n0 = (int64_t)w.wt * Sh::kTileWeights;
@@ -827,27 +829,28 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
   } else if (warp == 9) {
     // ------------------------------------------------- matrix instructions
     RingPos at;
-    uint32_t nb = 0;                       // blocks so far
+    uint32_t buf = 0, phase = 0;           // the next block's sums
     bool ok = true;
     const uint64_t desc0 = tc::operand_desc(m.base);
     for (int32_t tile = t0; ok && tile < tiles; tile += tstep) {
       const Tile w = find_tile(g, p.E, tile, wts, Sh::kBn);
       const uint32_t idesc = tc::idesc_e4m3(kTcWeights, filled(w));
-      for (int c = 0; c < nc; ++c, ++nb, at.next(NS)) {
-        const uint32_t s = at.stage, b = nb & 1;
+      for (int c = 0; c < nc; ++c, at.next(NS)) {
+        const uint32_t s = at.stage;
+        const uint32_t free = f8_ask(m.aempty + 8 * buf, phase ^ 1);
         ok = f8_wait(m.full + 8 * s, at.phase, abort_flag, p.err, kErrTcFull) &&
-             f8_wait(m.aempty + 8 * b, ((nb >> 1) & 1) ^ 1, abort_flag, p.err,
-                                 kErrTcTile);
+             f8_answer(free, m.aempty + 8 * buf, phase ^ 1, abort_flag, p.err, kErrTcTile);
         if (!ok) break;
         tc::fence_after();
         const uint64_t da = desc0 + (s * Sh::kStageBytes >> 4), db = da + (Sh::kABytes >> 4);
         if (tc::elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc::mma_fp8<1>(tmem + b * Sh::kBn, da + 2 * k, db + 2 * k, idesc, k > 0 ? 1u : 0u);
-          tc::commit<1>(m.afull + 8 * b);
+            tc::mma_fp8<1>(tmem + buf * Sh::kBn, da + 2 * k, db + 2 * k, idesc, k > 0 ? 1u : 0u);
+          tc::commit<1>(m.afull + 8 * buf);
           tc::commit<1>(m.empty + 8 * s);
         }
+        if (++buf == Sh::kBufs) { buf = 0; phase ^= 1; }
       }
     }
     __syncwarp();
