@@ -530,8 +530,8 @@ int farn_fp8_grouped_workspace(const farn_ctx *ctx, int64_t n_slots, int E,
  *   q_out, k_out  bf16, with strides of their own; each may be exactly its input
  *               (same address and stride), and rows of equal strides may lie
  *               between each other's
- * Fast: D and the strides multiples of 8, D <= 256, pointers 16-byte aligned, and
- * R a multiple of 16 unless interleaved; else a slower kernel.  Returns
+ * Fast: D a multiple of 8 up to 256, strides multiples of 4, pointers 8-byte
+ * aligned, and R a multiple of 8 unless interleaved; else a slower kernel.  Returns
  * FARN_ERR_INVALID_ARG, FARN_ERR_ALIAS or FARN_ERR_CUDA. */
 int farn_qk_norm_rope(const farn_ctx *ctx, int64_t T, int D, const void *q,
                       int q_heads, int64_t q_stride, const void *k, int k_heads,

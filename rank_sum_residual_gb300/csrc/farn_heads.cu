@@ -8,9 +8,9 @@
 //                                             positions[axis of the pair] * freq
 //
 // in fp32, one rounding at the end.  A row is a token's head: 8 elements per
-// lane on 8, 16 or 32 lanes (D <= 64, 128, 256), so the sum of squares, the
-// partner of a pair and a row's amax are shuffles within the row's lanes.  A
-// warp keeps one token's angles in registers for all the heads it takes.
+// lane on 8, 16 or 32 lanes (D <= 64, 128, 256), so the sum of squares and a row's
+// amax are shuffles within the row's lanes.  A warp keeps one token's angles in
+// registers for all the heads it takes.
 // Memory bound for long calls, one launch and two dependent loads for short
 // ones.
 //
@@ -37,6 +37,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 4;             // rows per lane group whose loads are in flight
+constexpr int kCtas = 8;              // per SM
 constexpr int kMaxDim = 1024;
 constexpr int kMaxAxes = 4;
 
@@ -87,155 +88,234 @@ __device__ __forceinline__ void sincos_at(int32_t pos, uint64_t step, float* s, 
   const int32_t top = (int32_t)(uint32_t)(((uint64_t)(int64_t)pos * step) >> 32);
   sincospif((float)top * 4.656612873077393e-10f, s, c);        // 2^-31 half turns
 }
-__device__ __forceinline__ int32_t position_of(const HeadsParams& p, int64_t t, int pair) {
+__device__ __forceinline__ int axis_of(const HeadsParams& p, int pair) {
   int a = 0;
 #pragma unroll
   for (int i = 0; i < kMaxAxes - 1; ++i) a += pair >= p.axis_end[i];
-  return p.positions[a * p.T + t];
+  return a;
+}
+
+// Where a lane's 8 elements of a row lie: two runs of four, elements [a, a + 4) and
+// [b, b + 4).
+//
+// Contiguous (b = a + 4): unrotated rows, and pairs of neighbours.  Halved: a lane
+// of the first R / 8 has the first and the second elements of four pairs, so that
+// a pair never leaves its lane and its angle is computed once; the others have
+// what follows the rotated part.  (With 8 neighbouring elements per lane a pair's
+// partner was 8 shuffles away: 8192 tokens of 40 and 8 heads of 128 took 96 us.)
+struct Runs {
+  int a, b;
+};
+__device__ __forceinline__ Runs contiguous(int l) { return Runs{l * 8, l * 8 + 4}; }
+__device__ __forceinline__ Runs halved(int l, int R) {
+  return l < R / 8 ? Runs{l * 4, R / 2 + l * 4} : contiguous(l);
 }
 
 // A row of the cache from a lane's 8 values; every lane of the warp calls it.
-// row: slot * heads + head.  live: the row and the lane's elements exist.
+// row: slot * heads + head.  live: the row and the lane's elements exist.  half:
+// the lane's runs lie in two halves of the row (NVFP4: all of the row's lanes' do,
+// and a block of 16 elements is a run of four lanes).
 template <int FMT, int L>
-__device__ __forceinline__ void store_cache8(const Cache& c, int which, int64_t row, int D, int l,
-                                             const float* x, bool live) {
-  float m = farn::amax8(x);
+__device__ __forceinline__ void store_cache8(const Cache& c, int which, int64_t row, int D,
+                                             const Runs& r, int l, bool half, const float* x,
+                                             bool live) {
   if constexpr (FMT == FARN_CACHE_FP8) {
+    float m = farn::amax8(x);
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     const farn::Fp8Scale s = farn::fp8_scale(m);
     if (!live) return;
-    *reinterpret_cast<uint2*>(c.codes[which] + row * D + l * 8) = farn::fp8_codes8(x, s.inv);
+    const uint2 w = farn::fp8_codes8(x, s.inv);
+    uint8_t* to = c.codes[which] + row * D;
+    *reinterpret_cast<uint32_t*>(to + r.a) = w.x;
+    *reinterpret_cast<uint32_t*>(to + r.b) = w.y;
     if (l == 0) static_cast<float*>(c.scale[which])[row] = s.scale;
   } else {
     // as nvfp4_vec, from fp32 values
-    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    const uint32_t s = farn::pack_e4m3x2((m / 6.0f) * c.g[which], 0.0f) & 0xFFu;
-    const float sv = farn::e4m3_to_f32(s), inv = c.g[which] / sv;
-    uint32_t w = 0u;
+    float m[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w |= farn::pack_e2m1x2(fminf(x[2 * e] * inv, 6.0f), fminf(x[2 * e + 1] * inv, 6.0f))
-           << (8 * e);
-    if (!live) return;
-    *reinterpret_cast<uint32_t*>(c.codes[which] + row * (D / 2) + l * 4) = sv > 0.0f ? w : 0u;
-    if ((l & 1) == 0)
-      static_cast<uint8_t*>(c.scale[which])[row * (D / 16) + (l >> 1)] = (uint8_t)s;
+    for (int i = 0; i < 2; ++i) {
+      m[i] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m[i] = fmaxf(m[i], fabsf(x[4 * i + e]));
+    }
+    if (half) {
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], o));
+    } else {
+      m[0] = fmaxf(m[0], m[1]);
+      m[0] = m[1] = fmaxf(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], 1));
+    }
+    uint8_t* to = c.codes[which] + row * (D / 2);
+    uint8_t* scale = static_cast<uint8_t*>(c.scale[which]) + row * (D / 16);
+    const float g = c.g[which];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t s = farn::pack_e4m3x2((m[i] / 6.0f) * g, 0.0f) & 0xFFu;
+      const float sv = farn::e4m3_to_f32(s), inv = g / sv;
+      uint32_t w = 0u;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        w |= farn::pack_e2m1x2(fminf(x[4 * i + 2 * e] * inv, 6.0f),
+                               fminf(x[4 * i + 2 * e + 1] * inv, 6.0f))
+             << (8 * e);
+      if (!live) continue;
+      const int at = i ? r.b : r.a;
+      *reinterpret_cast<uint16_t*>(to + at / 2) = (uint16_t)(sv > 0.0f ? w : 0u);
+      if (half ? (l & 3) == 0 : (l & 1) == 0 && i == 0) scale[at / 16] = (uint8_t)s;
+    }
   }
 }
 
-// FMT: the cache's format, or 0: keys go to out[1].
-template <int L, int FMT>
-__global__ void __launch_bounds__(kThreads)
+// What a lane keeps for all the rows of one role (0 queries, 1 keys, 2 values)
+// that its warp takes.
+struct Turn {
+  float c[4], s[4];
+  int pairs;                          // how many of its four turn
+};
+
+// The passes [lo, hi) of a role and token: kRows rows each, one per L lanes.
+// FMT: the cache's format, or 0: keys go to out[1].  HALF: pairs lie in halves.
+// The code is about instructions: with roles, layouts and addresses worked out
+// per row 8192 tokens of 40 and 8 heads of 128 took 77 us, 260 instructions to a
+// pass, two thirds of the issue slots.
+template <int ROLE, int L, int FMT, bool HALF>
+__device__ __forceinline__ void run_role(const HeadsParams& p, int64_t t, int lo, int hi, int l,
+                                         int sub, const uint2* weight, const Turn& turn,
+                                         int64_t slot, float inv_d) {
+  constexpr int kRows = 32 / L;
+  constexpr bool kTurned = ROLE < 2, kCached = FMT != 0 && ROLE > 0;
+  if (lo >= hi || (kCached && slot < 0)) return;
+  const int heads = p.heads[ROLE], D = p.D;
+  const Runs r = HALF && kTurned ? halved(l, p.R) : contiguous(l);
+  const int head0 = lo * kRows + sub;
+  // lanes without elements read and write nothing
+  const int end = l * 8 < D ? min(heads, hi * kRows) : 0;
+  const int step = kRows * D;
+  const uint16_t* in = p.in[ROLE] + t * p.in_stride[ROLE] + (int64_t)head0 * D;
+  uint16_t* out = nullptr;
+  if (!kCached) out = p.out[ROLE < 2 ? ROLE : 0] + t * p.out_stride[ROLE < 2 ? ROLE : 0] +
+                      (int64_t)head0 * D;
+  const bool norm = kTurned && p.weight[ROLE < 2 ? ROLE : 0] != nullptr;
+  float w[8];
+  if (kTurned) farn::unpack8(make_uint4(weight[0].x, weight[0].y, weight[1].x, weight[1].y), w);
+  for (int n = lo, head = head0; n < hi; n += kAhead) {
+    uint2 raw[kAhead][2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
+      if (head + i * kRows < end) {
+        raw[i][0] = *reinterpret_cast<const uint2*>(in + i * step + r.a);
+        raw[i][1] = *reinterpret_cast<const uint2*>(in + i * step + r.b);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (n + i >= hi) break;
+      float x[8];
+      farn::unpack8(make_uint4(raw[i][0].x, raw[i][0].y, raw[i][1].x, raw[i][1].y), x);
+      if (norm) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        const float rstd = rsqrtf(fmaf(ss, inv_d, p.eps));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (x[e] * rstd) * w[e];
+      }
+      if (kTurned) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float& a = x[HALF ? e : 2 * e];
+          float& b = x[HALF ? e + 4 : 2 * e + 1];
+          if (e < turn.pairs) {
+            const float ya = a * turn.c[e] - b * turn.s[e];
+            b = b * turn.c[e] + a * turn.s[e];
+            a = ya;
+          }
+        }
+      }
+      const int h = head + i * kRows;
+      if constexpr (!kCached) {
+        if (h < end) {
+          const uint4 v = farn::pack8(x);
+          *reinterpret_cast<uint2*>(out + i * step + r.a) = make_uint2(v.x, v.y);
+          *reinterpret_cast<uint2*>(out + i * step + r.b) = make_uint2(v.z, v.w);
+        }
+      } else {
+        store_cache8<FMT, L>(p.cache, ROLE - 1, slot * heads + h, D, r, l, HALF && kTurned, x,
+                             h < end);
+      }
+    }
+    head += kAhead * kRows;
+    in += kAhead * step;
+    if (!kCached) out += kAhead * step;
+  }
+}
+
+template <int L, int FMT, bool HALF>
+__global__ void __launch_bounds__(kThreads, kCtas)
 heads_kernel(const __grid_constant__ HeadsParams p) {
   constexpr int kRows = 32 / L;                       // rows of a pass
   farn::pdl_wait();
   farn::pdl_trigger();
   const int lane = threadIdx.x & 31, l = lane % L, sub = lane / L;
-  const int passes_of[3] = {(p.heads[0] + kRows - 1) / kRows, (p.heads[1] + kRows - 1) / kRows,
-                            (p.heads[2] + kRows - 1) / kRows};
-  const int turned = passes_of[0] + passes_of[1], passes = turned + passes_of[2];
+  const int passes_q = (p.heads[0] + kRows - 1) / kRows;
+  const int passes_k = (p.heads[1] + kRows - 1) / kRows;
+  const int passes_v = (p.heads[2] + kRows - 1) / kRows;
+  const int turned = passes_q + passes_k, passes = turned + passes_v;
   const int per = (passes + p.groups - 1) / p.groups;
-  const bool mine = l * 8 < p.D;
-  const int half = p.R >> 1;
-  // this lane's first pair, and how many of its elements turn
-  const bool second = !p.interleaved && l * 8 >= half;
-  const int pair0 = p.interleaved ? l * 4 : second ? l * 8 - half : l * 8;
-  const int turn = min(max(p.R - l * 8, 0), 8);
-  const int partner = p.interleaved || turn == 0 ? lane : second ? lane - half / 8
-                                                                 : lane + half / 8;
-  uint64_t step[8];
+  // this lane's pairs: the four from 4 l on, or fewer
+  const int pair0 = l * 4;
+  Turn turn;
+  turn.pairs = min(max(p.R / 2 - pair0, 0), 4);
+  const Runs r = HALF ? halved(l, p.R) : contiguous(l);
+  uint64_t step[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const bool have = p.interleaved ? 2 * i < turn : i < turn;
-    step[i] = have && !(p.interleaved && i >= 4) ? turn_step(p.freqs[pair0 + i]) : 0ull;
+  for (int i = 0; i < 4; ++i) step[i] = i < turn.pairs ? turn_step(p.freqs[pair0 + i]) : 0ull;
+  uint2 weight[2][2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const bool have = l * 8 < p.D && p.heads[w] && p.weight[w];
+    weight[w][0] = have ? __ldg(reinterpret_cast<const uint2*>(p.weight[w] + r.a))
+                        : make_uint2(0u, 0u);
+    weight[w][1] = have ? __ldg(reinterpret_cast<const uint2*>(p.weight[w] + r.b))
+                        : make_uint2(0u, 0u);
   }
+  const float inv_d = 1.0f / (float)p.D;
   const int64_t tasks = p.T * p.groups;
   for (int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); task < tasks;
        task += (int64_t)gridDim.x * kWarps) {
-    const int64_t t = task / p.groups;
+    const int64_t t = p.groups == 1 ? task : task / p.groups;
     const int first = (int)(task - t * p.groups) * per, end = min(first + per, passes);
     int64_t slot = 0;
     if (FMT != 0) {
       slot = p.slots[t];
       if (slot >= p.cache.slots) slot = -1;
     }
-    float cs[8], sn[8];
-    bool have_angles = false;
-    for (int p0 = first; p0 < end; p0 += kAhead) {
-      uint4 raw[kAhead];
+    if (first < turned && p.R > 0) {
+      const int a0 = axis_of(p, pair0);
+      const int32_t at0 = turn.pairs > 0 ? p.positions[a0 * p.T + t] : 0;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int pass = p0 + i;
-        const int role = pass < passes_of[0] ? 0 : pass < turned ? 1 : 2;
-        const int head = (pass - (role == 0 ? 0 : role == 1 ? passes_of[0] : turned)) * kRows + sub;
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (pass < end && mine && head < p.heads[role] && (FMT == 0 || role == 0 || slot >= 0))
-          raw[i] = *reinterpret_cast<const uint4*>(p.in[role] + t * p.in_stride[role] +
-                                                   (int64_t)head * p.D + l * 8);
-      }
-      if (!have_angles && p0 < turned) {
-        have_angles = true;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          cs[i] = 1.0f;
-          sn[i] = 0.0f;
-          const bool have = p.interleaved ? 2 * i < turn : i < turn;
-          if (have && !(p.interleaved && i >= 4))
-            sincos_at(position_of(p, t, pair0 + i), step[i], &sn[i], &cs[i]);
-          if (!p.interleaved && !second) sn[i] = -sn[i];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int pass = p0 + i;
-        if (pass >= end) break;
-        const int role = pass < passes_of[0] ? 0 : pass < turned ? 1 : 2;
-        const int head = (pass - (role == 0 ? 0 : role == 1 ? passes_of[0] : turned)) * kRows + sub;
-        const bool live = mine && head < p.heads[role];
-        float x[8];
-        farn::unpack8(raw[i], x);
-        if (role < 2) {
-          if (p.weight[role]) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-            for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-            const float rstd = 1.0f / sqrtf(ss / (float)p.D + p.eps);
-            uint4 wv = make_uint4(0u, 0u, 0u, 0u);
-            if (mine) wv = __ldg(reinterpret_cast<const uint4*>(p.weight[role]) + l);
-            float w[8];
-            farn::unpack8(wv, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = (x[e] * rstd) * w[e];
-          }
-          if (p.interleaved) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (2 * e < turn) {
-                const float a = x[2 * e], b = x[2 * e + 1];
-                x[2 * e] = a * cs[e] - b * sn[e];
-                x[2 * e + 1] = b * cs[e] + a * sn[e];
-              }
-          } else if (half > 0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float o = __shfl_sync(0xFFFFFFFFu, x[e], partner);
-              if (turn) x[e] = x[e] * cs[e] + o * sn[e];
-            }
-          }
-        }
-        if (role == 0 || (FMT == 0 && role == 1)) {
-          if (live)
-            *reinterpret_cast<uint4*>(p.out[role] + t * p.out_stride[role] +
-                                      (int64_t)head * p.D + l * 8) = farn::pack8(x);
-        } else if (FMT != 0) {
-          store_cache8<FMT, L>(p.cache, role - 1, slot * p.heads[1] + head, p.D, l, x,
-                               live && slot >= 0);
+      for (int i = 0; i < 4; ++i) {
+        turn.c[i] = 1.0f;
+        turn.s[i] = 0.0f;
+        if (i < turn.pairs) {
+          const int a = axis_of(p, pair0 + i);
+          sincos_at(a == a0 ? at0 : p.positions[a * p.T + t], step[i], &turn.s[i], &turn.c[i]);
         }
       }
     }
+    run_role<0, L, FMT, HALF>(p, t, first, min(end, passes_q), l, sub, weight[0], turn, slot,
+                              inv_d);
+    run_role<1, L, FMT, HALF>(p, t, max(first - passes_q, 0), min(end, turned) - passes_q, l, sub,
+                              weight[1], turn, slot, inv_d);
+    if (FMT != 0)
+      run_role<2, L, FMT, HALF>(p, t, max(first - turned, 0), end - turned, l, sub, nullptr, turn,
+                                slot, inv_d);
   }
 }
 
@@ -276,7 +356,7 @@ heads_plain_kernel(const __grid_constant__ HeadsParams p) {
       __syncwarp();
       for (int i = lane; i < half; i += 32) {
         float s, c;
-        sincos_at(position_of(p, t, i), turn_step(p.freqs[i]), &s, &c);
+        sincos_at(p.positions[axis_of(p, i) * p.T + t], turn_step(p.freqs[i]), &s, &c);
         const int ia = p.interleaved ? 2 * i : i, ib = p.interleaved ? 2 * i + 1 : i + half;
         const float a = x[ia], b = x[ib];
         x[ia] = a * c - b * s;
@@ -546,28 +626,40 @@ void set_cache(Cache* to, const farn_kv_cache* c) {
   to->slots = slots_of(c);
 }
 
-bool cache_aligned(const farn_kv_cache* c) {
-  const uintptr_t need = c->format == FARN_CACHE_FP8 ? 7u : 3u;
+// for reading, 8 elements at a time, or (write) four
+bool cache_aligned(const farn_kv_cache* c, bool write) {
+  const uintptr_t need = (c->format == FARN_CACHE_FP8 ? 8u : 4u) / (write ? 2u : 1u) - 1u;
   return (((uintptr_t)c->k_codes | (uintptr_t)c->v_codes) & need) == 0;
 }
 
 typedef void (*HeadsKernel)(const HeadsParams);
 
-template <int FMT>
+template <int FMT, bool HALF>
 HeadsKernel vector_kernel(int D) {
-  return D <= 64 ? heads_kernel<8, FMT> : D <= 128 ? heads_kernel<16, FMT> : heads_kernel<32, FMT>;
+  return D <= 64 ? heads_kernel<8, FMT, HALF>
+                 : D <= 128 ? heads_kernel<16, FMT, HALF> : heads_kernel<32, FMT, HALF>;
+}
+template <int FMT>
+HeadsKernel vector_kernel(int D, bool half) {
+  return half ? vector_kernel<FMT, true>(D) : vector_kernel<FMT, false>(D);
 }
 
 int launch_heads(const farn_ctx* ctx, HeadsParams& p, int fmt, bool cache_vec,
                  cudaStream_t stream) {
+  // Two runs of four elements per lane; in halves, the lanes of the rotated part
+  // have nothing else, and for NVFP4 they are all there is, four to a block.
+  const bool half = !p.interleaved && p.R > 0;
   bool vec = ctx->force_variant != kVariantGeneric && p.D % 8 == 0 && p.D <= 256 && cache_vec &&
-             (p.interleaved || p.R % 16 == 0);
+             (!half || p.R % 8 == 0) &&
+             !(half && fmt == FARN_CACHE_NVFP4 && (p.R != p.D || p.D % 32 != 0));
+  auto aligned8 = [](const void* at, int64_t stride) {
+    return ((uintptr_t)at & 7u) == 0 && stride % 4 == 0;
+  };
   for (int i = 0; i < 3 && vec; ++i)
-    if (p.heads[i] && (!aligned16(p.in[i]) || p.in_stride[i] % 8 != 0)) vec = false;
+    if (p.heads[i] && !aligned8(p.in[i], p.in_stride[i])) vec = false;
   for (int i = 0; i < 2 && vec; ++i) {
-    if (p.heads[i] && p.weight[i] && !aligned16(p.weight[i])) vec = false;
-    if (p.heads[i] && (i == 0 || fmt == 0) && (!aligned16(p.out[i]) || p.out_stride[i] % 8 != 0))
-      vec = false;
+    if (p.heads[i] && p.weight[i] && !aligned8(p.weight[i], 0)) vec = false;
+    if (p.heads[i] && (i == 0 || fmt == 0) && !aligned8(p.out[i], p.out_stride[i])) vec = false;
   }
   HeadsKernel k;
   int64_t tasks;
@@ -581,9 +673,9 @@ int launch_heads(const farn_ctx* ctx, HeadsParams& p, int fmt, bool cache_vec,
     int64_t groups = (want + p.T - 1) / p.T;
     p.groups = (int)(groups < 1 ? 1 : groups > passes ? passes : groups);
     tasks = p.T * p.groups;
-    k = fmt == 0 ? vector_kernel<0>(p.D)
-                 : fmt == FARN_CACHE_FP8 ? vector_kernel<FARN_CACHE_FP8>(p.D)
-                                         : vector_kernel<FARN_CACHE_NVFP4>(p.D);
+    k = fmt == 0 ? vector_kernel<0>(p.D, half)
+                 : fmt == FARN_CACHE_FP8 ? vector_kernel<FARN_CACHE_FP8>(p.D, half)
+                                         : vector_kernel<FARN_CACHE_NVFP4>(p.D, half);
   } else {
     p.groups = 1;
     tasks = p.T * ((int64_t)p.heads[0] + p.heads[1] + p.heads[2]);
@@ -697,7 +789,7 @@ int run_heads(const farn_ctx* ctx, int64_t T, int D, const void* const in[3], co
   p.freqs = freqs;
   p.T = T;
   p.slots = slots;
-  return launch_heads(ctx, p, cache ? cache->format : 0, !cache || cache_aligned(cache), stream);
+  return launch_heads(ctx, p, cache ? cache->format : 0, !cache || cache_aligned(cache, true), stream);
 }
 
 }  // namespace
@@ -791,7 +883,7 @@ int farn_kv_read(const farn_ctx* ctx, const farn_kv_cache* cache, const int32_t*
   p.out[0] = static_cast<uint16_t*>(k_out);
   p.out[1] = static_cast<uint16_t*>(v_out);
   const bool vec = ctx->force_variant != kVariantGeneric && cache->head_dim % 8 == 0 &&
-                   cache_aligned(cache) && aligned16(k_out) && aligned16(v_out);
+                   cache_aligned(cache, false) && aligned16(k_out) && aligned16(v_out);
   const int64_t grid = (n_tokens + kReadTokens - 1) / kReadTokens;
   const bool fp8 = cache->format == FARN_CACHE_FP8;
   return launch(ctx,
