@@ -1054,7 +1054,7 @@ def fp8_quantize(x, block_rows: int = 1, out=None, ctx=None, stream=None):
     scales fp32 [..,ceil(T/block_rows),ceil(H/128)]): the operands of
     ``fp8_matmul`` and ``fp8_grouped_matmul``."""
     args, out, _ = _fp8_quantize_args(x, block_rows, out, ctx, stream)
-    _call(_load().farn_fp8_quantize, args, "farn_fp8_quantize")
+    _call((_lib or _load()).farn_fp8_quantize, args, "farn_fp8_quantize")
     return out
 
 
@@ -1100,7 +1100,7 @@ def fp8_matmul(a_codes, a_scale, b_codes, b_scale, out=None, ctx=None, stream=No
     [T,ceil(H/128)]) and b [N,H] (scales [ceil(N/128),ceil(H/128)]), as
     ``fp8_quantize`` gives them with block_rows 1 and 128, in bf16 [T,N]."""
     args, out, _ = _fp8_matmul_args(a_codes, a_scale, b_codes, b_scale, out, ctx, stream)
-    _call(_load().farn_fp8_matmul, args, "farn_fp8_matmul")
+    _call((_lib or _load()).farn_fp8_matmul, args, "farn_fp8_matmul")
     return out
 
 
@@ -1174,7 +1174,7 @@ def fp8_grouped_matmul(x, x_scale, weights, w_scale, offsets, rows=None, out=Non
     none is given.  Returns out bf16 [S,N]."""
     args, out, _ = _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, workspace,
                                      ctx, stream)
-    _call(_load().farn_fp8_grouped_matmul, args, "farn_fp8_grouped_matmul")
+    _call((_lib or _load()).farn_fp8_grouped_matmul, args, "farn_fp8_grouped_matmul")
     return out
 
 
@@ -1204,84 +1204,111 @@ def kv_cache(n_pages: int, page_size: int, heads: int, head_dim: int, format: st
 
 def _cache_args(cache, tensor_scales, index, dev):
     """The C struct of a cache's four tensors."""
-    torch = _torch
     kc, vc, ks, vs = cache
-    sc = kc.shape
+    u8, sc, ss = _torch.uint8, kc.shape, ks.shape
+    kind = ks.dtype
     if len(sc) != 4:
         raise ValueError("the cache's codes must be [n_pages, page_size, heads, ..]")
-    fp8 = ks.dtype is torch.float32
-    D = sc[3] if fp8 else sc[3] * 2
-    if not fp8 and D % 16:
-        raise ValueError(f"NVFP4 needs head_dim % 16 == 0, got {D}")
-    scale_shape = sc[:3] if fp8 else (*sc[:3], D // 16)
-    scale_type = torch.float32 if fp8 else torch.uint8
-    if not (kc.dtype is torch.uint8 and vc.dtype is torch.uint8 and vc.shape == sc and
-            ks.dtype is scale_type and vs.dtype is scale_type and ks.shape == scale_shape and
-            vs.shape == scale_shape and kc.get_device() == index and vc.get_device() == index and
+    P, page, H, D = sc
+    if kind is _torch.float32:
+        format, gk, gv = FARN_CACHE_FP8, 1.0, 1.0
+        fits = ss == sc[:3]
+    else:
+        format = FARN_CACHE_NVFP4
+        D *= 2
+        if D % 16:
+            raise ValueError(f"NVFP4 needs head_dim % 16 == 0, got {D}")
+        if tensor_scales is None:
+            raise ValueError("an NVFP4 cache needs tensor_scales (keys', values')")
+        gk, gv = tensor_scales
+        fits = kind is u8 and ss == (P, page, H, D // 16)
+    if not (fits and vs.dtype is kind and kc.dtype is u8 and vc.dtype is u8 and vc.shape == sc and
+            vs.shape == ss and kc.get_device() == index and vc.get_device() == index and
             ks.get_device() == index and vs.get_device() == index and kc.is_contiguous() and
             vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
-        for t, name, shape, dt in ((kc, "k_codes", sc, torch.uint8),
-                                   (vc, "v_codes", sc, torch.uint8),
-                                   (ks, "k_scale", scale_shape, scale_type),
-                                   (vs, "v_scale", scale_shape, scale_type)):
-            _check_tensor(t, "the cache's " + name, shape, dev, (dt,))
-    if fp8:
-        gk = gv = 1.0
-    elif tensor_scales is None:
-        raise ValueError("an NVFP4 cache needs tensor_scales (keys', values')")
-    else:
-        gk, gv = tensor_scales
-    return KvCache(FARN_CACHE_FP8 if fp8 else FARN_CACHE_NVFP4, sc[1], sc[0], sc[2], D,
-                   kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), gk, gv)
+        shape = tuple(sc[:3]) if format == FARN_CACHE_FP8 else (P, page, H, D // 16)
+        for t, name, want, dt in ((kc, "k_codes", sc, u8), (vc, "v_codes", sc, u8),
+                                  (ks, "k_scale", shape, kind), (vs, "v_scale", shape, kind)):
+            _check_tensor(t, "the cache's " + name, want, dev,
+                          (dt if dt is _torch.float32 else u8,))
+    return KvCache(format, page, P, H, D, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
+                   vs.data_ptr(), gk, gv)
 
 
-def _heads_view(x, name, index, dev, T=None, D=None, heads=None):
-    """[T, heads, D] and the stride of its tokens: heads contiguous within a
-    token, tokens anywhere behind each other."""
+def _check_heads(x, name, index, dev, T, heads, D):
+    """What the short checks of [T, heads, D] turned down: heads contiguous
+    within a token, tokens anywhere behind each other."""
+    if not isinstance(x, _torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, D]")
+    if x.dtype is not _torch.bfloat16:
+        raise TypeError(f"{name} must be {_torch.bfloat16}, got {x.dtype}")
+    if not x.is_cuda or x.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {x.device}")
+    if tuple(x.shape) != (T, heads, D):
+        raise ValueError(f"{name} must have shape {(T, heads, D)}, got {tuple(x.shape)}")
+    st = x.stride()
+    if (D > 1 and st[2] != 1) or (heads > 1 and st[1] != D):
+        raise ValueError(f"{name}'s heads must lie one after the other within a token")
+
+
+def _token_stride(x, name, index, dev, T, heads, D):
+    """The stride of the tokens of a tensor [T, heads, D]."""
+    st = x.stride()
+    if not (len(st) == 3 and st[2] == 1 and st[1] == D and x.dtype is _torch.bfloat16 and
+            x.get_device() == index and index >= 0 and x.shape == (T, heads, D)):
+        _check_heads(x, name, index, dev, T, heads, D)
+    return st[0] if T > 1 else heads * D
+
+
+def _heads_shape(x, name):
     sx = x.shape
     if len(sx) != 3:
         raise ValueError(f"{name} must be [T, heads, D]")
-    if x.get_device() != index or x.dtype is not _torch.bfloat16 or index < 0:
-        _check_tensor(x, name, sx, dev)       # what it turns down first
-    if (T is not None and sx[0] != T) or (D is not None and sx[2] != D) or \
-            (heads is not None and sx[1] != heads):
-        raise ValueError(f"{name} must be [{T}, {heads if heads is not None else 'heads'}, {D}], "
-                         f"got {tuple(sx)}")
-    st = x.stride()
-    if (sx[2] > 1 and st[2] != 1) or (sx[1] > 1 and st[1] != sx[2]):
-        raise ValueError(f"{name}'s heads must lie one after the other within a token")
-    return st[0] if sx[0] > 1 else sx[1] * sx[2]
+    return sx
+
+
+def _check_rope(positions, freqs, sections, T, D, dev):
+    """What the short checks of a rotation turned down."""
+    i32, f32 = _torch.int32, _torch.float32
+    R = 2 * freqs.shape[0] if freqs.dim() == 1 else -1
+    if not 0 < R <= D:
+        raise ValueError(f"freqs must be [R / 2] for R in 2..{D}, got {tuple(freqs.shape)}")
+    if positions is None or positions.dim() not in (1, 2) or positions.shape[-1] != T:
+        raise ValueError(f"positions must be [T] or [axes, T] for T = {T}")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if not 1 <= axes <= 4:
+        raise ValueError(f"positions must have 1..4 axes, got {axes}")
+    _check_tensor(positions, "positions", positions.shape, dev, (i32,))
+    _check_tensor(freqs, "freqs", (R // 2,), dev, (f32,))
+    if axes > 1 and sections is None:
+        raise ValueError("positions of several axes need sections")
+    if sections is not None and (len(sections) != axes or min(sections) < 0 or
+                                 sum(sections) != R // 2):
+        raise ValueError(f"sections must be {axes} counts of pairs with the sum {R // 2}, got "
+                         f"{tuple(sections)}")
+
+
+_section_arrays = tuple(ctypes.c_int * n for n in range(5))
 
 
 def _rope_args(positions, freqs, sections, T, D, index, dev):
-    torch = _torch
+    """(positions, axes, sections, freqs, R) as the C call takes them."""
     if freqs is None:
         return None, 0, None, None, 0
-    sp = positions.shape
-    if len(sp) == 1:
-        sp = (1, *sp)
-    R = 2 * freqs.shape[0] if freqs.dim() == 1 else -1
-    if not (len(sp) == 2 and sp[1] == T and positions.dtype is torch.int32 and
-            freqs.dtype is torch.float32 and 0 < R <= D and positions.get_device() == index and
-            freqs.get_device() == index and positions.is_contiguous() and freqs.is_contiguous()):
-        if len(sp) != 2 or sp[1] != T:
-            raise ValueError(f"positions must be [T] or [axes, T] for T = {T}, got "
-                             f"{tuple(positions.shape)}")
-        if not 0 < R <= D:
-            raise ValueError(f"freqs must be [R / 2] for R in 2..{D}, got {tuple(freqs.shape)}")
-        _check_tensor(positions, "positions", positions.shape, dev, (torch.int32,))
-        _check_tensor(freqs, "freqs", (R // 2,), dev, (torch.float32,))
-    axes = sp[0]
-    if not 1 <= axes <= 4:
-        raise ValueError(f"positions must have 1..4 axes, got {axes}")
-    if sections is None:
-        if axes > 1:
-            raise ValueError("positions of several axes need sections")
-        sections = (R // 2,)
-    if len(sections) != axes or min(sections) < 0 or sum(sections) != R // 2:
-        raise ValueError(f"sections must be {axes} counts of pairs with the sum {R // 2}, got "
-                         f"{tuple(sections)}")
-    return positions, axes, (ctypes.c_int * axes)(*sections), freqs, R
+    half = freqs.shape[0] if freqs.dim() == 1 else 0
+    sp = positions.shape if positions is not None else ()
+    axes = sp[0] if len(sp) == 2 else 1
+    if not (0 < half <= D // 2 and sp and sp[-1] == T and 1 <= axes <= 4 and len(sp) <= 2 and
+            positions.dtype is _torch.int32 and freqs.dtype is _torch.float32 and
+            positions.get_device() == index and freqs.get_device() == index and
+            positions.is_contiguous() and freqs.is_contiguous() and
+            (axes == 1 if sections is None else len(sections) == axes and
+             sum(sections) == half and min(sections) >= 0)):
+        _check_rope(positions, freqs, sections, T, D, dev)
+    pairs = (half,) if sections is None else sections
+    return positions.data_ptr(), axes, _section_arrays[axes](*pairs), freqs.data_ptr(), 2 * half
 
 
 def _weight_arg(w, name, D, index, dev):
@@ -1296,29 +1323,28 @@ def _weight_arg(w, name, D, index, dev):
 def _qk_args(q, k, q_weight, k_weight, eps, positions, freqs, sections, interleaved, out, ctx,
              stream):
     torch = _torch or _load_torch()
-    index, dev = q.get_device(), q.device
-    q_stride = _heads_view(q, "q", index, dev)
-    T, HQ, D = q.shape
-    k_stride = _heads_view(k, "k", index, dev, T, D)
-    HK = k.shape[1]
+    index, dev, bf = q.get_device(), q.device, torch.bfloat16
+    T, HQ, D = _heads_shape(q, "q")
+    HK = _heads_shape(k, "k")[1]
+    q_stride = _token_stride(q, "q", index, dev, T, HQ, D)
+    k_stride = _token_stride(k, "k", index, dev, T, HK, D)
     pos, axes, sect, fr, R = _rope_args(positions, freqs, sections, T, D, index, dev)
     if out is None:
-        out = (torch.empty((T, HQ, D), dtype=torch.bfloat16, device=dev),
-               torch.empty((T, HK, D), dtype=torch.bfloat16, device=dev))
+        out = (torch.empty((T, HQ, D), dtype=bf, device=dev),
+               torch.empty((T, HK, D), dtype=bf, device=dev))
         qs, ks = HQ * D, HK * D
     else:
         out = tuple(out)
         if len(out) != 2:
             raise ValueError("out must be (q, k)")
-        qs = _heads_view(out[0], "the output of q", index, dev, T, D, HQ)
-        ks = _heads_view(out[1], "the output of k", index, dev, T, D, HK)
+        qs = _token_stride(out[0], "the output of q", index, dev, T, HQ, D)
+        ks = _token_stride(out[1], "the output of k", index, dev, T, HK, D)
     c = _context_of(ctx, index)
     return (c.handle, T, D, q.data_ptr(), HQ, q_stride, k.data_ptr(), HK, k_stride,
             _weight_arg(q_weight, "q_weight", D, index, dev),
-            _weight_arg(k_weight, "k_weight", D, index, dev), eps,
-            None if pos is None else pos.data_ptr(), axes, sect,
-            None if fr is None else fr.data_ptr(), R, 1 if interleaved else 0,
-            out[0].data_ptr(), qs, out[1].data_ptr(), ks, _raw_stream(stream, index)), out, c
+            _weight_arg(k_weight, "k_weight", D, index, dev), eps, pos, axes, sect, fr, R,
+            1 if interleaved else 0, out[0].data_ptr(), qs, out[1].data_ptr(), ks,
+            _raw_stream(stream, index)), out, c
 
 
 def prepare_qk_norm_rope(q, k, q_weight, k_weight, eps: float, positions=None, freqs=None,
@@ -1342,39 +1368,48 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps: float, positions=None, freqs=Non
     `interleaved`.  out may be (q, k) themselves.  Returns (q, k)."""
     args, out, _ = _qk_args(q, k, q_weight, k_weight, eps, positions, freqs, sections,
                             interleaved, out, ctx, stream)
-    _call(_load().farn_qk_norm_rope, args, "farn_qk_norm_rope")
+    _call((_lib or _load()).farn_qk_norm_rope, args, "farn_qk_norm_rope")
     return out
+
+
+def _slots_arg(slots, T, index, dev):
+    if not (slots.get_device() == index and slots.dtype is _torch.int32 and
+            slots.shape == (T,) and slots.is_contiguous()):
+        _check_tensor(slots, "slots", (T,), dev, (_torch.int32,))
+    return slots.data_ptr()
+
+
+def _cache_of(cache, tensor_scales, index, dev, HK, D):
+    store = _cache_args(cache, tensor_scales, index, dev)
+    if store.heads != HK or store.head_dim != D:
+        raise ValueError(f"the cache has {store.heads} heads of {store.head_dim}, k has {HK} of "
+                         f"{D}")
+    return store
 
 
 def _qk_cache_args(q, k, v, q_weight, k_weight, eps, positions, freqs, cache, slots,
                    tensor_scales, sections, interleaved, out, ctx, stream):
     torch = _torch or _load_torch()
     index, dev = q.get_device(), q.device
-    q_stride = _heads_view(q, "q", index, dev)
-    T, HQ, D = q.shape
-    k_stride = _heads_view(k, "k", index, dev, T, D)
-    HK = k.shape[1]
-    v_stride = _heads_view(v, "v", index, dev, T, D, HK)
+    T, HQ, D = _heads_shape(q, "q")
+    HK = _heads_shape(k, "k")[1]
+    q_stride = _token_stride(q, "q", index, dev, T, HQ, D)
+    k_stride = _token_stride(k, "k", index, dev, T, HK, D)
+    v_stride = _token_stride(v, "v", index, dev, T, HK, D)
     pos, axes, sect, fr, R = _rope_args(positions, freqs, sections, T, D, index, dev)
-    if not (slots.get_device() == index and slots.dtype is torch.int32 and
-            slots.shape == (T,) and slots.is_contiguous()):
-        _check_tensor(slots, "slots", (T,), dev, (torch.int32,))
-    store = _cache_args(cache, tensor_scales, index, dev)
-    if store.heads != HK or store.head_dim != D:
-        raise ValueError(f"the cache has {store.heads} heads of {store.head_dim}, k has {HK} of "
-                         f"{D}")
+    slots_at = _slots_arg(slots, T, index, dev)
+    store = _cache_of(cache, tensor_scales, index, dev, HK, D)
     if out is None:
         out = torch.empty((T, HQ, D), dtype=torch.bfloat16, device=dev)
         qs = HQ * D
     else:
-        qs = _heads_view(out, "the output of q", index, dev, T, D, HQ)
+        qs = _token_stride(out, "the output of q", index, dev, T, HQ, D)
     c = _context_of(ctx, index)
     return (c.handle, T, D, q.data_ptr(), HQ, q_stride, k.data_ptr(), k_stride, v.data_ptr(),
             v_stride, HK, _weight_arg(q_weight, "q_weight", D, index, dev),
-            _weight_arg(k_weight, "k_weight", D, index, dev), eps,
-            None if pos is None else pos.data_ptr(), axes, sect,
-            None if fr is None else fr.data_ptr(), R, 1 if interleaved else 0, out.data_ptr(), qs,
-            store, slots.data_ptr(), _raw_stream(stream, index)), out, c
+            _weight_arg(k_weight, "k_weight", D, index, dev), eps, pos, axes, sect, fr, R,
+            1 if interleaved else 0, out.data_ptr(), qs, store, slots_at,
+            _raw_stream(stream, index)), out, c
 
 
 def prepare_qk_norm_rope_cache(q, k, v, q_weight, k_weight, eps: float, positions, freqs, cache,
@@ -1397,25 +1432,20 @@ def qk_norm_rope_cache(q, k, v, q_weight, k_weight, eps: float, positions, freqs
     the values' of an NVFP4 cache.  Returns q."""
     args, out, _ = _qk_cache_args(q, k, v, q_weight, k_weight, eps, positions, freqs, cache,
                                   slots, tensor_scales, sections, interleaved, out, ctx, stream)
-    _call(_load().farn_qk_norm_rope_cache, args, "farn_qk_norm_rope_cache")
+    _call((_lib or _load()).farn_qk_norm_rope_cache, args, "farn_qk_norm_rope_cache")
     return out
 
 
 def _kv_write_args(k, v, cache, slots, tensor_scales, ctx, stream):
-    torch = _torch or _load_torch()
+    _torch or _load_torch()
     index, dev = k.get_device(), k.device
-    k_stride = _heads_view(k, "k", index, dev)
-    T, HK, D = k.shape
-    v_stride = _heads_view(v, "v", index, dev, T, D, HK)
-    if not (slots.get_device() == index and slots.dtype is torch.int32 and
-            slots.shape == (T,) and slots.is_contiguous()):
-        _check_tensor(slots, "slots", (T,), dev, (torch.int32,))
-    store = _cache_args(cache, tensor_scales, index, dev)
-    if store.heads != HK or store.head_dim != D:
-        raise ValueError(f"the cache has {store.heads} heads of {store.head_dim}, k has {HK} of "
-                         f"{D}")
+    T, HK, D = _heads_shape(k, "k")
+    k_stride = _token_stride(k, "k", index, dev, T, HK, D)
+    v_stride = _token_stride(v, "v", index, dev, T, HK, D)
+    slots_at = _slots_arg(slots, T, index, dev)
+    store = _cache_of(cache, tensor_scales, index, dev, HK, D)
     c = _context_of(ctx, index)
-    return (c.handle, T, k.data_ptr(), k_stride, v.data_ptr(), v_stride, store, slots.data_ptr(),
+    return (c.handle, T, k.data_ptr(), k_stride, v.data_ptr(), v_stride, store, slots_at,
             _raw_stream(stream, index)), c
 
 
@@ -1430,7 +1460,7 @@ def kv_write(k, v, cache, slots, tensor_scales=None, ctx=None, stream=None):
     cache as they are; slots and tensor_scales as for ``qk_norm_rope_cache``.
     Returns the cache."""
     args, _ = _kv_write_args(k, v, cache, slots, tensor_scales, ctx, stream)
-    _call(_load().farn_kv_write, args, "farn_kv_write")
+    _call((_lib or _load()).farn_kv_write, args, "farn_kv_write")
     return cache
 
 
@@ -1441,9 +1471,10 @@ def _kv_read_args(cache, table, offsets, n_tokens, tensor_scales, out, ctx, stre
     if index < 0:
         _check_tensor(cache[0], "the cache's k_codes", cache[0].shape, dev, (torch.uint8,))
     store = _cache_args(cache, tensor_scales, index, dev)
-    if table.dim() != 2:
+    st = table.shape
+    if len(st) != 2:
         raise ValueError("table must be [B, width]")
-    B, width = table.shape
+    B, width = st
     n = int(n_tokens)
     if n < 0:
         raise ValueError(f"n_tokens must not be negative, got {n}")
@@ -1483,5 +1514,5 @@ def kv_read(cache, table, offsets, n_tokens: int, tensor_scales=None, out=None, 
     [n_tokens,heads,head_dim]; a page outside the cache reads as zeros, and
     tokens that no sequence has are left as they were."""
     args, out, _ = _kv_read_args(cache, table, offsets, n_tokens, tensor_scales, out, ctx, stream)
-    _call(_load().farn_kv_read, args, "farn_kv_read")
+    _call((_lib or _load()).farn_kv_read, args, "farn_kv_read")
     return out

@@ -19,19 +19,39 @@ constexpr int kB = farn::kFp8Block;
 constexpr int kLanes = kB / 8;        // lanes of a block's row: 8 elements each
 constexpr int kRowBlocks = 4;         // blocks of one row per half warp, loads in flight
 
-// The 8 elements of a row from column h on; those outside the row are 0.
+// The 8 elements of a row from column h on, as bf16; those outside the row are 0.
 // VEC: x 16-byte aligned and H a multiple of 8, so all or none of them exist.
 template <bool VEC>
-__device__ __forceinline__ void load8(const uint16_t* x, int64_t at, int64_t h, int64_t H,
-                                      float* v) {
+__device__ __forceinline__ uint4 load8(const uint16_t* x, int64_t at, int64_t h, int64_t H) {
+  uint4 u = make_uint4(0u, 0u, 0u, 0u);
   if constexpr (VEC) {
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
     if (h < H) u = farn::ld_stream(reinterpret_cast<const uint4*>(x + at));
-    farn::unpack8(u, v);
   } else {
+    uint32_t v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = h + e < H ? farn::bf_lo(x[at + e]) : 0.0f;
+    for (int e = 0; e < 8; ++e) v[e] = h + e < H ? (uint32_t)x[at + e] : 0u;
+    u = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
   }
+  return u;
+}
+// The largest magnitudes of two pairs of bf16, NaN ignored.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t amax2(uint4 u) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  return max2(max2(u.x & kAbs, u.y & kAbs), max2(u.z & kAbs, u.w & kAbs));
+}
+// Of a pair, in fp32; two NaN are 0, as if they had been ignored.
+__device__ __forceinline__ float amax_of(uint32_t m) {
+  return fmaxf(fmaxf(farn::bf_lo(m), farn::bf_hi(m)), 0.0f);
+}
+__device__ __forceinline__ uint2 codes8(uint4 u, float inv) {
+  float v[8];
+  farn::unpack8(u, v);
+  return farn::fp8_codes8(v, inv);
 }
 template <bool VEC>
 __device__ __forceinline__ void store8(uint8_t* codes, int64_t at, int64_t h, int64_t H,
@@ -56,7 +76,7 @@ quantize_rows_kernel(const uint16_t* x, uint8_t* codes, float* scales, int64_t b
   const int lane = threadIdx.x % kLanes, half = threadIdx.x / kLanes;
   constexpr int kHalves = kThreads / kLanes;
   const int64_t b0 = (int64_t)blockIdx.x * (kHalves * kRowBlocks) + half;
-  float v[kRowBlocks][8];
+  uint4 v[kRowBlocks];
   int64_t at[kRowBlocks], col[kRowBlocks];
 #pragma unroll
   for (int i = 0; i < kRowBlocks; ++i) {
@@ -64,15 +84,15 @@ quantize_rows_kernel(const uint16_t* x, uint8_t* codes, float* scales, int64_t b
     const int64_t t = blocks <= 0xFFFFFFFFll ? (int64_t)((uint32_t)b / (uint32_t)HB) : b / HB;
     col[i] = b < blocks ? (b - t * HB) * kB + lane * 8 : H;      // H: no block
     at[i] = t * H + col[i];
-    load8<VEC>(x, at[i], col[i], H, v[i]);
+    v[i] = load8<VEC>(x, at[i], col[i], H);
   }
 #pragma unroll
   for (int i = 0; i < kRowBlocks; ++i) {
-    float m = farn::amax8(v[i]);
+    float m = amax_of(amax2(v[i]));
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     const farn::Fp8Scale s = farn::fp8_scale(m);
-    store8<VEC>(codes, at[i], col[i], H, farn::fp8_codes8(v[i], s.inv));
+    store8<VEC>(codes, at[i], col[i], H, codes8(v[i], s.inv));
     const int64_t b = b0 + i * kHalves;
     if (lane == 0 && b < blocks) scales[b] = s.scale;
   }
@@ -91,16 +111,16 @@ quantize_tiles_kernel(const uint16_t* x, uint8_t* codes, float* scales, int64_t 
   const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
   const int64_t hb = blockIdx.x % HB, q = blockIdx.x / HB, tb = q % TB, e = q / TB;
   const int64_t h = hb * kB + lane * 8;
-  float v[kPasses][8];
-  float m = 0.0f;
+  uint4 v[kPasses];
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int64_t t = tb * kB + i * kRows + sub;
-    load8<VEC>(x, (e * T + t) * H + h, t < T ? h : H, H, v[i]);
+    v[i] = load8<VEC>(x, (e * T + t) * H + h, t < T ? h : H, H);
   }
+  uint32_t m2 = 0u;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) m = fmaxf(m, farn::amax8(v[i]));
-  m = farn::warp_max(m);
+  for (int i = 0; i < kPasses; ++i) m2 = max2(m2, amax2(v[i]));
+  float m = farn::warp_max(amax_of(m2));
   if (threadIdx.x % 32 == 0) warp_max[threadIdx.x / 32] = m;
   __syncthreads();
 #pragma unroll
@@ -109,7 +129,7 @@ quantize_tiles_kernel(const uint16_t* x, uint8_t* codes, float* scales, int64_t 
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int64_t t = tb * kB + i * kRows + sub;
-    store8<VEC>(codes, (e * T + t) * H + h, t < T ? h : H, H, farn::fp8_codes8(v[i], s.inv));
+    store8<VEC>(codes, (e * T + t) * H + h, t < T ? h : H, H, codes8(v[i], s.inv));
   }
   if (threadIdx.x == 0) scales[blockIdx.x] = s.scale;
 }

@@ -411,8 +411,9 @@ struct ReadParams {
 };
 
 constexpr int kReadThreads = 256;
-constexpr int kReadTokens = 8;        // per CTA
-constexpr int kReadAhead = 4;         // vectors per thread whose loads are in flight
+constexpr int kReadTokens = 4;        // per warp, or part of a warp that has a token
+constexpr int kReadAhead = 4;         // vectors per lane, of keys and of values, in flight
+constexpr int kPlainTokens = 8;       // per CTA of the scalar kernel
 
 // The cache slot of output token n: -1 where its page does not exist, -2
 // where no sequence has it.
@@ -441,13 +442,13 @@ struct Piece {
 };
 template <int FMT>
 __device__ __forceinline__ Piece<FMT> load_piece(const ReadParams& p, int which, int64_t slot,
-                                                 int e) {
+                                                 int e, int head) {
   Piece<FMT> r;
   const int64_t row = (int64_t)p.heads * p.D;
   if constexpr (FMT == FARN_CACHE_FP8) {
     r.codes = __ldg(reinterpret_cast<const uint2*>(p.cache.codes[which] + slot * row + e));
     r.scale = __ldg(static_cast<const float*>(p.cache.scale[which]) + slot * p.heads +
-                    e / p.D);
+                    head);
   } else {
     r.codes.x = __ldg(reinterpret_cast<const uint32_t*>(p.cache.codes[which] + (slot * row + e) / 2));
     r.codes.y = 0u;
@@ -478,59 +479,84 @@ __device__ __forceinline__ uint4 piece_values(const ReadParams& p, int which, co
   return farn::pack8(x);
 }
 
-template <int FMT, bool VEC>
+// LPT lanes to a token, 8 elements each at a time: a lane's places in the row, and
+// with them its heads, are the same for all its tokens.  Memory bound: at 5120
+// tokens of 32 sequences, 8 heads of 128 in 8 bits (a block per 8 tokens, places
+// worked out for every vector: 147 us).
+template <int FMT, int LPT>
 __global__ void __launch_bounds__(kReadThreads)
 cache_read_kernel(const __grid_constant__ ReadParams p) {
-  __shared__ int64_t slots[kReadTokens];
   farn::pdl_wait();
   farn::pdl_trigger();
-  const int64_t n0 = (int64_t)blockIdx.x * kReadTokens;
-  if (threadIdx.x < kReadTokens) slots[threadIdx.x] = slot_of(p, n0 + threadIdx.x);
-  __syncthreads();
-  const int row = p.heads * p.D;
-  if constexpr (VEC) {
-    const int vecs = row / 8, total = kReadTokens * 2 * vecs;
-    for (int i0 = threadIdx.x; i0 < total; i0 += kReadThreads * kReadAhead) {
-      Piece<FMT> r[kReadAhead];
+  constexpr int kSubs = 32 / LPT;
+  const int lane = threadIdx.x & 31, l = lane % LPT, sub = lane / LPT;
+  const int row = p.heads * p.D, vecs = row / 8;
+  const int64_t n0 =
+      ((int64_t)blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5)) * (kSubs * kReadTokens);
+  if (n0 >= p.tokens) return;
+  // lane i looks up token n0 + i
+  const int64_t mine = lane < kSubs * kReadTokens ? slot_of(p, n0 + lane) : -2;
+  for (int v0 = 0; v0 < vecs; v0 += LPT * kReadAhead) {
+    int head[kReadAhead];
+#pragma unroll
+    for (int j = 0; j < kReadAhead; ++j) head[j] = (v0 + j * LPT + l) * 8 / p.D;
+#pragma unroll 1
+    for (int i = 0; i < kReadTokens; ++i) {
+      const int at = i * kSubs + sub;
+      const int64_t slot = __shfl_sync(0xFFFFFFFFu, mine, at);
+      Piece<FMT> r[2][kReadAhead];
 #pragma unroll
       for (int j = 0; j < kReadAhead; ++j) {
-        const int i = i0 + j * kReadThreads;
-        if (i >= total) break;
-        const int t = i / (2 * vecs), v = i - t * 2 * vecs, which = v >= vecs;
-        if (slots[t] >= 0) r[j] = load_piece<FMT>(p, which, slots[t], (v - which * vecs) * 8);
-      }
-#pragma unroll
-      for (int j = 0; j < kReadAhead; ++j) {
-        const int i = i0 + j * kReadThreads;
-        if (i >= total) break;
-        const int t = i / (2 * vecs), v = i - t * 2 * vecs, which = v >= vecs;
-        if (slots[t] == -2) continue;
-        uint4 o = make_uint4(0u, 0u, 0u, 0u);
-        if (slots[t] >= 0) o = piece_values<FMT>(p, which, r[j]);
-        *reinterpret_cast<uint4*>(p.out[which] + (n0 + t) * row + (v - which * vecs) * 8) = o;
-      }
-    }
-  } else {
-    const int total = kReadTokens * 2 * row;
-    for (int i = threadIdx.x; i < total; i += kReadThreads) {
-      const int t = i / (2 * row), v = i - t * 2 * row, which = v >= row, e = v - which * row;
-      const int64_t slot = slots[t];
-      if (slot == -2) continue;
-      float x = 0.0f;
-      if (slot >= 0) {
-        const int64_t at = slot * row + e;
-        if constexpr (FMT == FARN_CACHE_FP8) {
-          x = farn::e4m3_to_f32(p.cache.codes[which][at]) *
-              static_cast<const float*>(p.cache.scale[which])[slot * p.heads + e / p.D];
-        } else {
-          const float2 f = farn::e2m1x2_to_f32(p.cache.codes[which][at / 2]);
-          x = ((at & 1) ? f.y : f.x) *
-              (farn::e4m3_to_f32(static_cast<const uint8_t*>(p.cache.scale[which])[at / 16]) /
-               p.cache.g[which]);
+        const int v = v0 + j * LPT + l;
+        if (v < vecs && slot >= 0) {
+          r[0][j] = load_piece<FMT>(p, 0, slot, v * 8, head[j]);
+          r[1][j] = load_piece<FMT>(p, 1, slot, v * 8, head[j]);
         }
       }
-      p.out[which][(n0 + t) * row + e] = farn::to_bf16(x);
+#pragma unroll
+      for (int j = 0; j < kReadAhead; ++j) {
+        const int v = v0 + j * LPT + l;
+        if (v < vecs && slot != -2) {
+#pragma unroll
+          for (int which = 0; which < 2; ++which) {
+            uint4 o = make_uint4(0u, 0u, 0u, 0u);
+            if (slot >= 0) o = piece_values<FMT>(p, which, r[which][j]);
+            *reinterpret_cast<uint4*>(p.out[which] + (n0 + at) * row + v * 8) = o;
+          }
+        }
+      }
     }
+  }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kReadThreads)
+cache_read_plain_kernel(const __grid_constant__ ReadParams p) {
+  __shared__ int64_t slots[kPlainTokens];
+  farn::pdl_wait();
+  farn::pdl_trigger();
+  const int64_t n0 = (int64_t)blockIdx.x * kPlainTokens;
+  if (threadIdx.x < kPlainTokens) slots[threadIdx.x] = slot_of(p, n0 + threadIdx.x);
+  __syncthreads();
+  const int row = p.heads * p.D, total = kPlainTokens * 2 * row;
+  for (int i = threadIdx.x; i < total; i += kReadThreads) {
+    const int t = i / (2 * row), v = i - t * 2 * row, which = v >= row, e = v - which * row;
+    const int64_t slot = slots[t];
+    if (slot == -2) continue;
+    float x = 0.0f;
+    if (slot >= 0) {
+      const int64_t at = slot * row + e;
+      if constexpr (FMT == FARN_CACHE_FP8) {
+        x = farn::e4m3_to_f32(p.cache.codes[which][at]) *
+            static_cast<const float*>(p.cache.scale[which])[slot * p.heads + e / p.D];
+      } else {
+        const float2 f = farn::e2m1x2_to_f32(p.cache.codes[which][at / 2]);
+        x = ((at & 1) ? f.y : f.x) *
+            (farn::e4m3_to_f32(static_cast<const uint8_t*>(p.cache.scale[which])[at / 16]) /
+             p.cache.g[which]);
+      }
+    }
+    p.out[which][(n0 + t) * row + e] = farn::to_bf16(x);
   }
 }
 
@@ -630,6 +656,15 @@ void set_cache(Cache* to, const farn_kv_cache* c) {
 bool cache_aligned(const farn_kv_cache* c, bool write) {
   const uintptr_t need = (c->format == FARN_CACHE_FP8 ? 8u : 4u) / (write ? 2u : 1u) - 1u;
   return (((uintptr_t)c->k_codes | (uintptr_t)c->v_codes) & need) == 0;
+}
+
+typedef void (*ReadKernel)(const ReadParams);
+
+template <int FMT>
+ReadKernel read_kernel(int lpt) {
+  return lpt == 32 ? cache_read_kernel<FMT, 32>
+                   : lpt == 16 ? cache_read_kernel<FMT, 16>
+                               : lpt == 8 ? cache_read_kernel<FMT, 8> : cache_read_kernel<FMT, 4>;
 }
 
 typedef void (*HeadsKernel)(const HeadsParams);
@@ -884,14 +919,18 @@ int farn_kv_read(const farn_ctx* ctx, const farn_kv_cache* cache, const int32_t*
   p.out[1] = static_cast<uint16_t*>(v_out);
   const bool vec = ctx->force_variant != kVariantGeneric && cache->head_dim % 8 == 0 &&
                    cache_aligned(cache, false) && aligned16(k_out) && aligned16(v_out);
-  const int64_t grid = (n_tokens + kReadTokens - 1) / kReadTokens;
-  const bool fp8 = cache->format == FARN_CACHE_FP8;
+  if (!vec)
+    return launch(ctx,
+                  cache->format == FARN_CACHE_FP8 ? cache_read_plain_kernel<FARN_CACHE_FP8>
+                                                  : cache_read_plain_kernel<FARN_CACHE_NVFP4>,
+                  (n_tokens + kPlainTokens - 1) / kPlainTokens, kReadThreads, stream, p);
+  const int64_t vecs = row / 8;
+  const int lpt = vecs > 16 ? 32 : vecs > 8 ? 16 : vecs > 4 ? 8 : 4;
+  const int64_t per = (kReadThreads / 32) * (32 / lpt) * kReadTokens;
   return launch(ctx,
-                fp8 ? (vec ? cache_read_kernel<FARN_CACHE_FP8, true>
-                           : cache_read_kernel<FARN_CACHE_FP8, false>)
-                    : (vec ? cache_read_kernel<FARN_CACHE_NVFP4, true>
-                           : cache_read_kernel<FARN_CACHE_NVFP4, false>),
-                grid, kReadThreads, stream, p);
+                cache->format == FARN_CACHE_FP8 ? read_kernel<FARN_CACHE_FP8>(lpt)
+                                                : read_kernel<FARN_CACHE_NVFP4>(lpt),
+                (n_tokens + per - 1) / per, kReadThreads, stream, p);
 }
 
 }  // extern "C"
