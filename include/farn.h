@@ -507,6 +507,22 @@ int farn_fp8_grouped_matmul(const farn_ctx *ctx, const void *x,
 int farn_fp8_grouped_workspace(const farn_ctx *ctx, int64_t n_slots, int E,
                                int64_t N, int64_t H, int64_t *bytes);
 
+/* Which kernel farn_fp8_matmul or farn_fp8_grouped_matmul would launch for these
+ * sizes and pointers, without launching: 2 generic (any H or alignment), 6 tensor
+ * (the tensor cores, a tile of 128 weights by 64 slots per CTA, *ctas of them
+ * splitting the row), 7 pair (the tensor cores, two CTAs per tile of 256 slots by
+ * 256 weights; with `rows` only if a workspace is given, here any 16-byte aligned
+ * pointer).  Otherwise as farn_plan_grouped_matmul. */
+int farn_plan_fp8_matmul(const farn_ctx *ctx, const void *a_codes,
+                         const void *b_codes, int64_t T, int64_t N, int64_t H,
+                         const void *out, int *variant, int *ctas, int *threads);
+int farn_plan_fp8_grouped_matmul(const farn_ctx *ctx, const void *x,
+                                 int64_t n_rows, const int32_t *rows,
+                                 int64_t n_slots, const void *weights, int E,
+                                 int64_t N, int64_t H, const void *out,
+                                 const void *workspace, int *variant, int *ctas,
+                                 int *threads);
+
 /* farn_qk_norm_rope - RMSNorm of every query and key head and its rotation by
  * position, in one pass.  For a head's elements x[0..D):
  *     y[i] = (x[i] * rstd) * f(weight[i]),  rstd = 1 / sqrt(mean(x^2) + eps)

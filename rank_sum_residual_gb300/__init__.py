@@ -36,6 +36,7 @@ __all__ = [
     "farn_plan_grouped_matmul", "farn_plan_nvfp4_matmul",
     "farn_fp8_quantize", "fp8_quantize", "farn_fp8_matmul", "fp8_matmul",
     "farn_fp8_grouped_matmul", "fp8_grouped_matmul", "farn_fp8_grouped_workspace",
+    "farn_plan_fp8_matmul", "farn_plan_fp8_grouped_matmul",
     "FARN_CACHE_FP8", "FARN_CACHE_NVFP4", "KvCache", "kv_cache",
     "farn_qk_norm_rope", "qk_norm_rope", "farn_qk_norm_rope_cache", "qk_norm_rope_cache",
     "farn_kv_write", "kv_write", "farn_kv_read", "kv_read",
@@ -130,8 +131,13 @@ def _load():
                                                 i64, i64, vp, vp, i64, vp]
         lib.farn_fp8_grouped_workspace.argtypes = [vp, i64, i32, i64, i64, ctypes.POINTER(i64)]
         lib.farn_fp8_grouped_workspace.restype = i32
+        lib.farn_plan_fp8_matmul.argtypes = [vp, cvp, cvp, i64, i64, i64, cvp, pi, pi, pi]
+        lib.farn_plan_fp8_matmul.restype = i32
+        lib.farn_plan_fp8_grouped_matmul.argtypes = [vp, cvp, i64, cvp, i64, cvp, i32, i64, i64,
+                                                     cvp, cvp, pi, pi, pi]
+        lib.farn_plan_fp8_grouped_matmul.restype = i32
         lib.farn_fp8_grouped_matmul.restype = i32
-        pc, pi = ctypes.POINTER(KvCache), ctypes.POINTER(i32)
+        pc = ctypes.POINTER(KvCache)
         rope = [cvp, cvp, f32, cvp, i32, pi, cvp, i32, i32]
         lib.farn_qk_norm_rope.argtypes = [vp, i64, i32, cvp, i32, i64, cvp, i32, i64, *rope, vp,
                                           i64, vp, i64, vp]
@@ -331,6 +337,20 @@ def farn_fp8_grouped_workspace(ctx, n_slots, E, N, H) -> int:
     if st != FARN_OK:
         raise FarnError(st, "farn_fp8_grouped_workspace")
     return n.value
+
+
+def farn_plan_fp8_matmul(ctx, a_codes, b_codes, T, N, H, out):
+    """C ``farn_plan_fp8_matmul``: (variant name, CTAs per tile, threads per CTA)."""
+    return _plan(_load().farn_plan_fp8_matmul, "farn_plan_fp8_matmul", _addr(ctx),
+                 _addr(a_codes), _addr(b_codes), int(T), int(N), int(H), _addr(out))
+
+
+def farn_plan_fp8_grouped_matmul(ctx, x, n_rows, rows, n_slots, weights, E, N, H, out,
+                                 workspace=0):
+    """C ``farn_plan_fp8_grouped_matmul``: (variant name, CTAs per tile, threads per CTA)."""
+    return _plan(_load().farn_plan_fp8_grouped_matmul, "farn_plan_fp8_grouped_matmul",
+                 _addr(ctx), _addr(x), int(n_rows), _addr(rows), int(n_slots), _addr(weights),
+                 int(E), int(N), int(H), _addr(out), _addr(workspace))
 
 
 def _int_array(v):

@@ -764,7 +764,7 @@ int farn_create(farn_ctx** out, int device) {
   const bool inject_setup = inject && strcmp(inject, "setup") == 0;
   c->route_ok = !inject_setup && farn_host::route_setup(c) ? 1 : 0;
   c->encode_tiled = nullptr;
-  if (!inject_setup) c->fp8_ok = farn_host::product_setup(c) && farn_host::fp8_product_setup(c);
+  c->fp8_ok = !inject_setup && farn_host::product_setup(c) && farn_host::fp8_product_setup(c);
   cudaGetLastError();
   // The bulk kernel's status word: set on a bounded-wait timeout, read and
   // cleared by farn_device_status.

@@ -253,6 +253,23 @@ int launch(const farn_ctx* ctx, Fp8Params t, void* workspace, cudaStream_t strea
                        k->cg == 2 ? 2u : (unsigned)pl.ks, stream, t, map_w, map_x);
 }
 
+int report_plan(const farn_ctx* ctx, const ProductParams& p, bool can_copy, int* variant,
+                int* ctas, int* threads) {
+  Plan pl;
+  if (tc_takes(ctx, p) && plan_tc(ctx, p, can_copy, &pl)) {
+    *variant = pl.kind->cg == 2 ? kVariantPair : kVariantTensor;
+    *ctas = pl.kind->cg == 2 ? 2 : pl.ks;
+    *threads = pl.kind->warps * 32;
+  } else if (plain_tiles(p) > kMaxTiles) {
+    return FARN_ERR_UNSUPPORTED;
+  } else {
+    *variant = kVariantGeneric;
+    *ctas = 1;
+    *threads = farn::kPlainThreads;
+  }
+  return FARN_OK;
+}
+
 // Slots are 32-bit numbers, and a row of weights fits 31 bits.
 bool sizes_ok(int64_t S, int64_t N, int64_t H) {
   return S >= 0 && S <= 0x7FFFFFFF && N >= 1 && N <= 0x7FFFFFFF && H >= 1 && H <= 0x7FFFFFFF &&
@@ -317,6 +334,46 @@ int farn_fp8_matmul(const farn_ctx* ctx, const void* a_codes, const float* a_sca
   return launch(ctx, t, nullptr, stream);
 }
 
+int farn_plan_fp8_matmul(const farn_ctx* ctx, const void* a_codes, const void* b_codes, int64_t T,
+                         int64_t N, int64_t H, const void* out, int* variant, int* ctas,
+                         int* threads) {
+  if (!ctx || !variant || !ctas || !threads || !sizes_ok(T, N, H) || T < 1 || !product_fits(N, H) ||
+      !a_codes || !b_codes || !out)
+    return FARN_ERR_INVALID_ARG;
+  ProductParams p;
+  memset(&p, 0, sizeof p);
+  p.a = a_codes;
+  p.b = b_codes;
+  p.n_a = T;
+  p.S = T;
+  p.N = N;
+  p.H = H;
+  p.E = 1;
+  return report_plan(ctx, p, false, variant, ctas, threads);
+}
+
+int farn_plan_fp8_grouped_matmul(const farn_ctx* ctx, const void* x, int64_t n_rows,
+                                 const int32_t* rows, int64_t n_slots, const void* weights, int E,
+                                 int64_t N, int64_t H, const void* out, const void* workspace,
+                                 int* variant, int* ctas, int* threads) {
+  if (!ctx || !variant || !ctas || !threads || n_rows < 0 || n_rows > 0x7FFFFFFF ||
+      !sizes_ok(n_slots, N, H) || n_slots < 1 || E < 1 || E > FARN_MAX_EXPERTS ||
+      !product_fits(n_rows, 2 * H) || !product_fits(2 * N * H, E) ||
+      (!rows && n_rows != n_slots) || !weights || !out)
+    return FARN_ERR_INVALID_ARG;
+  ProductParams p;
+  memset(&p, 0, sizeof p);
+  p.a = x;
+  p.b = weights;
+  p.rows = rows;
+  p.n_a = n_rows;
+  p.S = n_slots;
+  p.N = N;
+  p.H = H;
+  p.E = E;
+  return report_plan(ctx, p, workspace && aligned16(workspace), variant, ctas, threads);
+}
+
 int farn_fp8_grouped_workspace(const farn_ctx* ctx, int64_t n_slots, int E, int64_t N, int64_t H,
                                int64_t* bytes) {
   if (!ctx || !bytes || !sizes_ok(n_slots, N, H) || E < 1 || E > FARN_MAX_EXPERTS)
@@ -346,7 +403,7 @@ int farn_fp8_grouped_matmul(const farn_ctx* ctx, const void* x, const float* x_s
                             void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
   if (!ctx || workspace_bytes < 0 || n_rows < 0 || n_rows > 0x7FFFFFFF || !sizes_ok(n_slots, N, H) || E < 1 ||
       E > FARN_MAX_EXPERTS || !product_fits(n_rows, 2 * H) || !product_fits(2 * N * H, E) ||
-      (!rows && n_rows != n_slots))
+      (!rows && n_slots > 0 && n_rows != n_slots))
     return FARN_ERR_INVALID_ARG;
   if (n_slots == 0) return FARN_OK;
   if ((n_rows > 0 && (!x || !x_scale)) || !weights || !w_scale || !offsets || !out)
