@@ -85,8 +85,17 @@ __device__ __forceinline__ uint64_t turn_step(float freq) {
   return (b >> 31) ? 0ull - f : f;
 }
 __device__ __forceinline__ void sincos_at(int32_t pos, uint64_t step, float* s, float* c) {
-  const int32_t top = (int32_t)(uint32_t)(((uint64_t)(int64_t)pos * step) >> 32);
-  sincospif((float)top * 4.656612873077393e-10f, s, c);        // 2^-31 half turns
+  // The place in the turn: the nearest quarter, and what is left in fp32, at most
+  // an eighth of a turn (a whole turn's place in 24 bits would be off four times
+  // as far).
+  const uint32_t top = (uint32_t)(((uint64_t)(int64_t)pos * step) >> 32);
+  const uint32_t quarter = (top + 0x20000000u) >> 30;
+  const int32_t left = (int32_t)(top - (quarter << 30));
+  float a, b;
+  sincospif((float)left * 4.656612873077393e-10f, &a, &b);       // 2^-31 half turns
+  const float u = quarter & 1u ? b : a, v = quarter & 1u ? a : b;
+  *s = quarter & 2u ? -u : u;
+  *c = (quarter + 1u) & 2u ? -v : v;
 }
 __device__ __forceinline__ int axis_of(const HeadsParams& p, int pair) {
   int a = 0;
@@ -222,7 +231,7 @@ __device__ __forceinline__ void run_role(const HeadsParams& p, int64_t t, int lo
         for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
         for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        const float rstd = rsqrtf(fmaf(ss, inv_d, p.eps));
+        const float rstd = __frsqrt_rn(fmaf(ss, inv_d, p.eps));
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = (x[e] * rstd) * w[e];
       }

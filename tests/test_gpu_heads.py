@@ -455,9 +455,8 @@ def test_cache_beyond_4_gib(dev, ctxs, which, fmt):
     (9, 3, 1, 256, 256, 1, False), (7, 2, 1, 272, 32, 1, False), (5, 3, 2, 128, 0, 1, False),
     (11, 1, 2, 48, 48, 1, False)])
 def test_heads_to_cache(O, dev, ctxs, which, fmt, T, HQ, HK, D, R, axes, interleaved):
-    """Queries as in the call that writes bf16; values' bits as kv_write's; keys'
-    codes are those of the 64-bit values or, where the roundings of fp32 reach a
-    border between two codes, a neighbour's."""
+    """Values' bits as kv_write's; keys' codes are those of the 64-bit values or,
+    where the roundings of fp32 reach a border between two codes, a neighbour's."""
     q, k, wq, wk, pos, fr, sect = case_inputs(dev, T, HQ, HK, D, R, axes, 40 + T)
     v = normal(dev, (T, HK, D), 41)
     c = empty(dev, fmt, T + 4, 1, HK, D)
@@ -467,8 +466,7 @@ def test_heads_to_cache(O, dev, ctxs, which, fmt, T, HQ, HK, D, R, axes, interle
     live = slots >= 0
     got = farn.qk_norm_rope_cache(q, k, v, wq, wk, 1e-5, pos, fr, c, slots, scales_arg(fmt), sect,
                                   interleaved, ctx=ctxs[which])
-    plain, _ = farn.qk_norm_rope(q, k, wq, wk, 1e-5, pos, fr, sect, interleaved, ctx=ctxs[which])
-    assert torch.equal(got, plain)
+    check_heads(got, *heads_reference(q, wq, 1e-5, pos, fr, sect, interleaved))
     at = slots[live].long()
     other = empty(dev, fmt, T + 4, 1, HK, D)
     farn.kv_write(k, v, other, slots, tensor_scales=scales_arg(fmt))
