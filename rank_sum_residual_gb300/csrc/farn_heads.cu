@@ -37,7 +37,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 4;             // rows per lane group whose loads are in flight
-constexpr int kCtas = 8;              // per SM
+constexpr int kCtas = 7;              // per SM
 constexpr int kMaxDim = 1024;
 constexpr int kMaxAxes = 4;
 
