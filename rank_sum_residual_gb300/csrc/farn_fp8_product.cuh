@@ -103,27 +103,47 @@ struct Fp8One {
   static constexpr int kPartBytes = kF8Adders * kTurnBytes;
 };
 
-// A warp's wait as tc_wait_warp, with a short way for a phase that is complete:
-// the general one takes 150 to 200 cycles even then.
-// The first half of a wait: asks without looking at the answer, so that other
-// instructions fill the time until it is there.
+// What a wait orders.  kOwn: the CTA's own threads (and TMA, and the matrix
+// instructions) arrive on the barrier.  kCluster: another CTA of the pair too, and
+// what it did to shared memory is ordered before what follows.  kTensor: tensor
+// memory alone is handed over, which the tcgen05 fences on both sides order: the
+// arrivals and the wait are relaxed, at the cluster's scope.
+enum Fp8Wait { kOwn, kCluster, kTensor };
+
+// A warp's wait as tc_wait_warp, with a short way for a phase that is complete (the
+// general one takes 150 to 200 cycles even then), in two halves: the first asks
+// without looking at the answer, so that other instructions fill the time until
+// it is there.
+template <Fp8Wait WHAT>
 __device__ __forceinline__ uint32_t f8_ask(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  if constexpr (WHAT == kTensor)
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  else if constexpr (WHAT == kCluster)
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok;
 }
+template <Fp8Wait WHAT>
 __device__ __forceinline__ bool f8_answer(uint32_t ok, uint32_t bar, uint32_t parity,
                                           volatile int* abort_flag, int* err, int code) {
   if (__all_sync(0xFFFFFFFFu, ok)) return true;
-  return tc_wait_warp<false>(bar, parity, abort_flag, err, code);
+  return tc_wait_warp<WHAT != kOwn>(bar, parity, abort_flag, err, code);
 }
-
+template <Fp8Wait WHAT>
 __device__ __forceinline__ bool f8_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                         int* err, int code) {
-  return f8_answer(f8_ask(bar, parity), bar, parity, abort_flag, err, code);
+  return f8_answer<WHAT>(f8_ask<WHAT>(bar, parity), bar, parity, abort_flag, err, code);
 }
 
 // Arrive on the first CTA's barrier for reads of tensor memory that are done
@@ -273,10 +293,6 @@ __device__ __forceinline__ void drain_stages(uint32_t full, uint32_t armed, uint
 // CTA r of a pair has the tile's slots r * 128 .. + 127 (the lanes of its tensor
 // memory) and brings, of each half of the weights, the rows r * 64 .. + 63.
 //
-// The barriers of this kernel are signalled by TMA and by the matrix
-// instructions' commits, or (acc_empty) carry no ordinary memory: their waits
-// acquire at the CTA's scope, as a wait at the cluster's takes 190 cycles.
-//
 // Gathered rows have been copied one after the other before (see
 // fp8_gather_kernel); p.rows then only says which of the slots have a row.
 __global__ void __launch_bounds__(Fp8Pair::kWarps * 32, 1)
@@ -364,14 +380,14 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
       const bool used = has_half(w, half);
       uint32_t v[2][32];
       if (used) {
-        ok = f8_wait(m.afull + at, phase, abort_flag, p.err, kErrTcTile);
+        ok = f8_wait<kTensor>(m.afull + at, phase, abort_flag, p.err, kErrTcTile);
         if (!ok) break;
         tc::fence_after();
         tc::tmem_ld32(sums, v[0]);
       }
       for (int c0 = 0; ok && c0 < nc; c0 += kF8ScaleBlocks, ++ng) {
         const uint32_t slot = ng % kF8ScaleSlots;
-        ok = f8_wait(m.sfull + 8 * slot, ng / kF8ScaleSlots & 1, abort_flag, p.err, kErrTcFull);
+        ok = f8_wait<kOwn>(m.sfull + 8 * slot, ng / kF8ScaleSlots & 1, abort_flag, p.err, kErrTcFull);
         if (!ok) break;
         const float4 f = factors[slot * (Sh::kScaleSlot / 16)];
         __syncwarp();
@@ -400,12 +416,12 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
           // its first sums are on their way while the last of this one are added
           const bool more = c0 + j + 1 < nc;
           uint32_t asked = 1;
-          if (more) asked = f8_ask(m.afull + at, phase);
+          if (more) asked = f8_ask<kTensor>(m.afull + at, phase);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             acc[96 + i] = fmaf(__uint_as_float(v[1][i]), s, acc[96 + i]);
           if (more) {
-            ok = f8_answer(asked, m.afull + at, phase, abort_flag, p.err, kErrTcTile);
+            ok = f8_answer<kTensor>(asked, m.afull + at, phase, abort_flag, p.err, kErrTcTile);
             if (!ok) break;
             tc::fence_after();
             tc::tmem_ld32(sums, v[0]);
@@ -448,7 +464,7 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
       const int n0 = w.wt * Sh::kTileWeights + w_rank * 64;
       for (int c = 0; c < nc; ++c, at.next(NS), ++armed) {
         const uint32_t s = at.stage;
-        ok = f8_wait(m.empty + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
+        ok = f8_wait<kCluster>(m.empty + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
         if (!ok) break;
         const uint32_t to = m.base + s * Sh::kStageBytes;
         if (tc::elect_one()) {
@@ -483,11 +499,11 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
         const bool used = has_half(w, h);
         for (int c = 0; c < nc; ++c, at.next(NS)) {
           const uint32_t s = at.stage;
-          ok = f8_wait(m.full + 8 * s, at.phase, abort_flag, p.err, kErrTcFull);
+          ok = f8_wait<kCluster>(m.full + 8 * s, at.phase, abort_flag, p.err, kErrTcFull);
           if (!ok) break;
           if (used) {
             const uint32_t b = nb & 1, bar = (b * 2 + h) * 8;
-            ok = f8_wait(m.aempty + bar, ((nb >> 1) & 1) ^ 1, abort_flag, p.err, kErrTcTile);
+            ok = f8_wait<kTensor>(m.aempty + bar, ((nb >> 1) & 1) ^ 1, abort_flag, p.err, kErrTcTile);
             if (!ok) break;
             tc::fence_after();
             const uint64_t da = desc0 + (s * Sh::kStageBytes >> 4);
@@ -534,7 +550,7 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
       }
       for (int c = 0; c < nc; c += kF8ScaleBlocks, ++ng) {
         const uint32_t slot = ng % kF8ScaleSlots;
-        ok = f8_wait(m.sempty + 8 * slot, (ng / kF8ScaleSlots & 1) ^ 1, abort_flag, p.err,
+        ok = f8_wait<kOwn>(m.sempty + 8 * slot, (ng / kF8ScaleSlots & 1) ^ 1, abort_flag, p.err,
                      kErrTcEmpty);
         if (!ok) break;
         float4* to = to0 + slot * (Sh::kScaleSlot / 16);
@@ -696,15 +712,15 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
       float acc[Sh::kWarpCols];
 #pragma unroll
       for (int i = 0; i < Sh::kWarpCols; ++i) acc[i] = 0.0f;
-      uint32_t asked = f8_ask(m.afull + 8 * buf, phase);
+      uint32_t asked = f8_ask<kOwn>(m.afull + 8 * buf, phase);
       for (int c = 0; ok && c < nc; ++ng) {
         const uint32_t slot = ng % kF8ScaleSlots;
-        ok = f8_wait(m.sfull + 8 * slot, ng / kF8ScaleSlots & 1, abort_flag, p.err, kErrTcFull);
+        ok = f8_wait<kOwn>(m.sfull + 8 * slot, ng / kF8ScaleSlots & 1, abort_flag, p.err, kErrTcFull);
         if (!ok) break;
         const int end = min(nc, c + kF8ScaleBlocks);
         const float* s = scales + slot * (Sh::kScaleSlot / 4);
         for (; c < end; ++c, s += Sh::kBn) {
-          ok = f8_answer(asked, m.afull + 8 * buf, phase, abort_flag, p.err, kErrTcTile);
+          ok = f8_answer<kOwn>(asked, m.afull + 8 * buf, phase, abort_flag, p.err, kErrTcTile);
           if (!ok) break;
           tc::fence_after();
           const uint32_t d = sums + buf * Sh::kBn, bar = m.aempty + 8 * buf;
@@ -713,7 +729,7 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
           for (int q = 0; q < Sh::kWarpCols / 16; ++q)
             if (q * 16 < mine) tc::tmem_ld16(d + q * 16, v[q]);
           if (++buf == Sh::kBufs) { buf = 0; phase ^= 1; }
-          if (c + 1 < nc) asked = f8_ask(m.afull + 8 * buf, phase);
+          if (c + 1 < nc) asked = f8_ask<kOwn>(m.afull + 8 * buf, phase);
           tc::tmem_ld_wait();
           tc::fence_before();       // orders the reads of tensor memory before the arrival
           __syncwarp();
@@ -813,7 +829,7 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
           Sh::kABytes + (GATHER ? 0 : (filled(w) + kF8Box - 1) / kF8Box * kF8Box * kTcRowBytes);
       for (int c = c0; c < c1; ++c, at.next(NS), ++armed) {
         const uint32_t s = at.stage;
-        ok = f8_wait(m.empty + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
+        ok = f8_wait<kOwn>(m.empty + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
         if (!ok) break;
         if (tc::elect_one()) {
           mbar_arrive_expect_tx(m.full + 8 * s, bytes);
@@ -837,9 +853,9 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
       const uint32_t idesc = tc::idesc_e4m3(kTcWeights, filled(w));
       for (int c = 0; c < nc; ++c, at.next(NS)) {
         const uint32_t s = at.stage;
-        const uint32_t free = f8_ask(m.aempty + 8 * buf, phase ^ 1);
-        ok = f8_wait(m.full + 8 * s, at.phase, abort_flag, p.err, kErrTcFull) &&
-             f8_answer(free, m.aempty + 8 * buf, phase ^ 1, abort_flag, p.err, kErrTcTile);
+        const uint32_t free = f8_ask<kOwn>(m.aempty + 8 * buf, phase ^ 1);
+        ok = f8_wait<kOwn>(m.full + 8 * s, at.phase, abort_flag, p.err, kErrTcFull) &&
+             f8_answer<kOwn>(free, m.aempty + 8 * buf, phase ^ 1, abort_flag, p.err, kErrTcTile);
         if (!ok) break;
         tc::fence_after();
         const uint64_t da = desc0 + (s * Sh::kStageBytes >> 4), db = da + (Sh::kABytes >> 4);
@@ -880,7 +896,7 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
         const float4 vb = load_scales(sb, c, c1, vec);
         const float4 v[2] = {load_scales(row[0], c, c1, vec), load_scales(row[1], c, c1, vec)};
         const uint32_t slot = ng % kF8ScaleSlots;
-        ok = f8_wait(m.sempty + 8 * slot, (ng / kF8ScaleSlots & 1) ^ 1, abort_flag,
+        ok = f8_wait<kOwn>(m.sempty + 8 * slot, (ng / kF8ScaleSlots & 1) ^ 1, abort_flag,
                                  p.err, kErrTcEmpty);
         if (!ok) break;
         float* to = to0 + slot * (Sh::kScaleSlot / 4);
@@ -904,7 +920,7 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
       const Tile w = find_tile(g, p.E, tile, wts, Sh::kBn);
       for (int c = c0; c < c1; ++c, at.next(NS)) {
         const uint32_t s = at.stage;
-        ok = f8_wait(m.empty + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
+        ok = f8_wait<kOwn>(m.empty + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
         if (!ok) break;
         if (tc::elect_one()) {
 #pragma unroll
@@ -930,7 +946,7 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
       int c = c0 + ahead;
       for (; c < c1; c += kF8Gather, at.skip(kF8Gather, NS)) {
         const uint32_t s = at.stage;
-        ok = f8_wait(m.empty + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
+        ok = f8_wait<kOwn>(m.empty + 8 * s, at.phase ^ 1, abort_flag, p.err, kErrTcEmpty);
         if (!ok) break;
         rows.copy(p, m.base + s * Sh::kStageBytes + Sh::kABytes, c, filled(w), lane);
         __syncwarp();
