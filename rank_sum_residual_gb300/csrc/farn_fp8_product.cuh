@@ -103,6 +103,16 @@ struct Fp8One {
   static constexpr int kPartBytes = kF8Adders * kTurnBytes;
 };
 
+// d += v * s for two values each, s twice the same; one rounding per value.  (Single
+// multiply-adds took 1 to 2 % longer.)
+__device__ __forceinline__ void fma_pair(uint64_t& d, uint32_t v0, uint32_t v1, uint64_t s) {
+  asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}"
+      : "+l"(d) : "r"(v0), "r"(v1), "l"(s));
+}
+__device__ __forceinline__ uint64_t twice(float s) {
+  return ((uint64_t)__float_as_uint(s) << 32) | __float_as_uint(s);
+}
+
 // What a wait orders.  kOwn: the CTA's own threads (and TMA, and the matrix
 // instructions) arrive on the barrier.  kCluster: another CTA of the pair too, and
 // what it did to shared memory is ordered before what follows.  kTensor: tensor
@@ -110,40 +120,48 @@ struct Fp8One {
 // arrivals and the wait are relaxed, at the cluster's scope.
 enum Fp8Wait { kOwn, kCluster, kTensor };
 
-// A warp's wait as tc_wait_warp, with a short way for a phase that is complete (the
-// general one takes 150 to 200 cycles even then), in two halves: the first asks
-// without looking at the answer, so that other instructions fill the time until
-// it is there.
-template <Fp8Wait WHAT>
-__device__ __forceinline__ uint32_t f8_ask(uint32_t bar, uint32_t parity) {
+// Whether a phase is complete: test_wait (LOOK) says so at once, try_wait may let
+// the thread sleep first.
+template <Fp8Wait WHAT, bool LOOK>
+__device__ __forceinline__ uint32_t f8_phase(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  if constexpr (WHAT == kTensor)
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  else if constexpr (WHAT == kCluster)
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  else
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+#define FARN_F8_PHASE(form)                                                             \
+  asm volatile("{\n\t.reg .pred p;\n\t" form " p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" \
+               : "=r"(ok) : "r"(bar), "r"(parity) : "memory")
+  if constexpr (WHAT == kTensor) {
+    if constexpr (LOOK) FARN_F8_PHASE("mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64");
+    else FARN_F8_PHASE("mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64");
+  } else if constexpr (WHAT == kCluster) {
+    if constexpr (LOOK) FARN_F8_PHASE("mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64");
+    else FARN_F8_PHASE("mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64");
+  } else {
+    if constexpr (LOOK) FARN_F8_PHASE("mbarrier.test_wait.parity.shared::cta.b64");
+    else FARN_F8_PHASE("mbarrier.try_wait.parity.shared::cta.b64");
+  }
+#undef FARN_F8_PHASE
   return ok;
 }
-template <Fp8Wait WHAT>
-__device__ __forceinline__ bool f8_answer(uint32_t ok, uint32_t bar, uint32_t parity,
-                                          volatile int* abort_flag, int* err, int code) {
-  if (__all_sync(0xFFFFFFFFu, ok)) return true;
-  return tc_wait_warp<WHAT != kOwn>(bar, parity, abort_flag, err, code);
-}
+
+// A warp's wait as tc_wait_warp, with a short way for a phase that is complete:
+// the general one takes 150 to 200 cycles even then.
 template <Fp8Wait WHAT>
 __device__ __forceinline__ bool f8_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                         int* err, int code) {
-  return f8_answer<WHAT>(f8_ask<WHAT>(bar, parity), bar, parity, abort_flag, err, code);
+  if (__all_sync(0xFFFFFFFFu, f8_phase<WHAT, false>(bar, parity))) return true;
+  return tc_wait_warp<WHAT != kOwn>(bar, parity, abort_flag, err, code);
+}
+// The same in two halves: a look ahead, whose answer is not needed yet, and the
+// wait that it may save.  (A try_wait in place of the look held up what stood
+// between the two: 8192^3 421 us instead of 415.)
+template <Fp8Wait WHAT>
+__device__ __forceinline__ uint32_t f8_look(uint32_t bar, uint32_t parity) {
+  return f8_phase<WHAT, true>(bar, parity);
+}
+template <Fp8Wait WHAT>
+__device__ __forceinline__ bool f8_answer(uint32_t looked, uint32_t bar, uint32_t parity,
+                                          volatile int* abort_flag, int* err, int code) {
+  if (__all_sync(0xFFFFFFFFu, looked)) return true;
+  return f8_wait<WHAT>(bar, parity, abort_flag, err, code);
 }
 
 // Arrive on the first CTA's barrier for reads of tensor memory that are done
@@ -180,14 +198,16 @@ __device__ __forceinline__ float4 load_scales(const float* row, int c, int end, 
 // shared memory (rows of 80 bytes: 16-byte accesses without bank conflicts) and
 // written in runs of 64 bytes.  rows: those that exist; col: the first column.
 __device__ __forceinline__ void store_rows(const ProductParams& p, int store_bytes,
-                                           const float* acc, bool live, uint32_t* turn,
+                                           const uint64_t* acc, bool live, uint32_t* turn,
                                            int64_t slot, int rows, int64_t col, int lane) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      w[i] = live ? pack_bf16x2(acc[j * 8 + 2 * i], acc[j * 8 + 2 * i + 1]) : 0u;
+      w[i] = live ? pack_bf16x2(__uint_as_float((uint32_t)acc[j * 4 + i]),
+                                __uint_as_float((uint32_t)(acc[j * 4 + i] >> 32)))
+                  : 0u;
     *reinterpret_cast<uint4*>(turn + lane * 20 + j * 4) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __syncwarp();
@@ -374,9 +394,9 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
     bool ok = true;
     for (int32_t tile = t0; ok && tile < tiles; tile += tstep) {
       const Tile w = find_tile(g, p.E, tile, wts, Sh::kBn);
-      float acc[Sh::kHalf];
+      uint64_t acc[Sh::kHalf / 2];
 #pragma unroll
-      for (int i = 0; i < Sh::kHalf; ++i) acc[i] = 0.0f;
+      for (int i = 0; i < Sh::kHalf / 2; ++i) acc[i] = 0ull;
       const bool used = has_half(w, half);
       uint32_t v[2][32];
       if (used) {
@@ -396,14 +416,14 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
 #pragma unroll
         for (int j = 0; j < kF8ScaleBlocks; ++j) {
           if (c0 + j >= nc) break;
-          const float s = j == 0 ? f.x : j == 1 ? f.y : j == 2 ? f.z : f.w;
+          const uint64_t s = twice(j == 0 ? f.x : j == 1 ? f.y : j == 2 ? f.z : f.w);
 #pragma unroll
           for (int q = 0; q < 3; ++q) {
             tc::tmem_ld_wait();
             tc::tmem_ld32(sums + (q + 1) * 32, v[(q + 1) & 1]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              acc[q * 32 + i] = fmaf(__uint_as_float(v[q & 1][i]), s, acc[q * 32 + i]);
+            for (int i = 0; i < 16; ++i)
+              fma_pair(acc[q * 16 + i], v[q & 1][2 * i], v[q & 1][2 * i + 1], s);
           }
           tc::tmem_ld_wait();
           tc::fence_before();       // orders the reads of tensor memory before the arrival
@@ -415,20 +435,18 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
           phase ^= (at >> 4 & 1) ^ 1;
           // its first sums are on their way while the last of this one are added
           const bool more = c0 + j + 1 < nc;
-          uint32_t asked = 1;
-          if (more) asked = f8_ask<kTensor>(m.afull + at, phase);
+          uint32_t looked = 1;
+          if (more) looked = f8_look<kTensor>(m.afull + at, phase);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            acc[96 + i] = fmaf(__uint_as_float(v[1][i]), s, acc[96 + i]);
+          for (int i = 0; i < 8; ++i) fma_pair(acc[48 + i], v[1][2 * i], v[1][2 * i + 1], s);
           if (more) {
-            ok = f8_answer<kTensor>(asked, m.afull + at, phase, abort_flag, p.err, kErrTcTile);
+            ok = f8_answer<kTensor>(looked, m.afull + at, phase, abort_flag, p.err, kErrTcTile);
             if (!ok) break;
             tc::fence_after();
             tc::tmem_ld32(sums, v[0]);
           }
 #pragma unroll
-          for (int i = 16; i < 32; ++i)
-            acc[96 + i] = fmaf(__uint_as_float(v[1][i]), s, acc[96 + i]);
+          for (int i = 8; i < 16; ++i) fma_pair(acc[48 + i], v[1][2 * i], v[1][2 * i + 1], s);
         }
       }
       if (!ok) break;
@@ -443,7 +461,7 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          store_rows(p, t.store_bytes, acc + q * 32, live, turn, slot, rows, n0 + q * 32, lane);
+          store_rows(p, t.store_bytes, acc + q * 16, live, turn, slot, rows, n0 + q * 32, lane);
       }
     }
   } else if (warp == 8) {
@@ -712,7 +730,7 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
       float acc[Sh::kWarpCols];
 #pragma unroll
       for (int i = 0; i < Sh::kWarpCols; ++i) acc[i] = 0.0f;
-      uint32_t asked = f8_ask<kOwn>(m.afull + 8 * buf, phase);
+      uint32_t looked = f8_look<kOwn>(m.afull + 8 * buf, phase);
       for (int c = 0; ok && c < nc; ++ng) {
         const uint32_t slot = ng % kF8ScaleSlots;
         ok = f8_wait<kOwn>(m.sfull + 8 * slot, ng / kF8ScaleSlots & 1, abort_flag, p.err, kErrTcFull);
@@ -720,7 +738,7 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
         const int end = min(nc, c + kF8ScaleBlocks);
         const float* s = scales + slot * (Sh::kScaleSlot / 4);
         for (; c < end; ++c, s += Sh::kBn) {
-          ok = f8_answer<kOwn>(asked, m.afull + 8 * buf, phase, abort_flag, p.err, kErrTcTile);
+          ok = f8_answer<kOwn>(looked, m.afull + 8 * buf, phase, abort_flag, p.err, kErrTcTile);
           if (!ok) break;
           tc::fence_after();
           const uint32_t d = sums + buf * Sh::kBn, bar = m.aempty + 8 * buf;
@@ -729,7 +747,7 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
           for (int q = 0; q < Sh::kWarpCols / 16; ++q)
             if (q * 16 < mine) tc::tmem_ld16(d + q * 16, v[q]);
           if (++buf == Sh::kBufs) { buf = 0; phase ^= 1; }
-          if (c + 1 < nc) asked = f8_ask<kOwn>(m.afull + 8 * buf, phase);
+          if (c + 1 < nc) looked = f8_look<kOwn>(m.afull + 8 * buf, phase);
           tc::tmem_ld_wait();
           tc::fence_before();       // orders the reads of tensor memory before the arrival
           __syncwarp();
@@ -853,7 +871,7 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
       const uint32_t idesc = tc::idesc_e4m3(kTcWeights, filled(w));
       for (int c = 0; c < nc; ++c, at.next(NS)) {
         const uint32_t s = at.stage;
-        const uint32_t free = f8_ask<kOwn>(m.aempty + 8 * buf, phase ^ 1);
+        const uint32_t free = f8_look<kOwn>(m.aempty + 8 * buf, phase ^ 1);
         ok = f8_wait<kOwn>(m.full + 8 * s, at.phase, abort_flag, p.err, kErrTcFull) &&
              f8_answer<kOwn>(free, m.aempty + 8 * buf, phase ^ 1, abort_flag, p.err, kErrTcTile);
         if (!ok) break;

@@ -27,7 +27,7 @@ def test_blocks_have_started_before_their_memory_is_touched():
 
 
 def waits(body):
-    return re.findall(r"f8_(?:ask|wait|answer)<(\w+)>\(\s*(?:\w+,\s*)?m\.(\w+)", body)
+    return re.findall(r"f8_(?:look|wait|answer)<(\w+)>\(\s*(?:\w+,\s*)?m\.(\w+)", body)
 
 
 def test_waits_say_what_they_order():
