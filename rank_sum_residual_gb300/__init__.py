@@ -12,7 +12,10 @@ functions have the C names and arguments and only marshal them through
 ctypes; ``forward`` is the same call for torch tensors.  Next to it stand
 the operators of an expert layer and of NVFP4 projections that its outputs
 go through: ``moe_route``, ``grouped_matmul`` and ``moe_combine``;
-``nvfp4_quantize``, ``nvfp4_dequantize`` and ``nvfp4_matmul``.  Every
+``nvfp4_quantize``, ``nvfp4_dequantize`` and ``nvfp4_matmul``;
+``fp8_quantize``, ``fp8_matmul`` and ``fp8_grouped_matmul``; and those of the
+attention half up to the cache, ``qk_norm_rope``, ``qk_norm_rope_cache``,
+``kv_write`` and ``kv_read``.  Every
 arithmetic step runs in the CUDA kernels.  There is no CPU fallback: if the library
 is not built, every call raises.
 """
@@ -137,7 +140,7 @@ def _load():
                                                      cvp, cvp, pi, pi, pi]
         lib.farn_plan_fp8_grouped_matmul.restype = i32
         lib.farn_fp8_grouped_matmul.restype = i32
-        pc = ctypes.POINTER(KvCache)
+        pc = vp     # a KvCache by reference, of whichever load of this module
         rope = [cvp, cvp, f32, cvp, i32, pi, cvp, i32, i32]
         lib.farn_qk_norm_rope.argtypes = [vp, i64, i32, cvp, i32, i64, cvp, i32, i64, *rope, vp,
                                           i64, vp, i64, vp]
@@ -1428,7 +1431,7 @@ def _qk_cache_args(q, k, v, q_weight, k_weight, eps, positions, freqs, cache, sl
     return (c.handle, T, D, q.data_ptr(), HQ, q_stride, k.data_ptr(), k_stride, v.data_ptr(),
             v_stride, HK, _weight_arg(q_weight, "q_weight", D, index, dev),
             _weight_arg(k_weight, "k_weight", D, index, dev), eps, pos, axes, sect, fr, R,
-            1 if interleaved else 0, out.data_ptr(), qs, store, slots_at,
+            1 if interleaved else 0, out.data_ptr(), qs, ctypes.byref(store), slots_at,
             _raw_stream(stream, index)), out, c
 
 
@@ -1465,8 +1468,8 @@ def _kv_write_args(k, v, cache, slots, tensor_scales, ctx, stream):
     slots_at = _slots_arg(slots, T, index, dev)
     store = _cache_of(cache, tensor_scales, index, dev, HK, D)
     c = _context_of(ctx, index)
-    return (c.handle, T, k.data_ptr(), k_stride, v.data_ptr(), v_stride, store, slots_at,
-            _raw_stream(stream, index)), c
+    return (c.handle, T, k.data_ptr(), k_stride, v.data_ptr(), v_stride, ctypes.byref(store),
+            slots_at, _raw_stream(stream, index)), c
 
 
 def prepare_kv_write(k, v, cache, slots, tensor_scales=None, ctx=None, stream=None):
@@ -1514,7 +1517,7 @@ def _kv_read_args(cache, table, offsets, n_tokens, tensor_scales, out, ctx, stre
         _check_tensor(out[0], "the output of k", shape, dev)
         _check_tensor(out[1], "the output of v", shape, dev)
     c = _context_of(ctx, index)
-    return (c.handle, store, table.data_ptr(), B, width, offsets.data_ptr(), n,
+    return (c.handle, ctypes.byref(store), table.data_ptr(), B, width, offsets.data_ptr(), n,
             out[0].data_ptr(), out[1].data_ptr(), _raw_stream(stream, index)), out, c
 
 
