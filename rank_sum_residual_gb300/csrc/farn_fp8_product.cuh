@@ -355,13 +355,16 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
     tc::prefetch_map(&map_w);
     tc::prefetch_map(&map_x);
   }
-  pdl_wait();
-  pdl_trigger();
-  load_groups(g, p, Sh::kBn);       // ends with a block barrier
+  // What does not depend on the kernel before comes before the wait for it: the
+  // groups too, unless they are in memory (it took a microsecond behind the wait).
+  if (!p.offsets) load_groups(g, p, Sh::kBn);
   tc::fence_before();
   tc::cluster_sync();
   tc::fence_after();
   const uint32_t tmem = uniform(m.bb->tmem);
+  pdl_wait();
+  pdl_trigger();
+  if (p.offsets) load_groups(g, p, Sh::kBn);       // ends with a block barrier
   const int wts = (int)((p.N + Sh::kTileWeights - 1) / Sh::kTileWeights);
   const int32_t tiles = g.tile[p.E] * wts;
   const int32_t t0 = blockIdx.x / 2, tstep = gridDim.x / 2;
@@ -694,13 +697,14 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
     tc::prefetch_map(&map_w);
     if constexpr (!GATHER) tc::prefetch_map(&map_x);
   }
-  pdl_wait();
-  pdl_trigger();
-  load_groups(g, p, Sh::kBn);       // ends with a block barrier
+  if (!p.offsets) load_groups(g, p, Sh::kBn);      // as in the pair
   tc::fence_before();
   if (csize > 1) tc::cluster_sync(); else __syncthreads();
   tc::fence_after();
   const uint32_t tmem = uniform(m.bb->tmem);
+  pdl_wait();
+  pdl_trigger();
+  if (p.offsets) load_groups(g, p, Sh::kBn);
 
   const int wts = (int)((p.N + Sh::kTileWeights - 1) / Sh::kTileWeights);
   const int32_t tiles = g.tile[p.E] * wts;
