@@ -93,6 +93,7 @@ bool fit(const farn_ctx* ctx, const Kind* k, int E, int ks, Plan* pl) {
 // 28.7, 35.2, 30.1; 128 x 10240 x 5120 27.4, 30.7, 35.8, 22.9; 400 x 8192 x 2048
 // 19.9, 35.9, 57.9, 14.2; 700 x 1000 x 8192 22.2, 27.3, 26.5, 29.7; 64 experts of 64
 // slots 2048 -> 4096 114, 235, 392, 126, of 250 4096 -> 2048 353, 517, 757, 183.
+//
 // can_copy: gathered rows can be laid side by side first, as the pair needs them.
 bool plan_tc(const farn_ctx* ctx, const ProductParams& p, bool can_copy, Plan* pl) {
   const bool gather = p.rows != nullptr;
@@ -401,8 +402,9 @@ int farn_fp8_grouped_matmul(const farn_ctx* ctx, const void* x, const float* x_s
                             const void* weights, const float* w_scale, int E,
                             const int32_t* offsets, int64_t N, int64_t H, void* out,
                             void* workspace, int64_t workspace_bytes, cudaStream_t stream) {
-  if (!ctx || workspace_bytes < 0 || n_rows < 0 || n_rows > 0x7FFFFFFF || !sizes_ok(n_slots, N, H) || E < 1 ||
-      E > FARN_MAX_EXPERTS || !product_fits(n_rows, 2 * H) || !product_fits(2 * N * H, E) ||
+  if (!ctx || workspace_bytes < 0 || n_rows < 0 || n_rows > 0x7FFFFFFF ||
+      !sizes_ok(n_slots, N, H) || E < 1 || E > FARN_MAX_EXPERTS ||
+      !product_fits(n_rows, 2 * H) || !product_fits(2 * N * H, E) ||
       (!rows && n_slots > 0 && n_rows != n_slots))
     return FARN_ERR_INVALID_ARG;
   if (n_slots == 0) return FARN_OK;

@@ -410,7 +410,8 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
       }
       for (int c0 = 0; ok && c0 < nc; c0 += kF8ScaleBlocks, ++ng) {
         const uint32_t slot = ng % kF8ScaleSlots;
-        ok = f8_wait<kOwn>(m.sfull + 8 * slot, ng / kF8ScaleSlots & 1, abort_flag, p.err, kErrTcFull);
+        ok = f8_wait<kOwn>(m.sfull + 8 * slot, ng / kF8ScaleSlots & 1, abort_flag, p.err,
+                           kErrTcFull);
         if (!ok) break;
         const float4 f = factors[slot * (Sh::kScaleSlot / 16)];
         __syncwarp();
@@ -524,7 +525,8 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
           if (!ok) break;
           if (used) {
             const uint32_t b = nb & 1, bar = (b * 2 + h) * 8;
-            ok = f8_wait<kTensor>(m.aempty + bar, ((nb >> 1) & 1) ^ 1, abort_flag, p.err, kErrTcTile);
+            ok = f8_wait<kTensor>(m.aempty + bar, ((nb >> 1) & 1) ^ 1, abort_flag, p.err,
+                                  kErrTcTile);
             if (!ok) break;
             tc::fence_after();
             const uint64_t da = desc0 + (s * Sh::kStageBytes >> 4);
@@ -612,9 +614,10 @@ farn_fp8_pair_kernel(const __grid_constant__ Fp8Params t,
 // ------------------------------------------------------- rows side by side
 // The rows of a long call's slots and their scales, copied to where `pair`
 // reads them with TMA: every row is read once here instead of once for every 256
-// weights there, by threads (copied by the tile's own warps, 4096 tokens of 8
-// experts, 7168 -> 4096, took 1557 us; without a copy to make 855).  A slot without
-// a row gets zeros.  16 bytes of a row per thread and step; a warp per slot.
+// weights there.  (4096 tokens of 8 experts, 7168 -> 4096: 912 us, 844 of them the
+// product; with the rows copied by the tile's own warps 1557, fetched by TMA four
+// rows to an instruction from the tile's own order 2360.)  A slot without a row gets
+// zeros.  16 bytes of a row per thread and step; a warp per slot.
 struct Fp8GatherParams {
   const uint8_t* x;
   const float* x_scale;
@@ -737,7 +740,8 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
       uint32_t looked = f8_look<kOwn>(m.afull + 8 * buf, phase);
       for (int c = 0; ok && c < nc; ++ng) {
         const uint32_t slot = ng % kF8ScaleSlots;
-        ok = f8_wait<kOwn>(m.sfull + 8 * slot, ng / kF8ScaleSlots & 1, abort_flag, p.err, kErrTcFull);
+        ok = f8_wait<kOwn>(m.sfull + 8 * slot, ng / kF8ScaleSlots & 1, abort_flag, p.err,
+                           kErrTcFull);
         if (!ok) break;
         const int end = min(nc, c + kF8ScaleBlocks);
         const float* s = scales + slot * (Sh::kScaleSlot / 4);
@@ -1033,7 +1037,8 @@ farn_fp8_product_plain_kernel(const Fp8Params t) {
             va = e4m3_to_f32(static_cast<const uint8_t*>(p.a)[at * p.H + h]);
         }
         if (h < p.H && n0 + r < p.N)
-          vb = e4m3_to_f32(static_cast<const uint8_t*>(p.b)[((int64_t)w.e * p.N + n0 + r) * p.H + h]);
+          vb = e4m3_to_f32(
+              static_cast<const uint8_t*>(p.b)[((int64_t)w.e * p.N + n0 + r) * p.H + h]);
         as[k][r] = va;
         bs[k][r] = vb;
       }

@@ -189,7 +189,8 @@ struct Turn {
 // FMT: the cache's format, or 0: keys go to out[1].  HALF: pairs lie in halves.
 // The code is about instructions: with roles, layouts and addresses worked out
 // per row 8192 tokens of 40 and 8 heads of 128 took 77 us, 260 instructions to a
-// pass, two thirds of the issue slots.
+// pass, two thirds of the issue slots; it takes 47.  (One loop for all roles: 50;
+// the rows brought ahead of the warps through shared memory: 62.)
 template <int ROLE, int L, int FMT, bool HALF>
 __device__ __forceinline__ void run_role(const HeadsParams& p, int64_t t, int lo, int hi, int l,
                                          int sub, const uint2* weight, const Turn& turn,
@@ -459,7 +460,8 @@ __device__ __forceinline__ Piece<FMT> load_piece(const ReadParams& p, int which,
     r.scale = __ldg(static_cast<const float*>(p.cache.scale[which]) + slot * p.heads +
                     head);
   } else {
-    r.codes.x = __ldg(reinterpret_cast<const uint32_t*>(p.cache.codes[which] + (slot * row + e) / 2));
+    r.codes.x =
+        __ldg(reinterpret_cast<const uint32_t*>(p.cache.codes[which] + (slot * row + e) / 2));
     r.codes.y = 0u;
     r.scale = __uint_as_float(
         (uint32_t)__ldg(static_cast<const uint8_t*>(p.cache.scale[which]) + (slot * row + e) / 16));
@@ -472,7 +474,8 @@ __device__ __forceinline__ uint4 piece_values(const ReadParams& p, int which, co
   if constexpr (FMT == FARN_CACHE_FP8) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = farn::e4m3x2_to_f32(((i < 2 ? r.codes.x : r.codes.y) >> (16 * (i & 1))) & 0xFFFFu);
+      const uint32_t two = (i < 2 ? r.codes.x : r.codes.y) >> (16 * (i & 1)) & 0xFFFFu;
+      const float2 f = farn::e4m3x2_to_f32(two);
       x[2 * i] = f.x * r.scale;
       x[2 * i + 1] = f.y * r.scale;
     }
@@ -786,7 +789,8 @@ int run_heads(const farn_ctx* ctx, int64_t T, int D, const void* const in[3], co
   for (int i = 0; i < 2; ++i)
     outs[i] = Rows{heads[i] && (i == 0 || !cache) ? out[i] : nullptr, out_stride[i] * 2,
                    (int64_t)heads[i] * D * 2, T};
-  const Span reads[5] = {{heads[0] ? weight[0] : nullptr, D * 2}, {heads[1] ? weight[1] : nullptr, D * 2},
+  const Span reads[5] = {{heads[0] ? weight[0] : nullptr, D * 2},
+                         {heads[1] ? weight[1] : nullptr, D * 2},
                          {R ? positions : nullptr, (R ? axes : 0) * T * 4},
                          {R ? freqs : nullptr, R * 2}, {cache ? slots : nullptr, T * 4}};
   for (int o = 0; o < 2; ++o) {
@@ -833,7 +837,8 @@ int run_heads(const farn_ctx* ctx, int64_t T, int D, const void* const in[3], co
   p.freqs = freqs;
   p.T = T;
   p.slots = slots;
-  return launch_heads(ctx, p, cache ? cache->format : 0, !cache || cache_aligned(cache, true), stream);
+  return launch_heads(ctx, p, cache ? cache->format : 0, !cache || cache_aligned(cache, true),
+                      stream);
 }
 
 }  // namespace
