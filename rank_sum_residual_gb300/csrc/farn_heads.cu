@@ -901,7 +901,8 @@ int farn_kv_read(const farn_ctx* ctx, const farn_kv_cache* cache, const int32_t*
       n_tokens > 0x7FFFFFFF)
     return FARN_ERR_INVALID_ARG;
   const int64_t row = (int64_t)cache->heads * cache->head_dim;
-  if (!product_fits(n_tokens, row * 2)) return FARN_ERR_INVALID_ARG;
+  if (!product_fits(n_tokens, row * 2) || !product_fits(width, (int64_t)B * 4))
+    return FARN_ERR_INVALID_ARG;
   if (row >= (1 << 26)) return FARN_ERR_UNSUPPORTED;
   if (n_tokens == 0 || B == 0) return FARN_OK;
   if ((width > 0 && !table) || !offsets || !k_out || !v_out || ((uintptr_t)table & 3u) ||

@@ -279,6 +279,14 @@ def test_read_refusals(ctx):
     assert read(ctx, cache=wide) == UNSUPPORTED
 
 
+def test_read_table_sizes(ctx):
+    """A table whose bytes do not fit 63 bits."""
+    most = (1 << 31) - 1
+    assert read(ctx, B=most, width=most) == INVALID
+    assert read(ctx, B=most, width=1 << 30, n_tokens=0) == OK
+    assert read(ctx, B=most, width=(1 << 30) + 1) == INVALID
+
+
 def test_null_context():
     farn.build_library()
     assert quantize(0) == product(0) == grouped(0) == rope(0) == to_cache(0) == write(0) == \
