@@ -1165,10 +1165,13 @@ def _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, workspac
         _check_tensor(workspace, "workspace", workspace.shape, x.device, (u8,))
     elif rows is not None and S > 64:       # shorter calls never lay rows side by side
         n = farn_fp8_grouped_workspace(c.handle, S, E, N, H)
-        if n:
+        if n and stream is None:
             workspace = torch.empty(n, dtype=u8, device=x.device)
-            if stream is not None:          # its memory is not given away before the call has run
-                workspace.record_stream(stream)
+        elif n:
+            # in the call's own stream's memory: the current stream may still be
+            # at work on what its own was before
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(n, dtype=u8, device=x.device)
     return (c.handle, x.data_ptr(), x_scale.data_ptr(), n_rows,
             None if rows is None else rows.data_ptr(), S, weights.data_ptr(), w_scale.data_ptr(),
             E, offsets.data_ptr(), N, H, out.data_ptr(),

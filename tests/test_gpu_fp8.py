@@ -457,6 +457,27 @@ def test_grouped_workspaces(dev, ctxs):
     assert (buf[:16] == 77).all() and (buf[16 + need:] == 77).all()
 
 
+def test_workspace_of_a_side_stream(dev, ctxs):
+    """A call on another stream takes no memory that the current stream's pending
+    work still reads."""
+    counts, N, H = [300, 500, 90], 256, 400
+    x, w, offsets, rows, S = group_inputs(dev, counts, N, H, True, whole, 66)
+    c, side = ctxs["pair"], torch.cuda.Stream()
+    need = farn.farn_fp8_grouped_workspace(c.handle, S, len(counts), N, H)
+    out = torch.empty(S, N, dtype=BF, device=dev)
+    kept = torch.empty(need, dtype=torch.uint8, device=dev)
+    torch.cuda.synchronize()
+    before = torch.full((need,), 77, dtype=torch.uint8, device=dev)
+    torch.cuda._sleep(100_000_000)
+    kept.copy_(before)
+    del before                                   # its block is free for the current stream
+    farn.fp8_grouped_matmul(*x, *w, offsets, rows, out=out, ctx=c, stream=side)
+    torch.cuda.synchronize()
+    assert (kept == 77).all()
+    want, _ = group_reference(x, w, offsets, rows, S)
+    assert torch.equal(out, to_bf16(want))
+
+
 @pytest.mark.parametrize("which", ALL)
 def test_grouped_without_rows_of_x(dev, ctxs, which):
     """x without rows: every slot's row is missing."""
