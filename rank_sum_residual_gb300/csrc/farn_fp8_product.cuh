@@ -806,7 +806,8 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
         ok = tc_wait_warp<true>(part_full, nt & 1, abort_flag, p.err, kErrTcJoin);
         if (!ok) break;
         // each CTA sums its share of the tile, four weights to a thread, the
-        // parts in rank order
+        // parts in rank order.  (Parts written to the CTA that sums them, rather
+        // than read by it, took longer: 1 x 4096 x 4096 8.3 us, 7.9 this way.)
         const uint32_t from = tc::smem_addr(part);
         const int quads = w.n * (kTcWeights / 4);
         uint16_t* out = static_cast<uint16_t*>(p.out);

@@ -190,7 +190,8 @@ struct Turn {
 // The code is about instructions: with roles, layouts and addresses worked out
 // per row 8192 tokens of 40 and 8 heads of 128 took 77 us, 260 instructions to a
 // pass, two thirds of the issue slots; it takes 47.  (One loop for all roles: 50;
-// the rows brought ahead of the warps through shared memory: 62.)
+// the rows brought ahead of the warps through shared memory: 62; a token's angles
+// shared by four warps: 55; four rows' sums joined together: 53, for the registers.)
 template <int ROLE, int L, int FMT, bool HALF>
 __device__ __forceinline__ void run_role(const HeadsParams& p, int64_t t, int lo, int hi, int l,
                                          int sub, const uint2* weight, const Turn& turn,
