@@ -18,6 +18,12 @@ attention half up to the cache, ``qk_norm_rope``, ``qk_norm_rope_cache``,
 ``kv_write`` and ``kv_read``.  Every
 arithmetic step runs in the CUDA kernels.  There is no CPU fallback: if the library
 is not built, every call raises.
+
+A call runs on torch's current stream, or on ``stream``, and waits for no other:
+its inputs have to be ready there, and to stay as they are until it has run.  What
+it makes itself on a given stream (outputs that are not given, a workspace) lies in
+that stream's memory; the outputs may be used on the stream that was current at the
+call, once that waits for it, and dropped at any time.
 """
 from __future__ import annotations
 
@@ -621,7 +627,7 @@ def prepare_forward(partials, residual, weight, eps: float, out=None, ctx=None, 
     import torch
     partials, T, H, dev, dtype = _partials_checked(partials, residual, weight)
     if out is None:
-        out = tuple(torch.empty((T, H), dtype=torch.bfloat16, device=dev) for _ in range(3))
+        out = _new(stream, dev, *[((T, H), torch.bfloat16)] * 3)
     for name, t in zip(("reduced", "residual_out", "norm_out"), out):
         _check_tensor(t, name, (T, H), dev)
     c, s = _ctx_stream(ctx, stream, dev)
@@ -664,11 +670,10 @@ def prepare_forward_quant(partials, residual, weight, eps: float, write_norm: bo
     import torch
     partials, T, H, dev, dtype = _partials_checked(partials, residual, weight)
     if out is None:
-        out = (torch.empty((T, H), dtype=torch.bfloat16, device=dev),
-               torch.empty((T, H), dtype=torch.bfloat16, device=dev),
-               torch.empty((T, H), dtype=torch.bfloat16, device=dev) if write_norm else None,
-               torch.empty((T, H), dtype=torch.uint8, device=dev),
-               torch.empty((T,), dtype=torch.float32, device=dev))
+        norms = [((T, H), torch.bfloat16)] * (3 if write_norm else 2)
+        out = _new(stream, dev, *norms, ((T, H), torch.uint8), ((T,), torch.float32))
+        if not write_norm:
+            out = (*out[:2], None, *out[2:])
     _check_quant_out(out, T, H, dev, (T, H), torch.uint8, (T,), torch.float32)
     c, s = _ctx_stream(ctx, stream, dev)
     args = _common_args(c, partials, dtype, residual, weight, eps, T, H) + \
@@ -695,11 +700,10 @@ def prepare_forward_nvfp4(partials, residual, weight, eps: float, tensor_scale: 
     if H % 16:
         raise ValueError(f"NVFP4 output needs H % 16 == 0, got H = {H}")
     if out is None:
-        out = (torch.empty((T, H), dtype=torch.bfloat16, device=dev),
-               torch.empty((T, H), dtype=torch.bfloat16, device=dev),
-               torch.empty((T, H), dtype=torch.bfloat16, device=dev) if write_norm else None,
-               torch.empty((T, H // 2), dtype=torch.uint8, device=dev),
-               torch.empty((T, H // 16), dtype=torch.uint8, device=dev))
+        norms = [((T, H), torch.bfloat16)] * (3 if write_norm else 2)
+        out = _new(stream, dev, *norms, ((T, H // 2), torch.uint8), ((T, H // 16), torch.uint8))
+        if not write_norm:
+            out = (*out[:2], None, *out[2:])
     _check_quant_out(out, T, H, dev, (T, H // 2), torch.uint8, (T, H // 16), torch.uint8)
     c, s = _ctx_stream(ctx, stream, dev)
     args = _common_args(c, partials, dtype, residual, weight, eps, T, H) + \
@@ -732,7 +736,7 @@ def prepare_moe_combine(expert_out, index, gates, residual, weight, eps: float, 
     _check_tensor(residual, "residual", (T, H), dev)
     _check_tensor(weight, "weight", (H,), dev)
     if out is None:
-        out = tuple(torch.empty((T, H), dtype=torch.bfloat16, device=dev) for _ in range(3))
+        out = _new(stream, dev, *[((T, H), torch.bfloat16)] * 3)
     for name, t in zip(("reduced", "residual_out", "norm_out"), out):
         _check_tensor(t, name, (T, H), dev)
     c, s = _ctx_stream(ctx, stream, dev)
@@ -773,6 +777,40 @@ def _raw_stream(stream, index):
     return _current_raw_stream(index) if stream is None else stream.cuda_stream
 
 
+def _new(stream, device, *specs, returned=True):
+    """New tensors, a (shape, dtype) each, for a call on `stream` to write.  On a
+    given stream they come from that stream's own memory: the current stream may
+    still be at work on what a free block of its own was before, and the call does
+    not wait for it.  What is returned is used on the current stream, so its block
+    does not go to a later call on `stream` before that use is over."""
+    torch = _torch or _load_torch()
+    if stream is not None:
+        cuda = torch.cuda
+        here = cuda.current_stream(device)
+        if stream.cuda_stream != here.cuda_stream:
+            return _new_elsewhere(cuda, stream, here, device, specs, returned)
+    return tuple([torch.empty(s, dtype=d, device=device) for s, d in specs])
+
+
+def _new_elsewhere(cuda, stream, here, device, specs, returned):
+    if not isinstance(stream, cuda.Stream):
+        stream = cuda.ExternalStream(stream.cuda_stream, device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    # cuda.stream(stream) in its place takes 6 to 8 us more per call
+    index = cuda.current_device()
+    cuda.set_stream(stream)
+    try:
+        new = tuple([_torch.empty(s, dtype=d, device=device) for s, d in specs])
+    finally:
+        cuda.set_stream(here)               # makes its device the current one
+        cuda.set_device(index)
+    if returned:
+        for t in new:
+            t.record_stream(here)
+    return new
+
+
 def _call(fn, args, name):
     st = fn(*args)
     if st != FARN_OK:
@@ -794,13 +832,9 @@ def _moe_route_args(logits, top_k, renormalize, out, ctx, stream):
     if not 1 <= K <= min(E, FARN_MAX_W):
         raise ValueError(f"top_k must be 1..{min(E, FARN_MAX_W)}, got {K}")
     if out is None:
-        dev = logits.device
         pairs = (T, K)
-        out = (torch.empty(pairs, dtype=i32, device=dev),
-               torch.empty(pairs, dtype=f32, device=dev),
-               torch.empty(pairs, dtype=i32, device=dev),
-               torch.empty((T * K,), dtype=i32, device=dev),
-               torch.empty((E + 1,), dtype=i32, device=dev))
+        out = _new(stream, logits.device, (pairs, i32), (pairs, f32), (pairs, i32),
+                   ((T * K,), i32), ((E + 1,), i32))
     else:
         out = tuple(out)
         if len(out) != 5:
@@ -859,7 +893,7 @@ def _grouped_args(x, weights, offsets, rows, out, ctx, stream):
                 rows.is_contiguous()):
             _check_tensor(rows, "rows", (S,), x.device, (i32,))
     if out is None:
-        out = torch.empty((S, N), dtype=bf, device=x.device)
+        out, = _new(stream, x.device, ((S, N), bf))
     else:
         _check_tensor(out, "out", (S, N), x.device)
     c = ctx if ctx is not None else _context_for(index)
@@ -917,9 +951,7 @@ def _quantize_args(x, tensor_scale, out, ctx, stream):
     if H % 16:
         raise ValueError(f"NVFP4 needs H % 16 == 0, got H = {H}")
     if out is None:
-        dev = x.device
-        out = (torch.empty((T, H // 2), dtype=u8, device=dev),
-               torch.empty((T, H // 16), dtype=u8, device=dev))
+        out = _new(stream, x.device, ((T, H // 2), u8), ((T, H // 16), u8))
     else:
         out = tuple(out)
         if len(out) != 2:
@@ -952,7 +984,7 @@ def _dequantize_args(codes, block_scale, tensor_scale, out, ctx, stream):
     torch = _torch or _load_torch()
     T, H, index = _nvfp4_shape(codes, block_scale, "codes")
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=codes.device)
+        out, = _new(stream, codes.device, ((T, H), torch.bfloat16))
     else:
         _check_tensor(out, "out", (T, H), codes.device)
     c = ctx if ctx is not None else _context_for(index)
@@ -999,7 +1031,7 @@ def _nvfp4_matmul_args(a_codes, a_scale, a_tensor_scale, b_codes, b_scale, b_ten
             raise ValueError(f"b_codes must be on {a_codes.device}, got {b_codes.device}")
     T, N = sa[0], sb[0]
     if out is None:
-        out = torch.empty((T, N), dtype=bf, device=a_codes.device)
+        out, = _new(stream, a_codes.device, ((T, N), bf))
     else:
         _check_tensor(out, "out", (T, N), a_codes.device)
     c = ctx if ctx is not None else _context_for(index)
@@ -1050,9 +1082,7 @@ def _fp8_quantize_args(x, block_rows, out, ctx, stream):
         raise ValueError("x must have at least one column")
     shape = (*sx[:-2], -(-T // block_rows), -(-H // 128))
     if out is None:
-        dev = x.device
-        out = (torch.empty(sx, dtype=torch.uint8, device=dev),
-               torch.empty(shape, dtype=torch.float32, device=dev))
+        out = _new(stream, x.device, (sx, torch.uint8), (shape, torch.float32))
     else:
         out = tuple(out)
         if len(out) != 2:
@@ -1103,7 +1133,7 @@ def _fp8_matmul_args(a_codes, a_scale, b_codes, b_scale, out, ctx, stream):
         _check_tensor(a_scale, "a_scale", (T, HB), dev, (f32,))
         _check_tensor(b_scale, "b_scale", (NB, HB), dev, (f32,))
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=a_codes.device)
+        out, = _new(stream, a_codes.device, ((T, N), torch.bfloat16))
     else:
         _check_tensor(out, "out", (T, N), a_codes.device)
     c = _context_of(ctx, index)
@@ -1157,7 +1187,7 @@ def _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, workspac
                 rows.is_contiguous()):
             _check_tensor(rows, "rows", (S,), x.device, (i32,))
     if out is None:
-        out = torch.empty((S, N), dtype=torch.bfloat16, device=x.device)
+        out, = _new(stream, x.device, ((S, N), torch.bfloat16))
     else:
         _check_tensor(out, "out", (S, N), x.device)
     c = _context_of(ctx, index)
@@ -1165,13 +1195,8 @@ def _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, workspac
         _check_tensor(workspace, "workspace", workspace.shape, x.device, (u8,))
     elif rows is not None and S > 64:       # shorter calls never lay rows side by side
         n = farn_fp8_grouped_workspace(c.handle, S, E, N, H)
-        if n and stream is None:
-            workspace = torch.empty(n, dtype=u8, device=x.device)
-        elif n:
-            # in the call's own stream's memory: the current stream may still be
-            # at work on what its own was before
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(n, dtype=u8, device=x.device)
+        if n:
+            workspace, = _new(stream, x.device, (n, u8), returned=False)
     return (c.handle, x.data_ptr(), x_scale.data_ptr(), n_rows,
             None if rows is None else rows.data_ptr(), S, weights.data_ptr(), w_scale.data_ptr(),
             E, offsets.data_ptr(), N, H, out.data_ptr(),
@@ -1356,8 +1381,7 @@ def _qk_args(q, k, q_weight, k_weight, eps, positions, freqs, sections, interlea
     k_stride = _token_stride(k, "k", index, dev, T, HK, D)
     pos, axes, sect, fr, R = _rope_args(positions, freqs, sections, T, D, index, dev)
     if out is None:
-        out = (torch.empty((T, HQ, D), dtype=bf, device=dev),
-               torch.empty((T, HK, D), dtype=bf, device=dev))
+        out = _new(stream, dev, ((T, HQ, D), bf), ((T, HK, D), bf))
         qs, ks = HQ * D, HK * D
     else:
         out = tuple(out)
@@ -1426,7 +1450,7 @@ def _qk_cache_args(q, k, v, q_weight, k_weight, eps, positions, freqs, cache, sl
     slots_at = _slots_arg(slots, T, index, dev)
     store = _cache_of(cache, tensor_scales, index, dev, HK, D)
     if out is None:
-        out = torch.empty((T, HQ, D), dtype=torch.bfloat16, device=dev)
+        out, = _new(stream, dev, ((T, HQ, D), torch.bfloat16))
         qs = HQ * D
     else:
         qs = _token_stride(out, "the output of q", index, dev, T, HQ, D)
@@ -1511,8 +1535,7 @@ def _kv_read_args(cache, table, offsets, n_tokens, tensor_scales, out, ctx, stre
         _check_tensor(offsets, "offsets", (B + 1,), dev, (i32,))
     shape = (n, store.heads, store.head_dim)
     if out is None:
-        out = (torch.empty(shape, dtype=torch.bfloat16, device=dev),
-               torch.empty(shape, dtype=torch.bfloat16, device=dev))
+        out = _new(stream, dev, (shape, torch.bfloat16), (shape, torch.bfloat16))
     else:
         out = tuple(out)
         if len(out) != 2:
