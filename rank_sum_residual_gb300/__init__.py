@@ -1193,10 +1193,11 @@ def _fp8_grouped_args(x, x_scale, weights, w_scale, offsets, rows, out, workspac
     c = _context_of(ctx, index)
     if workspace is not None:
         _check_tensor(workspace, "workspace", workspace.shape, x.device, (u8,))
-    elif rows is not None and S > 64:       # shorter calls never lay rows side by side
-        n = farn_fp8_grouped_workspace(c.handle, S, E, N, H)
-        if n:
-            workspace, = _new(stream, x.device, (n, u8), returned=False)
+    elif rows is not None:
+        n = ctypes.c_int64()            # stays 0 where the call itself will be refused
+        (_lib or _load()).farn_fp8_grouped_workspace(c.handle, S, E, N, H, ctypes.byref(n))
+        if n.value:
+            workspace, = _new(stream, x.device, (n.value, u8), returned=False)
     return (c.handle, x.data_ptr(), x_scale.data_ptr(), n_rows,
             None if rows is None else rows.data_ptr(), S, weights.data_ptr(), w_scale.data_ptr(),
             E, offsets.data_ptr(), N, H, out.data_ptr(),
