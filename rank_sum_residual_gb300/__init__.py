@@ -146,7 +146,7 @@ def _load():
                                                      cvp, cvp, pi, pi, pi]
         lib.farn_plan_fp8_grouped_matmul.restype = i32
         lib.farn_fp8_grouped_matmul.restype = i32
-        pc = vp     # a KvCache by reference, of whichever load of this module
+        pc = vp     # a KvCache by reference: see _cache_ref
         rope = [cvp, cvp, f32, cvp, i32, pi, cvp, i32, i32]
         lib.farn_qk_norm_rope.argtypes = [vp, i64, i32, cvp, i32, i64, cvp, i32, i64, *rope, vp,
                                           i64, vp, i64, vp]
@@ -379,6 +379,9 @@ def farn_qk_norm_rope(ctx, T, D, q, q_heads, q_stride, k, k_heads, k_stride, q_w
 
 
 def _cache_ref(cache):
+    # the library reads a whole struct at the address
+    if cache is not None and not isinstance(cache, KvCache):
+        raise TypeError(f"cache must be a KvCache or None, got {type(cache).__name__}")
     return None if cache is None else ctypes.byref(cache)
 
 
