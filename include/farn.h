@@ -492,8 +492,10 @@ int farn_fp8_matmul(const farn_ctx *ctx, const void *a_codes,
  *              the call may overwrite, for this call alone until it has run: a
  *              long call with `rows` lays the slots' rows side by side there
  *              first and is then faster.  farn_fp8_grouped_workspace says how
- *              much such a call takes; less, or none, leads to the same results
- *              by the other kernel.  It may not overlap any tensor. */
+ *              much such a call takes; with less, or none, the other kernel runs,
+ *              whose sums are in another order: its results are the same up to the
+ *              rounding of fp32 sums, not always bit for bit.  It may not overlap any
+ *              tensor. */
 int farn_fp8_grouped_matmul(const farn_ctx *ctx, const void *x,
                             const float *x_scale, int64_t n_rows,
                             const int32_t *rows, int64_t n_slots,

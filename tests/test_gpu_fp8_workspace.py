@@ -5,7 +5,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import rank_sum_residual_gb300 as farn  # noqa: E402
-from test_gpu_fp8 import ctxs, dev, group_inputs, group_reference, to_bf16, whole  # noqa: E402,F401
+from test_gpu_fp8 import (ctxs, dev, group_inputs, group_reference, spread,  # noqa: E402,F401
+                          to_bf16, tolerance, whole)
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +45,20 @@ def test_the_plans_own_border(dev, ctxs):  # noqa: F811
     assert need == workspace_of(call) == S * H + S * 8 * 4
     want, _ = group_reference(x, w, offsets, rows, S)
     assert torch.equal(call(), to_bf16(want))
+
+
+def test_rounding_with_every_workspace(dev, ctxs):  # noqa: F811
+    """Operands whose sums round: both kernels stay within the roundings of the
+    definition, and each repeats bit for bit."""
+    counts, N, H = [300, 500, 90], 256, 2064
+    c = ctxs["pair"]
+    x, w, offsets, rows, S = group_inputs(dev, counts, N, H, True, spread, 65)
+    need = farn.farn_fp8_grouped_workspace(c.handle, S, len(counts), N, H)
+    buf = torch.zeros(need + 32, dtype=torch.uint8, device=dev)
+    want, mag = group_reference(x, w, offsets, rows, S)
+    most = tolerance(want, mag, H)
+    for ws in (None, buf[:need], buf[:need - 1], buf[1:1 + need], buf[:0]):
+        out = [farn.fp8_grouped_matmul(*x, *w, offsets, rows, workspace=ws, ctx=c)
+               for _ in range(2)]
+        assert ((out[0].double() - want).abs() <= most).all()
+        assert torch.equal(*out)
