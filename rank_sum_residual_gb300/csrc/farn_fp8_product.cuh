@@ -243,7 +243,7 @@ __device__ __forceinline__ void store_rows(const ProductParams& p, int store_byt
 // Eight lanes copy a row's 128 bytes, in the swizzled layout that TMA would
 // write: 16-byte column j of row r at j ^ (r & 7).  Lane l knows the rows l, l +
 // 32, ...  first: the CTA's first slot of a tile; rows: how many it has.
-template <int ROWS, int CG>
+template <int ROWS>
 struct RowCopier {
   static constexpr int kHeld = ROWS / 32;
   int32_t held[kHeld];                     // negative: zeros
@@ -962,7 +962,7 @@ farn_fp8_one_kernel(const __grid_constant__ Fp8Params t,
   } else if (GATHER && (warp == 10 || warp >= 12) && warp < 12 + kF8Gather - 1) {
     // -------------------------------------------------------- gathered rows
     const int mine = warp == 10 ? 0 : warp - 11;
-    RowCopier<64, 1> rows;
+    RowCopier<64> rows;
     RingPos at;
     at.skip(mine, NS);
     int ahead = mine;

@@ -39,7 +39,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 4;             // rows per lane group whose loads are in flight
 // CTAs per SM, of a warp each: warps have nothing in common, and one that is done
 // makes room at once (four to a CTA: 8192 tokens of 40 and 8 heads of 128 47.5 us, now
-// 46.9; 4099 of 16 and 16 of 80 15.8, now 15.3; 2048 of 8 written 6.2, now 5.5).
+// 46.9; 4099 of 16 and 16 of 80 15.8, now 15.3; 2048 of 8 written 6.2, now 5.5).  28
+// leave a thread 72 registers, and all instances but one spill (16 to 172 bytes of
+// loads); 25 to 32 CTAs with 2 to 6 rows ahead were no faster.
 constexpr int kCtas = 28;
 constexpr int kMaxDim = 1024;
 constexpr int kMaxAxes = 4;
@@ -192,7 +194,9 @@ struct Turn {
 // FMT: the cache's format, or 0: keys go to out[1].  HALF: pairs lie in halves.
 // The code is about instructions: with roles, layouts and addresses worked out
 // per row 8192 tokens of 40 and 8 heads of 128 took 77 us, 260 instructions to a
-// pass, two thirds of the issue slots; it takes 47.  (One loop for all roles: 50;
+// pass, two thirds of the issue slots; it takes 47 with 170.  What bounds it now is
+// latency: of the 9.3 cycles that a warp takes per instruction 3.1 wait for memory,
+// and 25 warps per SM leave a third of the issue slots empty.  (One loop for all roles: 50;
 // the rows brought ahead of the warps through shared memory: 62; a token's angles
 // shared by four warps: 55; four rows' sums joined together: 53, for the registers.)
 template <int ROLE, int L, int FMT, bool HALF>
